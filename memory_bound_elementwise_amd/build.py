@@ -4,7 +4,8 @@
 (``include/swiglu_probs.h``); ``libmoe_elementwise.so`` the MoE elementwise
 operations next to it (``include/moe_elementwise.h``); ``libhbm_probe.so`` plain
 streaming kernels that measure the practical HBM ceiling and calibrate the hardware
-byte counters (``include/hbm_probe.h``). All three are written to
+byte counters (``include/hbm_probe.h``); ``libmoe_block.so`` the operators of the block
+around the experts (``include/block/moe_block.h``). All are written to
 ``memory_bound_elementwise_amd/_lib``.
 """
 from __future__ import annotations
@@ -34,6 +35,7 @@ LIBS = {
     "swiglu_probs": ["swiglu_probs.hip"],
     "moe_elementwise": ["moe_elementwise.hip"],
     "hbm_probe": ["hbm_probe.hip"],
+    "moe_block": ["block_common.hip", "layer_norm.hip", "linear_act.hip", "moe_layer.hip"],
 }
 
 

@@ -1,0 +1,347 @@
+"""Python binding of ``libmoe_block.so`` (C ABI in ``include/block/moe_block.h``): layer norm,
+a matrix product with bias, activation and residual in its epilogue, the router, and a whole
+expert layer for a few tokens.
+
+Argument marshalling only: tensors are checked for device, dtype, shape and contiguity and
+their device pointers and a HIP stream are handed to the C functions. No CPU or PyTorch
+fallback.
+
+Every call runs on the tensors' own device and on ``stream`` (a ``torch.cuda.Stream`` or a
+raw handle; default: the current stream of that device). Where the C function needs a
+workspace it is taken from ``workspace`` (uint8, at least ``*_workspace`` bytes) or, without
+one, allocated on that stream, so that its memory is not reused before the work has run.
+"""
+from __future__ import annotations
+
+import ctypes
+import math
+import os
+import threading
+from typing import Optional
+
+import torch
+from torch.autograd.function import once_differentiable
+
+from . import build as _build
+
+BLOCK_BF16, BLOCK_FP16, BLOCK_FP32 = 0, 1, 2
+_TORCH = {torch.bfloat16: BLOCK_BF16, torch.float16: BLOCK_FP16, torch.float32: BLOCK_FP32}
+ACTIVATIONS = {None: 0, "none": 0, "silu": 1, "gelu": 2, "squared_relu": 3}
+EXPERT_ACTIVATIONS = {"squared_relu": 3, "swiglu": 4}
+
+_lock = threading.Lock()
+_lib = None
+_vp, _i64, _int, _f32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_float
+_SIGS = {
+    "block_layer_norm_fwd": [_vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _f32, _int, _int, _vp],
+    "block_layer_norm_bwd_workspace": [_i64, _i64],
+    "block_layer_norm_bwd": [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _int, _int, _vp, _i64, _vp],
+    "block_linear_act_workspace": [_i64, _i64, _i64],
+    "block_linear_act": [_vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _int, _int, _vp, _i64, _vp],
+    "block_moe_route_workspace": [_i64, _i64, _int],
+    "block_moe_route": [_vp, _vp, _int, _vp, _vp, _i64, _i64, _int, _int, _int, _vp, _vp, _i64, _vp],
+    "block_moe_experts_workspace": [_i64, _int, _i64],
+    "block_moe_experts": [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _int, _i64, _i64, _i64, _int, _int, _int, _f32, _vp,
+                          _vp, _i64, _vp],
+    "block_moe_layer_workspace": [_i64, _i64, _i64, _int, _int],
+    "block_moe_layer": [_vp, _vp, _int, _vp, _vp, _vp, _vp, _int, _vp, _vp, _i64, _i64, _i64, _int, _int, _int,
+                        _int, _f32, _vp, _vp, _i64, _vp],
+    "moe_block_status_string": [_int],
+    "moe_block_last_hip_error": [],
+    "moe_block_abi_version": [],
+}
+
+
+class MoeBlockError(RuntimeError):
+    def __init__(self, fn: str, status: int, hip_error: int = 0):
+        self.status, self.hip_error = status, hip_error
+        msg = load_library().moe_block_status_string(status).decode()
+        super().__init__(f"{fn} failed: {msg} (status {status}" +
+                         (f", hipError {hip_error})" if status == 3 else ")"))
+
+
+def load_library(path: Optional[str] = None) -> ctypes.CDLL:
+    """Load (building it first if nothing is built) the HIP library; cached."""
+    global _lib
+    if _lib is not None and path is None:
+        return _lib
+    with _lock:
+        if _lib is not None and path is None:
+            return _lib
+        p = path or _build.lib_path("moe_block")
+        if not os.path.exists(p):
+            _build.build_lib("moe_block")
+        lib = ctypes.CDLL(p)
+        for name, args in _SIGS.items():
+            f = getattr(lib, name)
+            f.argtypes = args
+            f.restype = (ctypes.c_char_p if name == "moe_block_status_string" else
+                         _i64 if name.endswith("_workspace") else _int)
+        if lib.moe_block_abi_version() != 1:
+            raise RuntimeError("libmoe_block.so ABI version mismatch")
+        if path is None:
+            _lib = lib
+        return lib
+
+
+def _tensor(t, name, dtypes, shape):
+    """Checks one tensor; returns its address (None for an absent one)."""
+    if t is None:
+        return None
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _device(first, *rest):
+    dev = first.device
+    if dev.type != "cuda":
+        raise ValueError("tensors must live on the GPU")
+    for t in rest:
+        if t is not None and t.device != dev:
+            raise ValueError("tensors must live on one device")
+    return dev
+
+
+def _call(fn, dev, stream, args, workspace, need):
+    """Runs one C function on `dev` and `stream`; `need` None: it takes no workspace."""
+    if dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return _call(fn, dev, stream, args, workspace, need)
+    if stream is None:
+        handle = torch.cuda.current_stream().cuda_stream
+    elif isinstance(stream, torch.cuda.Stream):
+        if stream.device != dev:
+            raise ValueError("the stream belongs to another device")
+        handle = stream.cuda_stream
+    else:
+        handle = int(stream)
+    if need is not None:
+        if workspace is not None:
+            if workspace.dtype != torch.uint8 or not workspace.is_contiguous() or workspace.device != dev:
+                raise ValueError("workspace must be a contiguous uint8 tensor on the tensors' device")
+            if workspace.numel() < need:
+                raise ValueError(f"workspace must hold at least {need} bytes, got {workspace.numel()}")
+        elif need > 0:
+            if stream is None:
+                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+            else:
+                own = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(handle, device=dev)
+                with torch.cuda.stream(own):
+                    workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        args += (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
+    lib = load_library()
+    st = getattr(lib, fn)(*args, handle)
+    if st:
+        raise MoeBlockError(fn, st, lib.moe_block_last_hip_error())
+
+
+def _rows(x, name):
+    if x.dim() != 2:
+        raise ValueError(f"{name} must be 2-D")
+    return x.shape
+
+
+_ANY = tuple(_TORCH)
+_BF16 = (torch.bfloat16,)
+_F32 = (torch.float32,)
+_I32 = (torch.int32,)
+
+
+# ---------------------------------------------------------------------------
+# Layer norm
+# ---------------------------------------------------------------------------
+def layer_norm_fwd(x, weight, bias, y, mean=None, rstd=None, *, eps=1e-5, stream=None):
+    """y = (x - mean) * rstd * weight + bias per row of x [rows, cols] (bf16, fp16 or fp32), in
+    fp32 with one rounding. ``weight`` and ``bias``: [cols] of x's dtype or fp32 (one dtype for
+    both), or None. ``mean`` and ``rstd`` (fp32 [rows], both or neither) take the statistics
+    that the backward needs."""
+    rows, cols = _rows(x, "x")
+    first = weight if weight is not None else bias
+    wd = (x.dtype, torch.float32) if first is None else (first.dtype,)
+    if first is not None and first.dtype not in (x.dtype, torch.float32):
+        raise TypeError(f"weight and bias must be {x.dtype} or fp32, got {first.dtype}")
+    args = (_tensor(x, "x", _ANY, x.shape), _tensor(weight, "weight", wd, (cols,)), _tensor(bias, "bias", wd, (cols,)),
+            _tensor(y, "y", (x.dtype,), x.shape), _tensor(mean, "mean", _F32, (rows,)),
+            _tensor(rstd, "rstd", _F32, (rows,)), rows, cols, float(eps), _TORCH[x.dtype],
+            _TORCH[wd[0]])
+    if (mean is None) != (rstd is None):
+        raise ValueError("mean and rstd go together")
+    _call("block_layer_norm_fwd", _device(x, weight, bias, y, mean, rstd), stream, args, None, None)
+    return y
+
+
+def layer_norm_bwd_workspace(rows: int, cols: int) -> int:
+    return load_library().block_layer_norm_bwd_workspace(rows, cols)
+
+
+def layer_norm_bwd(grad_y, x, weight, mean, rstd, grad_x, grad_weight=None, grad_bias=None, *, workspace=None,
+                   stream=None):
+    """Gradients of ``layer_norm_fwd``: grad_x in x's dtype, grad_weight and grad_bias in the
+    weight's (the same bits on every call); any of the three may be None. With ``weight`` None
+    (a norm without scale) grad_weight and grad_bias are x's dtype or fp32."""
+    rows, cols = _rows(x, "x")
+    first = next((t for t in (weight, grad_weight, grad_bias) if t is not None), None)
+    wd = (x.dtype,) if first is None else (first.dtype,)
+    if wd[0] not in (x.dtype, torch.float32):
+        raise TypeError(f"weight must be {x.dtype} or fp32, got {wd[0]}")
+    args = (_tensor(grad_y, "grad_y", (x.dtype,), x.shape), _tensor(x, "x", _ANY, x.shape),
+            _tensor(weight, "weight", wd, (cols,)), _tensor(mean, "mean", _F32, (rows,)),
+            _tensor(rstd, "rstd", _F32, (rows,)), _tensor(grad_x, "grad_x", (x.dtype,), x.shape),
+            _tensor(grad_weight, "grad_weight", wd, (cols,)), _tensor(grad_bias, "grad_bias", wd, (cols,)),
+            rows, cols, _TORCH[x.dtype], _TORCH[wd[0]])
+    dev = _device(x, grad_y, weight, mean, rstd, grad_x, grad_weight, grad_bias)
+    need = layer_norm_bwd_workspace(rows, cols) if grad_weight is not None or grad_bias is not None else 0
+    _call("block_layer_norm_bwd", dev, stream, args, workspace, need)
+    return grad_x, grad_weight, grad_bias
+
+
+class LayerNorm(torch.autograd.Function):
+    """Layer norm over the last axis, saving x and its fp32 statistics."""
+
+    @staticmethod
+    def forward(ctx, x, weight=None, bias=None, eps=1e-5):
+        flat = x.contiguous().view(-1, x.shape[-1])
+        mean = torch.empty(flat.shape[0], dtype=torch.float32, device=x.device)
+        rstd = torch.empty_like(mean)
+        y = layer_norm_fwd(flat, weight, bias, torch.empty_like(flat), mean, rstd, eps=eps)
+        ctx.save_for_backward(flat, weight, mean, rstd)
+        ctx.bias_dtype = None if bias is None else bias.dtype
+        return y.view(x.shape)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, grad_y):
+        flat, weight, mean, rstd = ctx.saved_tensors
+        grad_x = torch.empty_like(flat) if ctx.needs_input_grad[0] else None
+        grad_weight = torch.empty_like(weight) if ctx.needs_input_grad[1] else None
+        grad_bias = (torch.empty(flat.shape[1], dtype=ctx.bias_dtype, device=flat.device)
+                     if ctx.needs_input_grad[2] else None)
+        layer_norm_bwd(grad_y.contiguous().view(flat.shape), flat, weight, mean, rstd, grad_x, grad_weight, grad_bias)
+        return None if grad_x is None else grad_x.view(grad_y.shape), grad_weight, grad_bias, None
+
+
+# ---------------------------------------------------------------------------
+# Matrix product with an epilogue
+# ---------------------------------------------------------------------------
+def linear_act_workspace(m: int, n: int, k: int) -> int:
+    return load_library().block_linear_act_workspace(m, n, k)
+
+
+def linear_act(x, weight, y, *, bias=None, activation=None, residual=None, workspace=None, stream=None):
+    """y = act(x @ weight.T + bias) + residual; x [m, k], weight [n, k], bias [n], residual and y
+    [m, n], all bf16 or all fp16, summed and finished in fp32 with one rounding. ``activation``:
+    None, "silu", "gelu" (tanh form) or "squared_relu". n and k are multiples of 8. Forward
+    only: inputs that require a gradient are refused while gradients are recorded."""
+    m, k = _rows(x, "x")
+    n = _rows(weight, "weight")[0]
+    if activation not in ACTIVATIONS:
+        raise ValueError(f"unknown activation {activation!r}")
+    _forward_only("linear_act", x, weight, bias, residual)
+    same = (x.dtype,)
+    args = (_tensor(x, "x", (torch.bfloat16, torch.float16), x.shape), _tensor(weight, "weight", same, (n, k)),
+            _tensor(bias, "bias", same, (n,)), _tensor(residual, "residual", same, (m, n)),
+            _tensor(y, "y", same, (m, n)), m, n, k, ACTIVATIONS[activation], _TORCH[x.dtype])
+    _call("block_linear_act", _device(x, weight, bias, residual, y), stream, args, workspace,
+          linear_act_workspace(m, n, k))
+    return y
+
+
+def _forward_only(name, *tensors):
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
+        raise RuntimeError(f"{name} has no backward pass: call it under torch.no_grad()")
+
+
+# ---------------------------------------------------------------------------
+# Router and experts
+# ---------------------------------------------------------------------------
+def moe_route_workspace(tokens: int, hidden: int, experts: int) -> int:
+    return load_library().block_moe_route_workspace(tokens, hidden, experts)
+
+
+def moe_experts_workspace(tokens: int, top_k: int, inter: int) -> int:
+    return load_library().block_moe_experts_workspace(tokens, top_k, inter)
+
+
+def moe_layer_workspace(tokens: int, hidden: int, inter: int, experts: int, top_k: int) -> int:
+    return load_library().block_moe_layer_workspace(tokens, hidden, inter, experts, top_k)
+
+
+def _scalar(valid_tokens):
+    return None if valid_tokens is None else _tensor(valid_tokens.reshape(-1), "valid_tokens", _I32, (1,))
+
+
+def moe_route(x, router_weight, ids, probs, *, renormalize=False, valid_tokens=None, workspace=None, stream=None):
+    """The top experts of each token of x (bf16 [tokens, hidden]) and their softmax weights:
+    logits = x @ router_weight.T (bf16 or fp32 [experts, hidden]) in fp64, the ids.shape[1]
+    largest in descending order with ties to the lower expert into ``ids`` (int32 [tokens,
+    top_k]) and their weights, of all experts' or (``renormalize``) of the chosen ones', into
+    ``probs`` (fp32). Rows at or past ``valid_tokens`` (device int32) are left as they were."""
+    tokens, hidden = _rows(x, "x")
+    experts = _rows(router_weight, "router_weight")[0]
+    top_k = _rows(ids, "ids")[1]
+    _forward_only("moe_route", x, router_weight)
+    args = (_tensor(x, "x", _BF16, x.shape),
+            _tensor(router_weight, "router_weight", (torch.bfloat16, torch.float32), (experts, hidden)),
+            _TORCH[router_weight.dtype], _tensor(ids, "ids", _I32, (tokens, top_k)),
+            _tensor(probs, "probs", _F32, (tokens, top_k)), tokens, hidden, experts, top_k, int(bool(renormalize)),
+            _scalar(valid_tokens))
+    _call("block_moe_route", _device(x, router_weight, ids, probs, valid_tokens), stream, args, workspace,
+          moe_route_workspace(tokens, hidden, experts))
+    return ids, probs
+
+
+def _expert_shapes(x, w_up, w_down, activation, limit):
+    tokens, hidden = _rows(x, "x")
+    if activation not in EXPERT_ACTIVATIONS:
+        raise ValueError(f"unknown expert activation {activation!r}")
+    if w_down.dim() != 3:
+        raise ValueError("w_down must be [experts, hidden, inter]")
+    experts, _, inter = w_down.shape
+    ups = 2 * inter if activation == "swiglu" else inter
+    if activation == "swiglu" and not limit > 0:
+        raise ValueError("limit must be positive (inf for none)")
+    return (tokens, hidden, inter, experts, _tensor(x, "x", _BF16, x.shape),
+            _tensor(w_up, "w_up", _BF16, (experts, ups, hidden)),
+            _tensor(w_down, "w_down", _BF16, (experts, hidden, inter)))
+
+
+def moe_experts(x, w_up, w_down, ids, probs, y, *, activation="swiglu", limit=math.inf, residual=None,
+                valid_tokens=None, workspace=None, stream=None):
+    """y[t] = residual[t] + sum over j of (act(x[t] @ w_up[e].T) * probs[t, j]) @ w_down[e].T, e =
+    ids[t, j], for a few tokens (tokens * top_k <= 1024): each chosen expert's weights are read
+    once. ``activation``: "swiglu" (w_up [experts, 2 inter, hidden], gate rows first, clamped
+    at ``limit``) or "squared_relu" (w_up [experts, inter, hidden]). An id outside the experts
+    contributes nothing. x, weights and residual bf16; y bf16 or fp32; rows of y at or past
+    ``valid_tokens`` are left as they were."""
+    tokens, hidden, inter, experts, px, pu, pd = _expert_shapes(x, w_up, w_down, activation, limit)
+    top_k = _rows(ids, "ids")[1]
+    _forward_only("moe_experts", x, w_up, w_down, probs, residual)
+    args = (px, pu, pd, _tensor(ids, "ids", _I32, (tokens, top_k)), _tensor(probs, "probs", _F32, (tokens, top_k)),
+            _tensor(residual, "residual", _BF16, x.shape), _tensor(y, "y", (torch.bfloat16, torch.float32), x.shape),
+            _TORCH[y.dtype], tokens, hidden, inter, experts, top_k, EXPERT_ACTIVATIONS[activation], float(limit),
+            _scalar(valid_tokens))
+    _call("block_moe_experts", _device(x, w_up, w_down, ids, probs, residual, y, valid_tokens), stream, args,
+          workspace, moe_experts_workspace(tokens, top_k, inter))
+    return y
+
+
+def moe_layer(x, router_weight, w_up, w_down, y, ids, probs, *, activation="swiglu", limit=math.inf,
+              renormalize=False, residual=None, valid_tokens=None, workspace=None, stream=None):
+    """``moe_route`` into ids and probs, then ``moe_experts`` with them into y, in one call."""
+    tokens, hidden, inter, experts, px, pu, pd = _expert_shapes(x, w_up, w_down, activation, limit)
+    top_k = _rows(ids, "ids")[1]
+    _forward_only("moe_layer", x, router_weight, w_up, w_down, residual)
+    args = (px, _tensor(router_weight, "router_weight", (torch.bfloat16, torch.float32), (experts, hidden)),
+            _TORCH[router_weight.dtype], pu, pd, _tensor(residual, "residual", _BF16, x.shape),
+            _tensor(y, "y", (torch.bfloat16, torch.float32), x.shape), _TORCH[y.dtype],
+            _tensor(ids, "ids", _I32, (tokens, top_k)), _tensor(probs, "probs", _F32, (tokens, top_k)),
+            tokens, hidden, inter, experts, top_k, int(bool(renormalize)), EXPERT_ACTIVATIONS[activation],
+            float(limit), _scalar(valid_tokens))
+    _call("block_moe_layer", _device(x, router_weight, w_up, w_down, residual, y, ids, probs, valid_tokens), stream,
+          args, workspace, moe_layer_workspace(tokens, hidden, inter, experts, top_k))
+    return y
