@@ -113,7 +113,7 @@ block_status_t block_linear_act(const void *x, const void *weight, const void *b
  *   ids: int32 [tokens, top_k]; probs: fp32 [tokens, top_k].
  *   valid_tokens: device int32 scalar or NULL (= tokens), clamped to 0 .. tokens; rows of ids
  *   and probs at or past it are neither read nor written.
- *   0 <= tokens <= 2^20; hidden a multiple of 8, 8 .. 2^20; 1 <= top_k <= min(experts, 64);
+ *   0 <= tokens <= 2^19; hidden a multiple of 8, 8 .. 2^20; 1 <= top_k <= min(experts, 64);
  *   1 <= experts <= 1024; tokens * experts <= 2^25.
  */
 int64_t block_moe_route_workspace(int64_t tokens, int64_t hidden, int experts);
@@ -136,7 +136,7 @@ block_status_t block_moe_route(const uint16_t *x, const void *router_weight, blo
  *   valid_tokens: as for block_moe_route; rows of y at or past it are left as they were.
  *   hidden and inter multiples of 8, 8 .. 2^16; tokens * top_k <= 1024; 1 <= experts <= 1024.
  */
-int64_t block_moe_experts_workspace(int64_t tokens, int top_k, int64_t inter);
+int64_t block_moe_experts_workspace(int64_t tokens, int64_t hidden, int64_t inter, int experts, int top_k);
 block_status_t block_moe_experts(const uint16_t *x, const uint16_t *w_up, const uint16_t *w_down,
                                  const int32_t *ids, const float *probs, const uint16_t *residual,
                                  void *y, block_dtype_t y_dtype, int64_t tokens, int64_t hidden,

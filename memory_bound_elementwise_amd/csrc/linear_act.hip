@@ -40,19 +40,28 @@ __device__ __forceinline__ void finish(const Args &a, int row, int col, float z)
 template <int DT, int G, int WAVES>
 __global__ __launch_bounds__(WAVES * 64) void linear_few_kernel(Args a)
 {
-    __shared__ f32x4 joined[WAVES * G * 64];
-    const int lane = lane_id(), wave = wave_in_block(), k8 = lane / 16 * 8;
+    __shared__ u32x4 shared[WAVES * kStage<1, G>];
+    const int lane = lane_id(), wave = wave_in_block();
     const int c0 = blockIdx.x * 16;
-    const int wrow = c0 + lane % 16 < a.n ? c0 + lane % 16 : a.n - 1;
-    const uint16_t *w[1] = {a.w + (int64_t)wrow * a.k + k8}, *b[1][G];
+    constexpr int DEPTH = G == 4 ? 2 : 3;
+    const int there = a.n - c0 < 16 ? a.n - c0 : 16;
+    const uint32_t row_bytes = (uint32_t)a.k * 2u;
+    const rsrc_t w[1] = {make_rsrc(a.w + (int64_t)c0 * a.k, (uint32_t)there * row_bytes)};
+    const rsrc_t x = make_rsrc(a.x, (uint32_t)a.m * row_bytes);
+    uint32_t col[G][2];
     f32x4 acc[1][G];
+    clear(acc);
 #pragma unroll
-    for (int g = 0; g < G; ++g) {
-        const int r = g * 16 + lane % 16;
-        b[0][g] = a.x + (int64_t)(r < a.m ? r : a.m - 1) * a.k + k8;
-        acc[0][g] = f32x4{0, 0, 0, 0};
-    }
-    stream_products<DT, 1, G, 1>(acc, w, b, 1, a.k, wave * kStreamStep, WAVES * kStreamStep);
+    for (int g = 0; g < G; ++g)
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+            const int r = g * 16 + p * 8 + lane / 8;
+            col[g][p] = r < a.m ? (uint32_t)r * row_bytes + lane % 8 * 16 : kNowhere;
+        }
+    stream_products<DT, 1, G, DEPTH, 1>(acc, w, row_bytes, x, col, a.k, wave * kLineK, WAVES * kLineK,
+                                        shared + wave * kStage<1, G>);
+    __syncthreads();  // the sums take the place of the stages
+    f32x4 *joined = reinterpret_cast<f32x4 *>(shared);
 #pragma unroll
     for (int g = 0; g < G; ++g)
         joined[(wave * G + g) * 64 + lane] = acc[0][g];
@@ -164,10 +173,10 @@ block_status_t run(const Args &a, hipStream_t st)
     if (a.m <= 64) {
         const dim3 grid((unsigned)ceil_div(a.n, 16));
         if (a.m <= 16)
-            return launch(linear_few_kernel<DT, 1, 4>, grid, dim3(256), 0, st, a);
+            return launch(linear_few_kernel<DT, 1, 16>, grid, dim3(1024), 0, st, a);
         if (a.m <= 32)
-            return launch(linear_few_kernel<DT, 2, 4>, grid, dim3(256), 0, st, a);
-        return launch(linear_few_kernel<DT, 4, 4>, grid, dim3(256), 0, st, a);
+            return launch(linear_few_kernel<DT, 2, 8>, grid, dim3(512), 0, st, a);
+        return launch(linear_few_kernel<DT, 4, 8>, grid, dim3(512), 0, st, a);
     }
     const dim3 grid((unsigned)(ceil_div(a.n, kTile) * ceil_div(a.m, kTile)));
     return launch(linear_tile_kernel<DT>, grid, dim3(256), 0, st, a);

@@ -24,7 +24,6 @@ using namespace block;
 
 constexpr int kMaxPairs = 1024;    // tokens * top_k
 constexpr int kMaxExperts = 1024;
-constexpr int kPass = 64;          // pairs of one expert that share a read of its weights
 
 __device__ __forceinline__ int live_tokens(const int *valid, int tokens)
 {
@@ -37,41 +36,58 @@ __device__ __forceinline__ int live_tokens(const int *valid, int tokens)
 // ---------------------------------------------------------------------------
 // Router
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ double wave_sum64(double v)
-{
-#pragma unroll
-    for (int m = 1; m < 64; m *= 2)
-        v += __shfl_xor(v, m);
-    return v;
-}
+typedef double f64x4 __attribute__((ext_vector_type(4)));
 
-// logits[t][e]: one wave a (token, expert). Products of two bf16 (or a bf16 and an fp32) are
-// exact in fp64 and the sums are fp64.
+constexpr int kRouteTile = 16;   // tokens and experts of a workgroup's tile
+constexpr int kRouteStep = 32;   // k of one load: four octets, one a group of 16 lanes
+constexpr int kRouteWaves = 16;  // waves that share a part of k
+
+// partial[part][t][e]: a workgroup's tile of 16 tokens x 16 experts over one part of k, on the
+// fp64 matrix cores. Products of two bf16 (or a bf16 and an fp32) are exact in fp64 and the
+// sums are fp64. A lane loads octet lane / 16 of its row; the eight instructions that follow
+// take one element of each lane's octet, so that k runs in the same order on both sides.
 template <int RDT>
-__global__ __launch_bounds__(256) void route_logits_kernel(const char *x, const char *router, double *logits,
-                                                           int tokens, int hidden, int experts, const int *valid)
+__global__ __launch_bounds__(kRouteWaves * 64) void route_logits_kernel(const char *x, const char *router,
+                                                                        double *partial, int tokens, int hidden,
+                                                                        int experts, int part_k, const int *valid)
 {
-    const int64_t at = (int64_t)blockIdx.x * 4 + wave_in_block();
-    const int t = (int)(at / experts), e = (int)(at % experts);
-    if (t >= live_tokens(valid, tokens))
+    __shared__ double joined[kRouteWaves][4][64];
+    const int lane = lane_id(), wave = wave_in_block(), i = lane % 16, k8 = lane / 16 * 8;
+    const int t0 = blockIdx.y * kRouteTile, e0 = blockIdx.x * kRouteTile;
+    if (t0 >= live_tokens(valid, tokens))
         return;
+    // past the last row: the last one again, not stored
+    const int t = t0 + i < tokens ? t0 + i : tokens - 1, e = e0 + i < experts ? e0 + i : experts - 1;
     const char *xr = x + (int64_t)t * hidden * 2, *wr = router + (int64_t)e * hidden * kSize<RDT>;
-    double sum = 0.0;
-    for (int j = lane_id() * 8; j < hidden; j += 512) {
+    const int first = blockIdx.z * part_k, last = first + part_k < hidden ? first + part_k : hidden;
+    f64x4 acc = {0.0, 0.0, 0.0, 0.0};
+#pragma unroll 4
+    for (int k = first + wave * kRouteStep; k < last; k += kRouteWaves * kRouteStep) {
+        const int n = k + k8 < last ? last : 0;  // an octet past the part: zeros
         float a[8], b[8];
-        widen8<DT_BF16>(load8<DT_BF16>(xr, j, hidden), a);
-        widen8<RDT>(load8<RDT>(wr, j, hidden), b);
+        widen8<DT_BF16>(load8<DT_BF16>(xr, k + k8, n), a);
+        widen8<RDT>(load8<RDT>(wr, k + k8, n), b);
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            sum = __builtin_fma((double)a[i], (double)b[i], sum);
+        for (int j = 0; j < 8; ++j)
+            acc = __builtin_amdgcn_mfma_f64_16x16x4f64((double)b[j], (double)a[j], acc, 0, 0, 0);
     }
-    sum = wave_sum64(sum);
-    if (lane_id() == 0)
-        logits[at] = sum;
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+        joined[wave][r][lane] = acc[r];
+    __syncthreads();
+    // element r of lane l: expert 4 r + l / 16 of the tile, token l % 16; wave r finishes it
+    if (wave >= 4)
+        return;
+    const int c = 4 * wave + lane / 16;
+    double sum = 0.0;
+#pragma unroll
+    for (int w = 0; w < kRouteWaves; ++w)
+        sum += joined[w][wave][lane];
+    if (t0 + i < tokens && e0 + c < experts)
+        partial[((int64_t)blockIdx.z * tokens + t0 + i) * experts + e0 + c] = sum;
 }
 
-// A double as an unsigned integer in the same order; +0 and -0 alike, NaN above all, and
-// nothing at 0 (which marks an expert already chosen).
+// A double as an unsigned integer in the same order; +0 and -0 alike, NaN above all.
 __device__ __forceinline__ uint64_t order_key(double v)
 {
     if (v != v)
@@ -80,71 +96,63 @@ __device__ __forceinline__ uint64_t order_key(double v)
     return b >> 63 ? ~b : b | (uint64_t)1 << 63;
 }
 
-// One wave a token; lane l holds experts l, l + 64, ... (PER of them). top_k times, the
-// largest remaining key, the lowest index first.
-template <int PER>
-__global__ __launch_bounds__(64) void route_choose_kernel(const double *logits, int *ids, float *probs, int tokens,
-                                                          int experts, int top_k, int renormalize, const int *valid)
+// One workgroup a token, a thread an expert: its logit is the sum of its parts in order, its
+// rank the number of experts before it (a larger logit, or an equal one and a lower index).
+// Counting against all others costs less than top_k reductions over the wave one after the
+// other (64 experts, top 8: 4.7 us so).
+__global__ __launch_bounds__(kMaxExperts) void route_choose_kernel(const double *partial, int *ids, float *probs,
+                                                                   int tokens, int experts, int parts, int top_k,
+                                                                   int renormalize, const int *valid)
 {
-    const int t = blockIdx.x, lane = lane_id();
+    __shared__ uint64_t keys[kMaxExperts];
+    __shared__ float sums[kMaxExperts / 64];
+    __shared__ int holder[kMaxExperts];
+    __shared__ int tied;
+    __shared__ double top;
+    const int t = blockIdx.x, e = threadIdx.x, lane = lane_id(), wave = wave_in_block();
     if (t >= live_tokens(valid, tokens))
         return;
-    const double *row = logits + (int64_t)t * experts;
-    double v[PER];
-    uint64_t key[PER];
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        const int e = lane + 64 * i;
-        v[i] = e < experts ? row[e] : 0.0;
-        key[i] = e < experts ? order_key(v[i]) : 0;
-    }
-    int chosen = 0;      // lane j keeps slot j
-    double logit = 0.0, top = 0.0;
-    for (int j = 0; j < top_k; ++j) {
-        uint64_t best = 0;
-        double value = 0.0;
-        int e = 0x7fffffff;
-#pragma unroll
-        for (int i = 0; i < PER; ++i)
-            if (key[i] > best) {
-                best = key[i];
-                value = v[i];
-                e = lane + 64 * i;
-            }
-#pragma unroll
-        for (int m = 1; m < 64; m *= 2) {
-            const uint64_t b2 = __shfl_xor(best, m);
-            const double v2 = __shfl_xor(value, m);
-            const int e2 = __shfl_xor(e, m);
-            if (b2 > best || (b2 == best && e2 < e)) {
-                best = b2;
-                value = v2;
-                e = e2;
-            }
-        }
-        if (lane == j) {
-            chosen = e;
-            logit = value;
-        }
-        if (j == 0)
-            top = value;
-#pragma unroll
-        for (int i = 0; i < PER; ++i)
-            if (e == lane + 64 * i)
-                key[i] = 0;
-    }
-    const float mine = lane < top_k ? expf((float)(logit - top)) : 0.0f;
-    float sum = mine;
-    if (!renormalize) {
-        sum = 0.0f;
-#pragma unroll
-        for (int i = 0; i < PER; ++i)
-            sum += lane + 64 * i < experts ? expf((float)(v[i] - top)) : 0.0f;
-    }
-    sum = wave_sum(sum);
-    if (lane < top_k) {
-        ids[(int64_t)t * top_k + lane] = chosen;
-        probs[(int64_t)t * top_k + lane] = mine / sum;
+    const double *mine = partial + (int64_t)t * experts + (e < experts ? e : 0);
+    const int64_t part = (int64_t)tokens * experts;
+    double v = 0.0;
+#pragma unroll 8
+    for (int s = 0; s < parts; ++s)
+        v += mine[s * part];
+    const uint64_t key = order_key(v);
+    keys[e] = key;
+    if (e == 0)
+        tied = 0;
+    __syncthreads();
+    int rank = 0;
+#pragma unroll 8
+    for (int j = 0; j < experts; ++j)
+        rank += keys[j] > key;
+    // equal logits got one rank: whoever finds another expert there has company
+    if (e < experts)
+        holder[rank] = e;
+    __syncthreads();
+    if (e < experts && holder[rank] != e)
+        tied = 1;
+    __syncthreads();
+    if (tied)
+        for (int j = 0; j < e && j < experts; ++j)
+            rank += keys[j] == key;
+    if (e >= experts)
+        rank = experts;
+    if (rank == 0)
+        top = v;
+    __syncthreads();
+    const float w = e < experts ? expf((float)(v - top)) : 0.0f;
+    float sum = wave_sum(renormalize && rank >= top_k ? 0.0f : w);
+    if (lane == 0)
+        sums[wave] = sum;
+    __syncthreads();
+    sum = 0.0f;
+    for (int i = 0; i < (int)blockDim.x / 64; ++i)
+        sum += sums[i];
+    if (rank < top_k) {
+        ids[(int64_t)t * top_k + rank] = e;
+        probs[(int64_t)t * top_k + rank] = w / sum;
     }
 }
 
@@ -200,29 +208,35 @@ struct UpArgs {
     float limit;
 };
 
+constexpr int kUpWaves = 4;
+
 template <int ACT, int G>
-__device__ __forceinline__ void up_pass(const UpArgs &a, int e, int i0, const uint16_t *list, int n, f32x4 *joined)
+__device__ __forceinline__ void up_pass(const UpArgs &a, int e, int i0, const uint16_t *list, int n, u32x4 *shared)
 {
     constexpr int RT = ACT == ACT_SWIGLU ? 2 : 1;  // gate and up, or the one product
+    constexpr int DEPTH = G == 1 ? 3 : 2;
     const int lane = lane_id(), wave = wave_in_block();
-    const int k8 = lane / 16 * 8;
-    const uint16_t *w[RT], *b[1][G];
-    const int row = i0 + lane % 16 < a.inter ? i0 + lane % 16 : a.inter - 1;  // past the end: read again, not stored
+    const int there = a.inter - i0 < 16 ? a.inter - i0 : 16;
+    const uint32_t row_bytes = (uint32_t)a.hidden * 2u;
+    rsrc_t w[RT];
 #pragma unroll
     for (int r = 0; r < RT; ++r)
-        w[r] = a.w + ((int64_t)e * RT * a.inter + (int64_t)r * a.inter + row) * a.hidden + k8;
+        w[r] = make_rsrc(a.w + (((int64_t)e * RT + r) * a.inter + i0) * a.hidden, (uint32_t)there * row_bytes);
+    const rsrc_t x = make_rsrc(a.x, (uint32_t)a.tokens * row_bytes);
+    uint32_t col[G][2];
 #pragma unroll
-    for (int g = 0; g < G; ++g) {
-        const int s = g * 16 + lane % 16;
-        b[0][g] = a.x + (int64_t)(list[s < n ? s : n - 1] / a.top_k) * a.hidden + k8;
-    }
+    for (int g = 0; g < G; ++g)
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+            const int s = g * 16 + p * 8 + lane / 8;
+            col[g][p] = s < n ? (uint32_t)(list[s] / a.top_k) * row_bytes + lane % 8 * 16 : kNowhere;
+        }
     f32x4 acc[RT][G];
-#pragma unroll
-    for (int r = 0; r < RT; ++r)
-#pragma unroll
-        for (int g = 0; g < G; ++g)
-            acc[r][g] = f32x4{0, 0, 0, 0};
-    stream_products<DT_BF16, RT, G, 1>(acc, w, b, 1, a.hidden, wave * kStreamStep, 4 * kStreamStep);
+    clear(acc);
+    stream_products<DT_BF16, RT, G, DEPTH, 1>(acc, w, row_bytes, x, col, a.hidden, wave * kLineK,
+                                              kUpWaves * kLineK, shared + wave * kStage<RT, G>);
+    __syncthreads();  // the sums take the place of the stages
+    f32x4 *joined = reinterpret_cast<f32x4 *>(shared);
 #pragma unroll
     for (int r = 0; r < RT; ++r)
 #pragma unroll
@@ -238,7 +252,7 @@ __device__ __forceinline__ void up_pass(const UpArgs &a, int e, int i0, const ui
         for (int r = 0; r < RT; ++r) {
             z[r] = 0.0f;
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
+            for (int q = 0; q < kUpWaves; ++q)
                 z[r] += joined[((q * RT + r) * G + g) * 64 + lane][wave];
         }
         const int s = g * 16 + lane % 16;
@@ -256,12 +270,13 @@ __device__ __forceinline__ void up_pass(const UpArgs &a, int e, int i0, const ui
 }
 
 // blockIdx.y: a pair (by_pair: it stands for its expert if no earlier pair has the same), or
-// an expert, whichever is fewer.
-template <int ACT>
-__global__ __launch_bounds__(256) void moe_up_kernel(UpArgs a)
+// an expert, whichever is fewer. G: groups of 16 tokens that share one read of the weights;
+// an expert with more tokens reads them again.
+template <int ACT, int G>
+__global__ __launch_bounds__(kUpWaves * 64) void moe_up_kernel(UpArgs a)
 {
     constexpr int RT = ACT == ACT_SWIGLU ? 2 : 1;
-    __shared__ f32x4 joined[4 * RT * (kPass / 16) * 64];
+    __shared__ u32x4 shared[kUpWaves * kStage<RT, G>];  // the waves' stages, then their sums
     __shared__ uint16_t list[kMaxPairs];
     __shared__ int count;
     const int pairs = live_tokens(a.valid, a.tokens) * a.top_k;
@@ -283,14 +298,14 @@ __global__ __launch_bounds__(256) void moe_up_kernel(UpArgs a)
     if (n == 0 || (a.by_pair && list[0] != (int)blockIdx.y))
         return;
     const int i0 = blockIdx.x * 16;
-    for (int p = 0; p < n; p += kPass) {
-        const int m = n - p < kPass ? n - p : kPass;
-        if (m <= 16)
-            up_pass<ACT, 1>(a, e, i0, list + p, m, joined);
-        else if (m <= 32)
-            up_pass<ACT, 2>(a, e, i0, list + p, m, joined);
+    for (int p = 0; p < n; p += G * 16) {
+        const int m = n - p < G * 16 ? n - p : G * 16;
+        if (G == 1 || m <= 16)
+            up_pass<ACT, 1>(a, e, i0, list + p, m, shared);
+        else if (G == 2 || m <= 32)
+            up_pass<ACT, G < 2 ? 1 : 2>(a, e, i0, list + p, m, shared);
         else
-            up_pass<ACT, 4>(a, e, i0, list + p, m, joined);
+            up_pass<ACT, G>(a, e, i0, list + p, m, shared);
     }
 }
 
@@ -302,87 +317,102 @@ struct DownArgs {
     int tokens, hidden, inter, experts, top_k, parts;
 };
 
-template <int G>
-__device__ __forceinline__ void down_pass(const DownArgs &a, const uint16_t *w, const uint16_t *list, int n, int part,
-                                          float *sums)
+template <int YDT>
+__device__ __forceinline__ void finish_row(const DownArgs &a, int64_t at, float v)
 {
-    const int lane = lane_id(), k8 = lane / 16 * 8;
-    const uint16_t *wr[1] = {w}, *b[2][G];
+    if (a.residual)
+        v += load1<DT_BF16>(a.residual, at);
+    store1<YDT>(a.y, at, v);
+}
+
+// Waves of a workgroup of the down products: fewer where their stages in shared memory are larger.
+template <int G>
+constexpr int kDownWaves = G == 4 ? 4 : 8;
+
+template <int G>
+__device__ __forceinline__ void h_columns(const DownArgs &a, const uint16_t *list, int n, uint32_t (&col)[G][2])
+{
+    const int lane = lane_id();
+#pragma unroll
+    for (int g = 0; g < G; ++g)
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+            const int s = g * 8 + p * 4 + lane / 16;
+            col[g][p] = s < n ? (uint32_t)list[s] * (uint32_t)a.inter * 4u + lane % 16 * 16 : kNowhere;
+        }
+}
+
+// The two terms of h take a column each: a group is 8 pairs, columns 0-7 their first terms and
+// 8-15 their second ones, joined after the sums.
+template <int G>
+__device__ __forceinline__ void down_pass(const DownArgs &a, const rsrc_t (&w)[1], const uint16_t *list, int n, int part,
+                                          float *sums, u32x4 *stage)
+{
+    constexpr int DEPTH = G == 1 ? 4 : (G == 2 ? 3 : 2);
+    const int lane = lane_id();
+    const rsrc_t h = make_rsrc(a.h, (uint32_t)(a.tokens * a.top_k) * (uint32_t)a.inter * 4u);
+    uint32_t col[G][2];
+    h_columns(a, list, n, col);
     f32x4 acc[1][G];
+    clear(acc);
+    stream_products<DT_BF16, 1, G, DEPTH, 2>(acc, w, (uint32_t)a.inter * 2u, h, col, a.inter, part * kLineK,
+                                             a.parts * kLineK, stage);
 #pragma unroll
     for (int g = 0; g < G; ++g) {
-        const int s = g * 16 + lane % 16;
-        b[0][g] = a.h + h_at(list[s < n ? s : n - 1], a.inter, k8);
-        b[1][g] = b[0][g] + 8;
-        acc[0][g] = f32x4{0, 0, 0, 0};
-    }
-    stream_products<DT_BF16, 1, G, 2>(acc, wr, b, 2, a.inter, part * kStreamStep, a.parts * kStreamStep);
+        f32x4 v = acc[0][g];
 #pragma unroll
-    for (int g = 0; g < G; ++g) {
-        const int s = g * 16 + lane % 16;
-        if (s < n)
-            *reinterpret_cast<f32x4 *>(sums + (list[s] * a.parts + part) * 16 + lane / 16 * 4) = acc[0][g];
+        for (int r = 0; r < 4; ++r)
+            v[r] += dpp<0x128>(v[r]);  // row_ror:8: the other term's column
+        const int s = g * 8 + lane % 8;
+        if (s < n && lane % 16 < 8)
+            *reinterpret_cast<f32x4 *>(sums + (list[s] * a.parts + part) * 16 + lane / 16 * 4) = v;
     }
 }
 
-template <int YDT>
-__global__ __launch_bounds__(256) void moe_down_kernel(DownArgs a)
+template <int YDT, int G>
+__global__ __launch_bounds__(kDownWaves<G> * 64) void moe_down_kernel(DownArgs a)
 {
+    constexpr int W = kDownWaves<G>;
     extern __shared__ f32x4 dynamic[];  // [pairs][parts][16] fp32
     __shared__ int ids[kMaxPairs];
-    __shared__ int first[kMaxExperts];
-    __shared__ uint16_t units[kMaxPairs];
-    __shared__ uint16_t lists[4][kMaxPairs];
-    __shared__ int unit_count;
+    __shared__ uint16_t lists[W][kMaxPairs];
+    __shared__ u32x4 stages[W * kStage<1, G>];
     float *sums = reinterpret_cast<float *>(dynamic);
-    const int lane = lane_id(), wave = wave_in_block(), tid = threadIdx.x;
+    const int wave = wave_in_block(), tid = threadIdx.x;
     const int live = live_tokens(a.valid, a.tokens), pairs = live * a.top_k;
-    for (int e = tid; e < a.experts; e += 256)
-        first[e] = kMaxPairs;
-    __syncthreads();
-    for (int p = tid; p < pairs; p += 256) {
+    for (int p = tid; p < pairs; p += W * 64) {
         const int e = a.ids[p];
-        const bool ok = e >= 0 && e < a.experts;
-        ids[p] = ok ? e : -1;
-        if (ok)
-            atomicMin(&first[e], p);
+        ids[p] = e >= 0 && e < a.experts ? e : -1;
     }
     __syncthreads();
-    if (wave == 0) {  // the pairs that are their expert's first
-        int n = 0;
-        for (int p0 = 0; p0 < pairs; p0 += 64) {
-            const int p = p0 + lane;
-            const bool is = p < pairs && ids[p] >= 0 && first[ids[p]] == p;
-            const uint64_t m = __ballot(is);
-            if (is)
-                units[n + __popcll(m & (((uint64_t)1 << lane) - 1))] = (uint16_t)p;
-            n += __popcll(m);
-        }
-        if (lane == 0)
-            unit_count = n;
-    }
-    __syncthreads();
-    const int n_units = unit_count;
     const int c0 = blockIdx.x * 16;
-    const int row = c0 + lane % 16 < a.hidden ? c0 + lane % 16 : a.hidden - 1;
+    const int there = a.hidden - c0 < 16 ? a.hidden - c0 : 16;
     uint16_t *list = lists[wave];
-    for (int u = wave; u < n_units * a.parts; u += 4) {
-        const int e = __builtin_amdgcn_readfirstlane(ids[units[u / a.parts]]), part = u % a.parts;
+    // a pair stands for its expert if no earlier pair has the same
+    for (int u = wave; u < pairs * a.parts; u += W) {
+        const int p = u / a.parts, part = u % a.parts;
+        const int e = __builtin_amdgcn_readfirstlane(ids[p]);
+        if (e < 0)
+            continue;
         const int n = list_pairs(ids, pairs, e, list);
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        const uint16_t *w = a.w + ((int64_t)e * a.hidden + row) * a.inter + lane / 16 * 8;
-        for (int p = 0; p < n; p += kPass) {
-            const int m = n - p < kPass ? n - p : kPass;
-            if (m <= 16)
-                down_pass<1>(a, w, list + p, m, part, sums);
-            else if (m <= 32)
-                down_pass<2>(a, w, list + p, m, part, sums);
+        if (__builtin_amdgcn_readfirstlane(list[0]) != p)
+            continue;
+        const rsrc_t w[1] = {
+            make_rsrc(a.w + ((int64_t)e * a.hidden + c0) * a.inter, (uint32_t)there * (uint32_t)a.inter * 2u)};
+        u32x4 *stage = stages + wave * kStage<1, G>;
+        for (int q = 0; q < n; q += G * 8) {
+            const int m = n - q < G * 8 ? n - q : G * 8;
+            if (G == 1 || m <= 8)
+                down_pass<1>(a, w, list + q, m, part, sums, stage);
+            else if (G == 2 || m <= 16)
+                down_pass<G < 2 ? 1 : 2>(a, w, list + q, m, part, sums, stage);
             else
-                down_pass<4>(a, w, list + p, m, part, sums);
+                down_pass<G>(a, w, list + q, m, part, sums, stage);
         }
     }
     __syncthreads();
-    for (int i = tid; i < live * 16; i += 256) {
+    for (int i = tid; i < live * 16; i += W * 64) {
         const int t = i / 16, c = c0 + i % 16;
         if (c >= a.hidden)
             continue;
@@ -394,11 +424,181 @@ __global__ __launch_bounds__(256) void moe_down_kernel(DownArgs a)
             for (int s = 0; s < a.parts; ++s)
                 v += sums[(p * a.parts + s) * 16 + i % 16];
         }
-        const int64_t at = (int64_t)t * a.hidden + c;
-        if (a.residual)
-            v += load1<DT_BF16>(a.residual, at);
-        store1<YDT>(a.y, at, v);
+        finish_row<YDT>(a, (int64_t)t * a.hidden + c, v);
     }
+}
+
+// The down product where the chosen experts' tokens are many: h (two terms of every pair) is
+// then as large a stream as the weights if each workgroup of 16 columns reads all of it. Here
+// a workgroup takes 128 columns and every gridDim.y-th chosen expert, a wave 16 of the
+// columns; the waves walk the same h at the same time, so all but one find it in the L1
+// cache. A wave adds each token's values in LDS, expert by expert in one order. With
+// gridDim.y > 1 the workgroups leave fp32 partial rows for moe_combine_kernel.
+constexpr int kManyTokens = 128, kManyPairs = 128;
+constexpr int kManyWaves = 1024;
+constexpr int kManyTiles = 2, kManyCols = 16 * kManyTiles;  // a wave's columns
+
+// Rows of eight pairs' sums added to their tokens'. Slots of one token (an id that a token
+// has twice) follow each other, as the list ascends.
+__device__ __forceinline__ void add_to_tokens(const f32x4 &v, int token, bool live, float *mine)
+{
+    const int lane = lane_id();
+    float *at = mine + token * kManyCols + lane / 16 * 4;
+    const int before = __shfl_up(token, 1);
+    const bool twice = live && lane % 16 > 0 && before == token;
+    if (__ballot(twice) == 0) {
+        if (live)
+            *reinterpret_cast<f32x4 *>(at) += v;
+        return;
+    }
+    for (int j = 0; j < 8; ++j) {
+        if (live && lane % 16 == j)
+            *reinterpret_cast<f32x4 *>(at) += v;
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    }
+}
+
+template <int G>
+__device__ __forceinline__ void down_many_pass(const DownArgs &a, const rsrc_t (&w)[kManyTiles], const rsrc_t &h,
+                                               const uint16_t *list, int n, float *mine, u32x4 *stage)
+{
+    constexpr int DEPTH = G == 1 ? 4 : (G == 2 ? 3 : 2);
+    const int lane = lane_id();
+    uint32_t col[G][2];
+    h_columns(a, list, n, col);
+    int token[G];
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+        const int s = g * 8 + lane % 8;
+        token[g] = list[s < n ? s : n - 1] / a.top_k;
+    }
+    f32x4 acc[kManyTiles][G];
+    clear(acc);
+    stream_products<DT_BF16, kManyTiles, G, DEPTH, 2>(acc, w, (uint32_t)a.inter * 2u, h, col, a.inter, 0, kLineK, stage);
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+#pragma unroll
+        for (int i = 0; i < kManyTiles; ++i) {
+            f32x4 v = acc[i][g];
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                v[r] += dpp<0x128>(v[r]);  // row_ror:8: the other term's column
+            add_to_tokens(v, token[g], g * 8 + lane % 8 < n && lane % 16 < 8, mine + i * 16);
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    }
+}
+
+template <int YDT, int G>
+__global__ __launch_bounds__(kDownWaves<G> * 64) void moe_down_many_kernel(DownArgs a, float *partial)
+{
+    constexpr int W = kDownWaves<G>;
+    extern __shared__ f32x4 dynamic[];  // [waves][tokens][kManyCols] fp32
+    __shared__ int ids[kMaxPairs];
+    __shared__ int first[kMaxExperts], count[kMaxExperts];
+    __shared__ uint16_t units[kMaxPairs], starts[kMaxPairs], list[kMaxPairs];
+    __shared__ u32x4 stages[W * kStage<kManyTiles, G>];
+    __shared__ int unit_count;
+    u32x4 *stage = stages + wave_in_block() * kStage<kManyTiles, G>;
+    const int lane = lane_id(), wave = wave_in_block(), tid = threadIdx.x;
+    const int live = live_tokens(a.valid, a.tokens), pairs = live * a.top_k;
+    float *mine = reinterpret_cast<float *>(dynamic) + wave * a.tokens * kManyCols;
+    for (int e = tid; e < a.experts; e += W * 64) {
+        first[e] = kMaxPairs;
+        count[e] = 0;
+    }
+    for (int i = lane; i < live * (kManyCols / 4); i += 64)
+        reinterpret_cast<f32x4 *>(mine)[i] = f32x4{0, 0, 0, 0};
+    __syncthreads();
+    for (int p = tid; p < pairs; p += W * 64) {
+        const int e = a.ids[p];
+        const bool ok = e >= 0 && e < a.experts;
+        ids[p] = ok ? e : -1;
+        if (ok) {
+            atomicMin(&first[e], p);
+            atomicAdd(&count[e], 1);
+        }
+    }
+    __syncthreads();
+    if (wave == 0) {  // the pairs that are their expert's first, and where its list starts
+        int n = 0, start = 0;
+        for (int p0 = 0; p0 < pairs; p0 += 64) {
+            const int p = p0 + lane;
+            const bool is = p < pairs && ids[p] >= 0 && first[ids[p]] == p;
+            const uint64_t m = __ballot(is);
+            int sum = is ? count[ids[p]] : 0;
+            const int own = sum;
+#pragma unroll
+            for (int d = 1; d < 64; d *= 2) {
+                const int up = __shfl_up(sum, d);
+                sum += lane >= d ? up : 0;
+            }
+            if (is) {
+                const int at = n + __popcll(m & (((uint64_t)1 << lane) - 1));
+                units[at] = (uint16_t)p;
+                starts[at] = (uint16_t)(start + sum - own);
+            }
+            n += __popcll(m);
+            start += __shfl(sum, 63);
+        }
+        if (lane == 0)
+            unit_count = n;
+    }
+    __syncthreads();
+    const int n_units = unit_count, step = gridDim.y;
+    for (int u = blockIdx.y + wave * step; u < n_units; u += W * step)
+        list_pairs(ids, pairs, ids[units[u]], list + starts[u]);
+    __syncthreads();
+    const int c0 = (blockIdx.x * W + wave) * kManyCols;
+    if (c0 >= a.hidden)
+        return;
+    const rsrc_t h = make_rsrc(a.h, (uint32_t)(a.tokens * a.top_k) * (uint32_t)a.inter * 4u);
+    for (int u = blockIdx.y; u < n_units; u += step) {
+        const int e = __builtin_amdgcn_readfirstlane(ids[units[u]]);
+        const int n = __builtin_amdgcn_readfirstlane(count[e]);
+        const uint16_t *l = list + starts[u];
+        rsrc_t w[kManyTiles];
+#pragma unroll
+        for (int i = 0; i < kManyTiles; ++i) {
+            const int c = c0 + 16 * i, there = a.hidden - c < 16 ? (a.hidden - c > 0 ? a.hidden - c : 0) : 16;
+            w[i] = make_rsrc(a.w + ((int64_t)e * a.hidden + (there ? c : 0)) * a.inter,
+                             (uint32_t)there * (uint32_t)a.inter * 2u);
+        }
+        for (int p = 0; p < n; p += G * 8) {
+            const int m = n - p < G * 8 ? n - p : G * 8;
+            if (G == 1 || m <= 8)
+                down_many_pass<1>(a, w, h, l + p, m, mine, stage);
+            else if (G == 2 || m <= 16)
+                down_many_pass<G < 2 ? 1 : 2>(a, w, h, l + p, m, mine, stage);
+            else
+                down_many_pass<G>(a, w, h, l + p, m, mine, stage);
+        }
+    }
+    for (int i = lane; i < live * kManyCols; i += 64) {
+        const int t = i / kManyCols, c = c0 + i % kManyCols;
+        if (c >= a.hidden)
+            continue;
+        const int64_t at = (int64_t)t * a.hidden + c;
+        if (step > 1)
+            partial[(int64_t)blockIdx.y * a.tokens * a.hidden + at] = mine[i];
+        else
+            finish_row<YDT>(a, at, mine[i]);
+    }
+}
+
+// y = residual + the partial rows in order. A lane takes two neighbouring columns.
+template <int YDT>
+__global__ __launch_bounds__(256) void moe_combine_kernel(DownArgs a, const float *partial, int parts)
+{
+    const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4, all = (int64_t)a.tokens * a.hidden;
+    if (i >= (int64_t)live_tokens(a.valid, a.tokens) * a.hidden)
+        return;
+    f32x4 v = *reinterpret_cast<const f32x4 *>(partial + i);
+    for (int p = 1; p < parts; ++p)
+        v += *reinterpret_cast<const f32x4 *>(partial + p * all + i);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        finish_row<YDT>(a, i + j, v[j]);
 }
 
 // ---------------------------------------------------------------------------
@@ -411,40 +611,48 @@ struct RouteSizes {
 
 bool good_route(const RouteSizes &s)
 {
-    return s.tokens >= 0 && s.tokens <= (1 << 20) && s.hidden >= 8 && s.hidden <= (1 << 20) && s.experts >= 1 &&
+    return s.tokens >= 0 && s.tokens <= (1 << 19) && s.hidden >= 8 && s.hidden <= (1 << 20) && s.experts >= 1 &&
            s.experts <= kMaxExperts && s.tokens * s.experts <= (1 << 25);
 }
 
-int64_t route_bytes(const RouteSizes &s) { return round_up(s.tokens * s.experts * 8, 16); }
-
-template <int PER>
-block_status_t choose(const double *logits, int *ids, float *probs, const RouteSizes &s, int top_k, int renormalize,
-                      const int *valid, hipStream_t st)
+// k of a part, and the parts: a workgroup of 16 waves a CU, and no part shorter than two steps
+// a wave. (Few parts: whoever chooses adds them up. Four waves a workgroup, so 28 parts of one
+// token's 7168 x 64, took 5.1 us for that.)
+int route_part(const RouteSizes &s)
 {
-    return launch(route_choose_kernel<PER>, dim3((unsigned)s.tokens), dim3(64), 0, st, logits, ids, probs,
-                  (int)s.tokens, s.experts, top_k, renormalize, valid);
+    const int64_t tiles = ceil_div(s.tokens, kRouteTile) * ceil_div(s.experts, kRouteTile);
+    const int64_t wanted = tiles < 256 ? 256 / tiles : 1;
+    const int64_t k = round_up(ceil_div(s.hidden, wanted), kRouteStep);
+    const int64_t least = 2 * kRouteWaves * kRouteStep;
+    return (int)(k < least ? least : k);
+}
+
+int64_t route_parts(const RouteSizes &s) { return ceil_div(s.hidden, route_part(s)); }
+
+int64_t route_bytes(const RouteSizes &s)
+{
+    return s.tokens > 0 ? round_up(route_parts(s) * s.tokens * s.experts * 8, 16) : 0;
 }
 
 block_status_t route(const uint16_t *x, const void *router, block_dtype_t rdt, int *ids, float *probs,
                      const RouteSizes &s, int top_k, int renormalize, const int *valid, void *ws, hipStream_t st)
 {
-    double *logits = static_cast<double *>(ws);
+    double *partial = static_cast<double *>(ws);
     const char *xc = reinterpret_cast<const char *>(x), *rc = static_cast<const char *>(router);
-    const dim3 grid((unsigned)ceil_div(s.tokens * s.experts, 4));
+    const dim3 grid((unsigned)ceil_div(s.experts, kRouteTile), (unsigned)ceil_div(s.tokens, kRouteTile),
+                    (unsigned)route_parts(s)),
+        threads(kRouteWaves * 64);
     block_status_t r;
     if (rdt == BLOCK_FP32)
-        r = launch(route_logits_kernel<DT_F32>, grid, dim3(256), 0, st, xc, rc, logits, (int)s.tokens, (int)s.hidden,
-                   s.experts, valid);
+        r = launch(route_logits_kernel<DT_F32>, grid, threads, 0, st, xc, rc, partial, (int)s.tokens, (int)s.hidden,
+                   s.experts, route_part(s), valid);
     else
-        r = launch(route_logits_kernel<DT_BF16>, grid, dim3(256), 0, st, xc, rc, logits, (int)s.tokens, (int)s.hidden,
-                   s.experts, valid);
+        r = launch(route_logits_kernel<DT_BF16>, grid, threads, 0, st, xc, rc, partial, (int)s.tokens, (int)s.hidden,
+                   s.experts, route_part(s), valid);
     if (r)
         return r;
-    if (s.experts <= 64)
-        return choose<1>(logits, ids, probs, s, top_k, renormalize, valid, st);
-    if (s.experts <= 256)
-        return choose<4>(logits, ids, probs, s, top_k, renormalize, valid, st);
-    return choose<16>(logits, ids, probs, s, top_k, renormalize, valid, st);
+    return launch(route_choose_kernel, dim3((unsigned)s.tokens), dim3((unsigned)round_up(s.experts, 64)), 0, st,
+                  partial, ids, probs, (int)s.tokens, s.experts, (int)route_parts(s), top_k, renormalize, valid);
 }
 
 struct ExpertSizes {
@@ -467,18 +675,89 @@ block_status_t check_experts(const ExpertSizes &s, block_act_t act, float limit)
     return BLOCK_OK;
 }
 
-int64_t expert_bytes(int64_t tokens, int top_k, int64_t inter) { return tokens * top_k * inter * 4; }
+// Workgroups that share the chosen experts of one block of 128 output columns in the down
+// product, or 0 for the form of a few pairs.
+int down_shares(const ExpertSizes &s);
 
-// Parts the down product of one expert is cut into, so that a workgroup's four waves all
-// have work when few experts are reached.
+struct ExpertSpace {
+    int64_t h, all;  // bytes: h, then the partial rows of y
+};
+
+ExpertSpace expert_space(const ExpertSizes &s)
+{
+    const int64_t h = round_up(s.tokens * s.top_k * s.inter * 4, 16), shares = down_shares(s);
+    return {h, h + (shares > 1 ? shares * s.tokens * s.hidden * 4 : 0)};
+}
+
+// Parts the down product of one expert is cut into, so that a workgroup's waves all have
+// work when few experts are reached.
 int down_parts(const ExpertSizes &s)
 {
     const int64_t pairs = s.tokens * s.top_k;
     const int64_t units = pairs < s.experts ? pairs : s.experts;
     int parts = 1;
-    while (units * parts < 8 && pairs * parts * 2 <= kMaxPairs && parts * 2 * kStreamStep <= s.inter)
+    while (units * parts < 16 && pairs * parts * 2 <= kMaxPairs && parts * 4 * kLineK <= s.inter)
         parts *= 2;
     return parts;
+}
+
+int down_shares(const ExpertSizes &s)
+{
+    const int64_t pairs = s.tokens * s.top_k;
+    if (s.tokens > kManyTokens || pairs < kManyPairs)
+        return 0;
+    const int64_t units = pairs < s.experts ? pairs : s.experts;
+    int shares = 1;
+    while (shares < 16 && shares * 2 <= units && ceil_div(s.hidden, kManyCols) * shares < kManyWaves)
+        shares *= 2;
+    return shares;
+}
+
+// Groups of tokens that share a read of an expert's weights: enough for one and a half times
+// the tokens an expert has on average. An expert with more reads its weights again, but
+// registers for more would cost waves in flight.
+int token_groups(const ExpertSizes &s, int group)
+{
+    const int64_t some = ceil_div(3 * s.tokens * s.top_k, 2 * s.experts);
+    const int64_t each = s.tokens < some ? s.tokens : some;
+    return each <= group ? 1 : (each <= 2 * group ? 2 : 4);
+}
+
+template <int ACT>
+block_status_t launch_up(const UpArgs &u, int groups, dim3 grid, hipStream_t st)
+{
+    if (groups == 1)
+        return launch(moe_up_kernel<ACT, 1>, grid, dim3(kUpWaves * 64), 0, st, u);
+    if (groups == 2)
+        return launch(moe_up_kernel<ACT, 2>, grid, dim3(kUpWaves * 64), 0, st, u);
+    return launch(moe_up_kernel<ACT, 4>, grid, dim3(kUpWaves * 64), 0, st, u);
+}
+
+template <int YDT>
+block_status_t launch_down(const DownArgs &d, int groups, dim3 grid, uint32_t lds, hipStream_t st)
+{
+    if (groups == 1)
+        return launch(moe_down_kernel<YDT, 1>, grid, dim3(kDownWaves<1> * 64), lds, st, d);
+    if (groups == 2)
+        return launch(moe_down_kernel<YDT, 2>, grid, dim3(kDownWaves<2> * 64), lds, st, d);
+    return launch(moe_down_kernel<YDT, 4>, grid, dim3(kDownWaves<4> * 64), lds, st, d);
+}
+
+template <int YDT>
+block_status_t launch_down_many(const DownArgs &d, int groups, int shares, dim3 grid, uint32_t lds, float *partial,
+                                hipStream_t st)
+{
+    block_status_t r;
+    if (groups == 1)
+        r = launch(moe_down_many_kernel<YDT, 1>, grid, dim3(kDownWaves<1> * 64), lds, st, d, partial);
+    else if (groups == 2)
+        r = launch(moe_down_many_kernel<YDT, 2>, grid, dim3(kDownWaves<2> * 64), lds, st, d, partial);
+    else
+        r = launch(moe_down_many_kernel<YDT, 4>, grid, dim3(kDownWaves<4> * 64), lds, st, d, partial);
+    if (r || shares == 1)
+        return r;
+    return launch(moe_combine_kernel<YDT>, dim3((unsigned)ceil_div((int64_t)d.tokens * d.hidden, 1024)), dim3(256), 0,
+                  st, d, partial, shares);
 }
 
 block_status_t experts(const uint16_t *x, const uint16_t *w_up, const uint16_t *w_down, const int *ids,
@@ -492,22 +771,27 @@ block_status_t experts(const uint16_t *x, const uint16_t *w_up, const uint16_t *
     const int64_t pairs = s.tokens * s.top_k;
     u.by_pair = pairs < s.experts;
     const dim3 grid((unsigned)ceil_div(s.inter, 16), (unsigned)(u.by_pair ? pairs : s.experts));
-    block_status_t r;
-    if (act == BLOCK_ACT_SWIGLU)
-        r = launch(moe_up_kernel<ACT_SWIGLU>, grid, dim3(256), 0, st, u);
-    else
-        r = launch(moe_up_kernel<ACT_SQUARED_RELU>, grid, dim3(256), 0, st, u);
-    if (r)
+    const int up_groups = token_groups(s, 16);
+    if (const block_status_t r = act == BLOCK_ACT_SWIGLU ? launch_up<ACT_SWIGLU>(u, up_groups, grid, st)
+                                                         : launch_up<ACT_SQUARED_RELU>(u, up_groups, grid, st))
         return r;
     DownArgs d = {};
     d.h = u.h, d.w = w_down, d.residual = residual, d.ids = ids, d.y = static_cast<char *>(y), d.valid = valid;
     d.tokens = u.tokens, d.hidden = u.hidden, d.inter = u.inter, d.experts = u.experts, d.top_k = u.top_k;
+    const int groups = token_groups(s, 8), shares = down_shares(s);
+    if (shares > 0) {
+        const int waves = groups == 4 ? kDownWaves<4> : kDownWaves<1>;
+        const uint32_t lds = (uint32_t)(waves * s.tokens * kManyCols * 4);
+        const dim3 tiles((unsigned)ceil_div(s.hidden, kManyCols * waves), (unsigned)shares);
+        float *partial = reinterpret_cast<float *>(static_cast<char *>(ws) + expert_space(s).h);
+        return ydt == BLOCK_FP32 ? launch_down_many<DT_F32>(d, groups, shares, tiles, lds, partial, st)
+                                 : launch_down_many<DT_BF16>(d, groups, shares, tiles, lds, partial, st);
+    }
     d.parts = down_parts(s);
     const uint32_t lds = (uint32_t)(pairs * d.parts * 64);
     const dim3 tiles((unsigned)ceil_div(s.hidden, 16));
-    if (ydt == BLOCK_FP32)
-        return launch(moe_down_kernel<DT_F32>, tiles, dim3(256), lds, st, d);
-    return launch(moe_down_kernel<DT_BF16>, tiles, dim3(256), lds, st, d);
+    return ydt == BLOCK_FP32 ? launch_down<DT_F32>(d, groups, tiles, lds, st)
+                             : launch_down<DT_BF16>(d, groups, tiles, lds, st);
 }
 
 bool good_choice(int top_k, int experts) { return top_k >= 1 && top_k <= experts && top_k <= 64; }
@@ -547,11 +831,10 @@ block_status_t block_moe_route(const uint16_t *x, const void *router_weight, blo
     return route(x, router_weight, router_dtype, ids, probs, s, top_k, renormalize, valid_tokens, workspace, stream);
 }
 
-int64_t block_moe_experts_workspace(int64_t tokens, int top_k, int64_t inter)
+int64_t block_moe_experts_workspace(int64_t tokens, int64_t hidden, int64_t inter, int n_experts, int top_k)
 {
-    if (tokens < 0 || tokens > kMaxPairs || top_k < 1 || top_k > kMaxPairs || inter < 0 || inter > (1 << 16))
-        return 0;
-    return expert_bytes(tokens, top_k, inter);
+    const ExpertSizes s = {tokens, hidden, inter, n_experts, top_k};
+    return check_experts(s, BLOCK_ACT_SQUARED_RELU, 0.0f) == BLOCK_OK ? expert_space(s).all : 0;
 }
 
 block_status_t block_moe_experts(const uint16_t *x, const uint16_t *w_up, const uint16_t *w_down, const int32_t *ids,
@@ -567,7 +850,7 @@ block_status_t block_moe_experts(const uint16_t *x, const uint16_t *w_up, const 
         return BLOCK_ERR_INVALID_ARG;
     if (tokens == 0)
         return BLOCK_OK;
-    const int64_t need = expert_bytes(tokens, top_k, inter);
+    const int64_t need = expert_space(s).all;
     if (!x || !w_up || !w_down || !ids || !probs || !y || !workspace || workspace_bytes < need)
         return BLOCK_ERR_INVALID_ARG;
     if (misaligned(x, 16) || misaligned(w_up, 16) || misaligned(w_down, 16) || misaligned(residual, 16) ||
@@ -589,7 +872,7 @@ block_status_t block_moe_experts(const uint16_t *x, const uint16_t *w_up, const 
 
 int64_t block_moe_layer_workspace(int64_t tokens, int64_t hidden, int64_t inter, int n_experts, int top_k)
 {
-    return block_moe_route_workspace(tokens, hidden, n_experts) + block_moe_experts_workspace(tokens, top_k, inter);
+    return block_moe_route_workspace(tokens, hidden, n_experts) + block_moe_experts_workspace(tokens, hidden, inter, n_experts, top_k);
 }
 
 block_status_t block_moe_layer(const uint16_t *x, const void *router_weight, block_dtype_t router_dtype,
@@ -608,7 +891,7 @@ block_status_t block_moe_layer(const uint16_t *x, const void *router_weight, blo
         return r;
     if (tokens == 0)
         return BLOCK_OK;
-    const int64_t route_need = route_bytes(rs), need = route_need + expert_bytes(tokens, top_k, inter);
+    const int64_t route_need = route_bytes(rs), need = route_need + expert_space(s).all;
     if (!x || !router_weight || !w_up || !w_down || !ids || !probs || !y || !workspace || workspace_bytes < need)
         return BLOCK_ERR_INVALID_ARG;
     if (misaligned(x, 16) || misaligned(router_weight, 16) || misaligned(w_up, 16) || misaligned(w_down, 16) ||

@@ -40,7 +40,7 @@ _SIGS = {
     "block_linear_act": [_vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _int, _int, _vp, _i64, _vp],
     "block_moe_route_workspace": [_i64, _i64, _int],
     "block_moe_route": [_vp, _vp, _int, _vp, _vp, _i64, _i64, _int, _int, _int, _vp, _vp, _i64, _vp],
-    "block_moe_experts_workspace": [_i64, _int, _i64],
+    "block_moe_experts_workspace": [_i64, _i64, _i64, _int, _int],
     "block_moe_experts": [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _int, _i64, _i64, _i64, _int, _int, _int, _f32, _vp,
                           _vp, _i64, _vp],
     "block_moe_layer_workspace": [_i64, _i64, _i64, _int, _int],
@@ -263,8 +263,8 @@ def moe_route_workspace(tokens: int, hidden: int, experts: int) -> int:
     return load_library().block_moe_route_workspace(tokens, hidden, experts)
 
 
-def moe_experts_workspace(tokens: int, top_k: int, inter: int) -> int:
-    return load_library().block_moe_experts_workspace(tokens, top_k, inter)
+def moe_experts_workspace(tokens: int, hidden: int, inter: int, experts: int, top_k: int) -> int:
+    return load_library().block_moe_experts_workspace(tokens, hidden, inter, experts, top_k)
 
 
 def moe_layer_workspace(tokens: int, hidden: int, inter: int, experts: int, top_k: int) -> int:
@@ -326,7 +326,7 @@ def moe_experts(x, w_up, w_down, ids, probs, y, *, activation="swiglu", limit=ma
             _TORCH[y.dtype], tokens, hidden, inter, experts, top_k, EXPERT_ACTIVATIONS[activation], float(limit),
             _scalar(valid_tokens))
     _call("block_moe_experts", _device(x, w_up, w_down, ids, probs, residual, y, valid_tokens), stream, args,
-          workspace, moe_experts_workspace(tokens, top_k, inter))
+          workspace, moe_experts_workspace(tokens, hidden, inter, experts, top_k))
     return y
 
 

@@ -128,7 +128,7 @@ def route(x=at(0), w=at(1), rdt=BF16, ids=at(2), probs=at(3), tokens=4, hidden=6
 def test_route_refusals():
     need = load_library().block_moe_route_workspace(4, 64, 8)
     assert need > 0 and route(tokens=0) == OK
-    for bad in (dict(tokens=-1), dict(tokens=(1 << 20) + 1), dict(hidden=0), dict(hidden=(1 << 20) + 8), dict(experts=0),
+    for bad in (dict(tokens=-1), dict(tokens=(1 << 19) + 1), dict(hidden=0), dict(hidden=(1 << 20) + 8), dict(experts=0),
                 dict(experts=1025), dict(k=0), dict(k=9), dict(k=65, experts=128), dict(rdt=F16), dict(x=None),
                 dict(w=None), dict(ids=None), dict(probs=None), dict(ws=None), dict(size=need - 1), dict(ids=at(0)),
                 dict(probs=at(2)), dict(ws=at(1)), dict(valid=at(2))):
@@ -153,7 +153,7 @@ def layer(x=at(0), rw=at(8), rdt=BF16, wu=at(1), wd=at(2), ids=at(3), probs=at(4
 @pytest.mark.parametrize("call", [experts, layer])
 def test_expert_refusals(call):
     lib = load_library()
-    need = (lib.block_moe_experts_workspace(4, 2, 24) if call is experts else
+    need = (lib.block_moe_experts_workspace(4, 64, 24, 8, 2) if call is experts else
             lib.block_moe_layer_workspace(4, 64, 24, 8, 2))
     assert need > 0 and call(tokens=0) == OK
     for bad in (dict(tokens=-1), dict(tokens=513), dict(tokens=1 << 40), dict(hidden=0), dict(inter=0),
