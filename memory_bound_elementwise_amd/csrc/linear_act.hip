@@ -34,6 +34,32 @@ __device__ __forceinline__ void finish(const Args &a, int row, int col, float z)
     store1<DT>(a.y, at, z);
 }
 
+// Eight neighbouring columns at once (col and n multiples of 8).
+template <int DT>
+__device__ __forceinline__ void finish8(const Args &a, int row, int col, float (&z)[8])
+{
+    float f[8];
+    if (a.bias) {
+        widen8<DT>(load8<DT>(reinterpret_cast<const char *>(a.bias), col, a.n), f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            z[i] += f[i];
+    }
+    if (a.act != ACT_NONE) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            z[i] = activate(a.act, z[i]);
+    }
+    const int64_t at = (int64_t)row * a.n;
+    if (a.residual) {
+        widen8<DT>(load8<DT>(reinterpret_cast<const char *>(a.residual + at), col, a.n), f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            z[i] += f[i];
+    }
+    store8<DT>(reinterpret_cast<char *>(a.y + at), col, a.n, z);
+}
+
 // ---------------------------------------------------------------------------
 // Few rows
 // ---------------------------------------------------------------------------
@@ -79,98 +105,229 @@ __global__ __launch_bounds__(WAVES * 64) void linear_few_kernel(Args a)
 }
 
 // ---------------------------------------------------------------------------
-// Many rows: 128 x 128 tiles, 64 k a step; four waves of 64 x 64
+// Many rows
 // ---------------------------------------------------------------------------
-constexpr int kTile = 128, kTileK = 64;
+typedef __attribute__((address_space(3))) void shared_void;
 
-template <int DT>
-__global__ __launch_bounds__(256) void linear_tile_kernel(Args a)
+// Waits for the wave's loads into shared memory and its reads of it, then for the workgroup.
+// (Loads into shared memory count as loads from memory: a fence need not wait for them.)
+// Nothing is moved across.
+__device__ __forceinline__ void wait_and_sync()
 {
-    // rows of eight 16-byte chunks; chunk c of row r lies at c ^ (r % 8), so that the 16 rows
-    // a matrix operand reads at one k fall into different banks
-    __shared__ u32x4 sx[kTile * 8], sw[kTile * 8];
-    const int lane = lane_id(), wave = wave_in_block(), tid = threadIdx.x;
-    const int wide = (a.n + kTile - 1) / kTile;
-    const int r0 = (int)blockIdx.x / wide * kTile, c0 = (int)blockIdx.x % wide * kTile;
-    u32x4 px[4], pw[4];
-    auto fetch = [&](int k0) {
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0)
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_sched_barrier(0);
+}
+
+// Tiles of TM rows of x by TN rows of W, WM x WN waves, 64 k a step. Both operands go straight
+// from memory to shared memory (no registers) into two buffers in turn. A row of a buffer is
+// its eight 16-byte chunks of 64 k, a whole line; chunk c of row r lies at c ^ (r % 8), so that
+// the 16 lanes whose reads of an operand go together fall into different banks. A load's
+// lanes fill shared memory in order, so the exchange is made in the addresses they read.
+// (Four buffers of 32 k reach further ahead but ask the cache for half lines: 9 TB/s of
+// requests were the limit, 413 us for 6720 x 7168 x 4096 where this takes XXX.)
+// Operands are read from shared memory half a step before their products, which leaves one
+// barrier a step and no product waiting for a read.
+//   parts > 1: the sums over one of `parts` ranges of k, to partial [parts][m][n] in fp32.
+template <int DT, int TM, int TN, int WM, int WN>
+__global__ __launch_bounds__(WM * WN * 64) void linear_tile_kernel(Args a, int tiles_m, int tiles_n, int parts,
+                                                                   float *partial)
+{
+    constexpr int W = WM * WN, FM = TM / WM / 16, FN = TN / WN / 16;
+    constexpr int kGroups = (TM + TN) / 8 / W;  // loads of a wave a step, of 8 rows each
+    static_assert((TM + TN) % (8 * W) == 0 && TM % (8 * kGroups) == 0, "");
+    constexpr int kBuffer = (TM + TN) * 8;  // 16-byte chunks
+    // one object each: the compiler then knows that a load into one does not touch the other
+    __shared__ u32x4 s0[kBuffer], s1[kBuffer];
+    const int lane = lane_id(), wave = wave_in_block();
+
+    // Workgroups go to the eight XCDs in turn; each XCD takes a run of tiles, in bands of
+    // rows of x, so that its cache serves one band's x and W moving past it.
+    const int tiles = tiles_m * tiles_n, all = tiles * parts;
+    const int run = (all + 7) / 8, id = (int)blockIdx.x % 8 * run + (int)blockIdx.x / 8;
+    if ((int)blockIdx.x / 8 >= run || id >= all)
+        return;
+    const int part = id / tiles, tile = id % tiles;
+    constexpr int kBand = 4;
+    const int band = tile / (kBand * tiles_n) * kBand, in_band = tile % (kBand * tiles_n);
+    const int high = tiles_m - band < kBand ? tiles_m - band : kBand;
+    const int r0 = (band + in_band % high) * TM, c0 = in_band / high * TN;
+
+    const uint32_t row_bytes = (uint32_t)a.k * 2u;
+    const int rows = a.m - r0 < TM ? a.m - r0 : TM, cols = a.n - c0 < TN ? a.n - c0 : TN;
+    // a wave loads rows of x or rows of W (rows past the end read zeros)
+    const int chunk = lane % 8 ^ lane / 8, group0 = wave * kGroups;
+    const bool loads_x = group0 * 8 < TM;
+    const rsrc_t from = make_rsrc(loads_x ? a.x + (int64_t)r0 * a.k : a.w + (int64_t)c0 * a.k,
+                                  (uint32_t)(loads_x ? rows : cols) * row_bytes);
+    const uint32_t base = (uint32_t)((group0 - (loads_x ? 0 : TM / 8)) * 8 + lane / 8) * row_bytes + chunk * 16;
+
+    const int steps = (a.k + kLineK - 1) / kLineK;
+    const int first = (int)((int64_t)steps * part / parts), last = (int)((int64_t)steps * (part + 1) / parts);
+    auto load = [&](u32x4 *to, int step) {
+        const int k = step * kLineK;
+        const bool in = step < last && k + chunk * 8 < a.k;  // past the last step: zeros
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int row = i * 32 + tid / 8, k = k0 + tid % 8 * 8;
-            const bool in = k < a.k;
-            const int xr = r0 + row < a.m ? r0 + row : a.m - 1, wr = c0 + row < a.n ? c0 + row : a.n - 1;
-            const u32x4 vx = *reinterpret_cast<const u32x4 *>(a.x + (int64_t)xr * a.k + (in ? k : 0));
-            const u32x4 vw = *reinterpret_cast<const u32x4 *>(a.w + (int64_t)wr * a.k + (in ? k : 0));
-            px[i] = in ? vx : u32x4{0, 0, 0, 0};
-            pw[i] = in ? vw : u32x4{0, 0, 0, 0};
+        for (int g = 0; g < kGroups; ++g)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(from, (shared_void *)(to + (group0 + g) * 64), 16,
+                                                     in ? base + (uint32_t)g * 8u * row_bytes : kNowhere, k * 2, 0, 0);
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    f32x4 acc[FM][FN];
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+            acc[i][j] = f32x4{0, 0, 0, 0};
+    const int wm = wave / WN * (TM / WM), wn = wave % WN * (TN / WN);
+    const int i16 = lane % 16, q = lane / 16;
+    struct Operands {
+        u32x4 x[FM], w[FN];
+    };
+    auto read = [&](Operands &o, const u32x4 *from, int half) {
+        const int c = (4 * half + q) ^ i16 % 8;
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+            o.w[j] = from[(TM + wn + j * 16 + i16) * 8 + c];
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+            o.x[i] = from[(wm + i * 16 + i16) * 8 + c];
+    };
+    auto multiply = [&](const Operands &o) {
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+            for (int j = 0; j < FN; ++j)
+                acc[i][j] = mfma16<DT>(o.w[j], o.x[i], acc[i][j]);
+        // order of issue: the reads of the next operands spread over the products
+#pragma unroll
+        for (int i = 0; i < FM + FN; ++i) {
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);                    // a read of shared memory
+            __builtin_amdgcn_sched_group_barrier(0x8, FM * FN / (FM + FN), 0);   // products
         }
     };
-    f32x4 acc[4][4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            acc[i][j] = f32x4{0, 0, 0, 0};
-    const int wx = wave / 2 * 64, ww = wave % 2 * 64;
-    fetch(0);
-    for (int k0 = 0; k0 < a.k; k0 += kTileK) {
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int row = i * 32 + tid / 8, slot = row * 8 + (tid % 8 ^ row % 8);
-            sx[slot] = px[i];
-            sw[slot] = pw[i];
-        }
-        __syncthreads();
-        if (k0 + kTileK < a.k)
-            fetch(k0 + kTileK);
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const int c = u * 4 + lane / 16;
-            u32x4 ax[4], aw[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int rx = wx + i * 16 + lane % 16, rw = ww + i * 16 + lane % 16;
-                ax[i] = sx[rx * 8 + (c ^ rx % 8)];
-                aw[i] = sw[rw * 8 + (c ^ rw % 8)];
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    acc[i][j] = mfma16<DT>(aw[j], ax[i], acc[i][j]);
-        }
+    Operands lo, hi;
+    // One step, its first half's operands in lo. At the barrier everyone has read all of `now`,
+    // which the loads of two steps ahead may then fill, and `after` has come.
+    auto step = [&](u32x4 *now, const u32x4 *after, int t) {
+        read(hi, now, 1);
+        multiply(lo);
+        wait_and_sync();
+        load(now, t + 2);
+        read(lo, after, 0);
+        multiply(hi);
+    };
+    load(s0, first);
+    load(s1, first + 1);
+    wait_and_sync();
+    read(lo, s0, 0);
+    for (int t = first; t < last; t += 2) {  // a step past the last adds zeros
+        step(s0, s1, t);
+        step(s1, s0, t + 1);
     }
-    // acc[i][j][q]: row wx + 16 i + lane % 16, column ww + 16 j + 4 (lane / 16) + q
+    wait_and_sync();  // the last loads, of nothing, also write shared memory
+    // acc[i][j][e] is row wm + 16 i + lane % 16, column wn + 16 j + 4 (lane / 16) + e. Through
+    // shared memory, kRows rows at a time, into rows of eight columns a lane.
+    constexpr int kCols = FN * 16, kChunks = kCols / 4, kOwn = kBuffer * 2 / W;  // 16-byte chunks of a wave
+    constexpr int kFit = kOwn / kChunks, kRows = kFit < FM * 16 ? kFit : FM * 16;
+    u32x4 *const own = wave < W / 2 ? s0 + wave * kOwn : s1 + (wave - W / 2) * kOwn;
+    const int lanes_a_row = kCols / 8, my_row = lane / lanes_a_row, my_col = lane % lanes_a_row * 8;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int row = r0 + wx + i * 16 + lane % 16;
-        if (row >= a.m)
-            continue;
+    for (int i0 = 0; i0 < FM; i0 += kRows / 16) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int i = 0; i < kRows / 16; ++i)
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int col = c0 + ww + j * 16 + lane / 16 * 4 + q;
-                if (col < a.n)
-                    finish<DT>(a, row, col, acc[i][j][q]);
+            for (int j = 0; j < FN; ++j) {
+                const int row = i * 16 + i16;
+                own[row * kChunks + (j * 4 + q ^ row % kChunks)] = __builtin_bit_cast(u32x4, acc[i0 + i][j]);
             }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll 1
+        for (int r = my_row; r < kRows; r += 64 / lanes_a_row) {
+            const int row = r0 + wm + i0 * 16 + r, col = c0 + wn + my_col;
+            float z[8];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const u32x4 v = own[r * kChunks + (my_col / 4 + h ^ r % kChunks)];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    z[4 * h + e] = __uint_as_float(v[e]);
+            }
+            if (row >= a.m || col >= a.n)
+                continue;
+            if (parts > 1)
+                store8<DT_F32>(reinterpret_cast<char *>(partial + ((int64_t)part * a.m + row) * a.n), col, a.n, z);
+            else
+                finish8<DT>(a, row, col, z);
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    }
+}
+
+// The parts' sums in order, then the epilogue. A lane takes eight neighbouring columns.
+template <int DT>
+__global__ __launch_bounds__(256) void linear_join_kernel(Args a, int parts, const float *partial)
+{
+    const int64_t all = (int64_t)a.m * a.n;
+    for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8; i < all; i += (int64_t)gridDim.x * 2048) {
+        float z[8], f[8];
+        widen8<DT_F32>(load8<DT_F32>(reinterpret_cast<const char *>(partial + i), 0, 8), z);
+        for (int p = 1; p < parts; ++p) {
+            widen8<DT_F32>(load8<DT_F32>(reinterpret_cast<const char *>(partial + p * all + i), 0, 8), f);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                z[e] += f[e];
+        }
+        finish8<DT>(a, (int)(i / a.n), (int)(i % a.n), z);
     }
 }
 
 // ---------------------------------------------------------------------------
 // Host
 // ---------------------------------------------------------------------------
+constexpr int kFewRows = 64;
+
 bool good_sizes(int64_t m, int64_t n, int64_t k)
 {
     return m >= 0 && m <= (1 << 24) && n >= 8 && k >= 8 && n <= (1 << 20) && k <= (1 << 20) &&
            n * k <= ((int64_t)1 << 36) && m * n <= ((int64_t)1 << 36) && m * k <= ((int64_t)1 << 36);
 }
 
-template <int DT>
-block_status_t run(const Args &a, hipStream_t st)
+// How a product of more than 64 rows is cut: the tile, and the parts of k.
+struct Plan {
+    int tile;   // 256, 128 or 64, square
+    int parts;
+};
+
+Plan plan(int64_t m, int64_t n, int64_t k)
 {
-    if (a.m <= 64) {
+    auto tiles = [&](int t) { return ceil_div(m, t) * ceil_div(n, t); };
+    const int64_t steps = ceil_div(k, kLineK);
+    int tile = 256;
+    while (tile > 64 && tiles(tile) < 192)
+        tile /= 2;
+    int64_t parts = 1;
+    while (tile == 64 && parts < 16 && tiles(tile) * parts * 2 <= 512 && parts * 16 <= steps)
+        parts *= 2;
+    return {tile, (int)parts};
+}
+
+template <int DT, int T, int WM, int WN>
+block_status_t run_tiles(const Args &a, int parts, float *partial, hipStream_t st)
+{
+    const int tm = (int)ceil_div(a.m, T), tn = (int)ceil_div(a.n, T);
+    const int64_t blocks = ceil_div((int64_t)tm * tn * parts, 8) * 8;
+    return launch(linear_tile_kernel<DT, T, T, WM, WN>, dim3((unsigned)blocks), dim3(WM * WN * 64), 0, st, a, tm, tn,
+                  parts, partial);
+}
+
+template <int DT>
+block_status_t run(const Args &a, float *partial, hipStream_t st)
+{
+    if (a.m <= kFewRows) {
         const dim3 grid((unsigned)ceil_div(a.n, 16));
         if (a.m <= 16)
             return launch(linear_few_kernel<DT, 1, 16>, grid, dim3(1024), 0, st, a);
@@ -178,15 +335,32 @@ block_status_t run(const Args &a, hipStream_t st)
             return launch(linear_few_kernel<DT, 2, 8>, grid, dim3(512), 0, st, a);
         return launch(linear_few_kernel<DT, 4, 8>, grid, dim3(512), 0, st, a);
     }
-    const dim3 grid((unsigned)(ceil_div(a.n, kTile) * ceil_div(a.m, kTile)));
-    return launch(linear_tile_kernel<DT>, grid, dim3(256), 0, st, a);
+    const Plan p = plan(a.m, a.n, a.k);
+    block_status_t s;
+    if (p.tile == 256)
+        s = run_tiles<DT, 256, 2, 4>(a, p.parts, partial, st);
+    else if (p.tile == 128)
+        s = run_tiles<DT, 128, 2, 2>(a, p.parts, partial, st);
+    else
+        s = run_tiles<DT, 64, 2, 2>(a, p.parts, partial, st);
+    if (s || p.parts == 1)
+        return s;
+    const int64_t blocks = ceil_div((int64_t)a.m * a.n, 2048);
+    return launch(linear_join_kernel<DT>, dim3((unsigned)(blocks < 4096 ? blocks : 4096)), dim3(256), 0, st, a, p.parts,
+                  partial);
 }
 
 }  // namespace
 
 extern "C" {
 
-int64_t block_linear_act_workspace(int64_t, int64_t, int64_t) { return 0; }
+int64_t block_linear_act_workspace(int64_t m, int64_t n, int64_t k)
+{
+    if (!good_sizes(m, n, k) || m <= kFewRows)
+        return 0;
+    const Plan p = plan(m, n, k);
+    return p.parts > 1 ? p.parts * m * n * 4 : 0;
+}
 
 block_status_t block_linear_act(const void *x, const void *weight, const void *bias, const void *residual, void *y,
                                 int64_t m, int64_t n, int64_t k, block_act_t act, block_dtype_t dtype, void *workspace,
@@ -212,7 +386,8 @@ block_status_t block_linear_act(const void *x, const void *weight, const void *b
     a.x = static_cast<const uint16_t *>(x), a.w = static_cast<const uint16_t *>(weight);
     a.bias = static_cast<const uint16_t *>(bias), a.residual = static_cast<const uint16_t *>(residual);
     a.y = static_cast<uint16_t *>(y), a.m = (int)m, a.n = (int)n, a.k = (int)k, a.act = act;
-    return dtype == BLOCK_BF16 ? run<DT_BF16>(a, stream) : run<DT_F16>(a, stream);
+    float *partial = static_cast<float *>(workspace);
+    return dtype == BLOCK_BF16 ? run<DT_BF16>(a, partial, stream) : run<DT_F16>(a, partial, stream);
 }
 
 }  // extern "C"
