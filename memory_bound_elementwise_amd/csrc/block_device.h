@@ -118,6 +118,46 @@ __device__ __forceinline__ void store8(char *row, int j, int n, const float (&f)
             store1<DT>(p, i, f[i]);
 }
 
+// The row accesses of a kernel: EVEN (rows of a multiple of eight elements, so 16-byte
+// aligned) through a buffer resource of the row, whose range check masks its end and rows
+// that are not there without a branch; otherwise one element at a time where a group of eight
+// is cut off. Loads stay cached (what was just written is read: 31 us against 34 for the
+// forward pass over 6720 x 7168 bf16), stores go past the caches.
+template <int DT, bool EVEN>
+struct Row {
+    rsrc_t rsrc;
+    char *p;
+    int n;
+    __device__ __forceinline__ Row(const void *base, int64_t row, int cols, bool live)
+        : p(const_cast<char *>(static_cast<const char *>(base)) + (live ? row * cols * kSize<DT> : 0)), n(live ? cols : 0)
+    {
+        if constexpr (EVEN)
+            rsrc = make_rsrc(p, (uint32_t)n * kSize<DT>);
+    }
+    __device__ __forceinline__ Raw8<DT> load(int j) const
+    {
+        if constexpr (EVEN) {
+            Raw8<DT> o;
+#pragma unroll
+            for (int i = 0; i < kSize<DT> / 2; ++i)
+                o.v[i] = __builtin_amdgcn_raw_buffer_load_b128(rsrc, (uint32_t)j * kSize<DT> + 16u * i, 0, 0);
+            return o;
+        }
+        return load8<DT>(p, j, n);
+    }
+    __device__ __forceinline__ void store(int j, const float (&f)[8]) const
+    {
+        if constexpr (EVEN) {
+            const Raw8<DT> o = narrow8<DT>(f);
+#pragma unroll
+            for (int i = 0; i < kSize<DT> / 2; ++i)
+                store_vec(rsrc, o.v[i], (uint32_t)j * kSize<DT> + 16u * i);
+            return;
+        }
+        store8<DT>(p, j, n, f);
+    }
+};
+
 }  // namespace block
 
 #endif  // MBE_BLOCK_DEVICE_H

@@ -84,60 +84,72 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
         return lib
 
 
-def _tensor(t, name, dtypes, shape):
-    """Checks one tensor; returns its address (None for an absent one)."""
+def _tensor(t, name, dtype, shape, dev):
+    """Address of a tensor that is checked against one dtype, shape and device (None for an
+    absent one). The checks are one expression: a decoding step's launches take a few
+    microseconds each, and so would as many separate ones here."""
     if t is None:
         return None
-    if t.dtype not in dtypes:
-        raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+        if t.dtype is not dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        if t.shape != shape:
+            raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        raise ValueError("tensors must live on one device")
     return t.data_ptr()
 
 
-def _device(first, *rest):
-    dev = first.device
-    if dev.type != "cuda":
+def _kind(t, name, dtypes):
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
+    return t.dtype
+
+
+def _call(fn, x, stream, args, workspace=None, need=None):
+    """Runs one C function on the device of x, and on ``stream``; `need` None: it takes no
+    workspace."""
+    if not x.is_cuda:
         raise ValueError("tensors must live on the GPU")
-    for t in rest:
-        if t is not None and t.device != dev:
-            raise ValueError("tensors must live on one device")
-    return dev
-
-
-def _call(fn, dev, stream, args, workspace, need):
-    """Runs one C function on `dev` and `stream`; `need` None: it takes no workspace."""
-    if dev.index != torch.cuda.current_device():
-        with torch.cuda.device(dev):
-            return _call(fn, dev, stream, args, workspace, need)
+    index = x.get_device()
+    if index != torch.cuda.current_device():
+        with torch.cuda.device(index):
+            return _call(fn, x, stream, args, workspace, need)
     if stream is None:
-        handle = torch.cuda.current_stream().cuda_stream
+        handle = _current_stream(index)
     elif isinstance(stream, torch.cuda.Stream):
-        if stream.device != dev:
+        if stream.device.index != index:
             raise ValueError("the stream belongs to another device")
         handle = stream.cuda_stream
     else:
         handle = int(stream)
     if need is not None:
         if workspace is not None:
-            if workspace.dtype != torch.uint8 or not workspace.is_contiguous() or workspace.device != dev:
+            if workspace.dtype != torch.uint8 or not workspace.is_contiguous() or workspace.get_device() != index:
                 raise ValueError("workspace must be a contiguous uint8 tensor on the tensors' device")
             if workspace.numel() < need:
                 raise ValueError(f"workspace must hold at least {need} bytes, got {workspace.numel()}")
         elif need > 0:
             if stream is None:
-                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+                workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
             else:
-                own = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(handle, device=dev)
+                own = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(handle, device=index)
                 with torch.cuda.stream(own):
-                    workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+                    workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
         args += (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
-    lib = load_library()
+    lib = _lib or load_library()
     st = getattr(lib, fn)(*args, handle)
     if st:
         raise MoeBlockError(fn, st, lib.moe_block_last_hip_error())
+
+
+def _current_stream(index):
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+if hasattr(torch._C, "_cuda_getCurrentRawStream"):  # the same handle without a Stream object
+    _current_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _rows(x, name):
@@ -147,9 +159,8 @@ def _rows(x, name):
 
 
 _ANY = tuple(_TORCH)
-_BF16 = (torch.bfloat16,)
-_F32 = (torch.float32,)
-_I32 = (torch.int32,)
+_HALF = (torch.bfloat16, torch.float16)
+_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
 
 
 # ---------------------------------------------------------------------------
@@ -160,23 +171,22 @@ def layer_norm_fwd(x, weight, bias, y, mean=None, rstd=None, *, eps=1e-5, stream
     fp32 with one rounding. ``weight`` and ``bias``: [cols] of x's dtype or fp32 (one dtype for
     both), or None. ``mean`` and ``rstd`` (fp32 [rows], both or neither) take the statistics
     that the backward needs."""
-    rows, cols = _rows(x, "x")
+    shape = rows, cols = _rows(x, "x")
+    dev, kind = x.get_device(), _kind(x, "x", _ANY)
     first = weight if weight is not None else bias
-    wd = (x.dtype, torch.float32) if first is None else (first.dtype,)
-    if first is not None and first.dtype not in (x.dtype, torch.float32):
-        raise TypeError(f"weight and bias must be {x.dtype} or fp32, got {first.dtype}")
-    args = (_tensor(x, "x", _ANY, x.shape), _tensor(weight, "weight", wd, (cols,)), _tensor(bias, "bias", wd, (cols,)),
-            _tensor(y, "y", (x.dtype,), x.shape), _tensor(mean, "mean", _F32, (rows,)),
-            _tensor(rstd, "rstd", _F32, (rows,)), rows, cols, float(eps), _TORCH[x.dtype],
-            _TORCH[wd[0]])
+    wkind = kind if first is None else _kind(first, "weight and bias", (kind, _F32))
     if (mean is None) != (rstd is None):
         raise ValueError("mean and rstd go together")
-    _call("block_layer_norm_fwd", _device(x, weight, bias, y, mean, rstd), stream, args, None, None)
+    _call("block_layer_norm_fwd", x, stream,
+          (_tensor(x, "x", kind, shape, dev), _tensor(weight, "weight", wkind, (cols,), dev),
+           _tensor(bias, "bias", wkind, (cols,), dev), _tensor(y, "y", kind, shape, dev),
+           _tensor(mean, "mean", _F32, (rows,), dev), _tensor(rstd, "rstd", _F32, (rows,), dev), rows, cols, eps,
+           _TORCH[kind], _TORCH[wkind]))
     return y
 
 
 def layer_norm_bwd_workspace(rows: int, cols: int) -> int:
-    return load_library().block_layer_norm_bwd_workspace(rows, cols)
+    return (_lib or load_library()).block_layer_norm_bwd_workspace(rows, cols)
 
 
 def layer_norm_bwd(grad_y, x, weight, mean, rstd, grad_x, grad_weight=None, grad_bias=None, *, workspace=None,
@@ -184,19 +194,18 @@ def layer_norm_bwd(grad_y, x, weight, mean, rstd, grad_x, grad_weight=None, grad
     """Gradients of ``layer_norm_fwd``: grad_x in x's dtype, grad_weight and grad_bias in the
     weight's (the same bits on every call); any of the three may be None. With ``weight`` None
     (a norm without scale) grad_weight and grad_bias are x's dtype or fp32."""
-    rows, cols = _rows(x, "x")
-    first = next((t for t in (weight, grad_weight, grad_bias) if t is not None), None)
-    wd = (x.dtype,) if first is None else (first.dtype,)
-    if wd[0] not in (x.dtype, torch.float32):
-        raise TypeError(f"weight must be {x.dtype} or fp32, got {wd[0]}")
-    args = (_tensor(grad_y, "grad_y", (x.dtype,), x.shape), _tensor(x, "x", _ANY, x.shape),
-            _tensor(weight, "weight", wd, (cols,)), _tensor(mean, "mean", _F32, (rows,)),
-            _tensor(rstd, "rstd", _F32, (rows,)), _tensor(grad_x, "grad_x", (x.dtype,), x.shape),
-            _tensor(grad_weight, "grad_weight", wd, (cols,)), _tensor(grad_bias, "grad_bias", wd, (cols,)),
-            rows, cols, _TORCH[x.dtype], _TORCH[wd[0]])
-    dev = _device(x, grad_y, weight, mean, rstd, grad_x, grad_weight, grad_bias)
+    shape = rows, cols = _rows(x, "x")
+    dev, kind = x.get_device(), _kind(x, "x", _ANY)
+    first = weight if weight is not None else grad_weight if grad_weight is not None else grad_bias
+    wkind = kind if first is None else _kind(first, "weight", (kind, _F32))
+    vec, st = (cols,), (rows,)
+    args = (_tensor(grad_y, "grad_y", kind, shape, dev), _tensor(x, "x", kind, shape, dev),
+            _tensor(weight, "weight", wkind, vec, dev), _tensor(mean, "mean", _F32, st, dev),
+            _tensor(rstd, "rstd", _F32, st, dev), _tensor(grad_x, "grad_x", kind, shape, dev),
+            _tensor(grad_weight, "grad_weight", wkind, vec, dev), _tensor(grad_bias, "grad_bias", wkind, vec, dev),
+            rows, cols, _TORCH[kind], _TORCH[wkind])
     need = layer_norm_bwd_workspace(rows, cols) if grad_weight is not None or grad_bias is not None else 0
-    _call("block_layer_norm_bwd", dev, stream, args, workspace, need)
+    _call("block_layer_norm_bwd", x, stream, args, workspace, need)
     return grad_x, grad_weight, grad_bias
 
 
@@ -229,7 +238,7 @@ class LayerNorm(torch.autograd.Function):
 # Matrix product with an epilogue
 # ---------------------------------------------------------------------------
 def linear_act_workspace(m: int, n: int, k: int) -> int:
-    return load_library().block_linear_act_workspace(m, n, k)
+    return (_lib or load_library()).block_linear_act_workspace(m, n, k)
 
 
 def linear_act(x, weight, y, *, bias=None, activation=None, residual=None, workspace=None, stream=None):
@@ -242,12 +251,11 @@ def linear_act(x, weight, y, *, bias=None, activation=None, residual=None, works
     if activation not in ACTIVATIONS:
         raise ValueError(f"unknown activation {activation!r}")
     _forward_only("linear_act", x, weight, bias, residual)
-    same = (x.dtype,)
-    args = (_tensor(x, "x", (torch.bfloat16, torch.float16), x.shape), _tensor(weight, "weight", same, (n, k)),
-            _tensor(bias, "bias", same, (n,)), _tensor(residual, "residual", same, (m, n)),
-            _tensor(y, "y", same, (m, n)), m, n, k, ACTIVATIONS[activation], _TORCH[x.dtype])
-    _call("block_linear_act", _device(x, weight, bias, residual, y), stream, args, workspace,
-          linear_act_workspace(m, n, k))
+    dev, kind = x.get_device(), _kind(x, "x", _HALF)
+    args = (_tensor(x, "x", kind, (m, k), dev), _tensor(weight, "weight", kind, (n, k), dev),
+            _tensor(bias, "bias", kind, (n,), dev), _tensor(residual, "residual", kind, (m, n), dev),
+            _tensor(y, "y", kind, (m, n), dev), m, n, k, ACTIVATIONS[activation], _TORCH[kind])
+    _call("block_linear_act", x, stream, args, workspace, linear_act_workspace(m, n, k))
     return y
 
 
@@ -260,19 +268,19 @@ def _forward_only(name, *tensors):
 # Router and experts
 # ---------------------------------------------------------------------------
 def moe_route_workspace(tokens: int, hidden: int, experts: int) -> int:
-    return load_library().block_moe_route_workspace(tokens, hidden, experts)
+    return (_lib or load_library()).block_moe_route_workspace(tokens, hidden, experts)
 
 
 def moe_experts_workspace(tokens: int, hidden: int, inter: int, experts: int, top_k: int) -> int:
-    return load_library().block_moe_experts_workspace(tokens, hidden, inter, experts, top_k)
+    return (_lib or load_library()).block_moe_experts_workspace(tokens, hidden, inter, experts, top_k)
 
 
 def moe_layer_workspace(tokens: int, hidden: int, inter: int, experts: int, top_k: int) -> int:
-    return load_library().block_moe_layer_workspace(tokens, hidden, inter, experts, top_k)
+    return (_lib or load_library()).block_moe_layer_workspace(tokens, hidden, inter, experts, top_k)
 
 
-def _scalar(valid_tokens):
-    return None if valid_tokens is None else _tensor(valid_tokens.reshape(-1), "valid_tokens", _I32, (1,))
+def _scalar(valid_tokens, dev):
+    return None if valid_tokens is None else _tensor(valid_tokens.reshape(-1), "valid_tokens", _I32, (1,), dev)
 
 
 def moe_route(x, router_weight, ids, probs, *, renormalize=False, valid_tokens=None, workspace=None, stream=None):
@@ -285,17 +293,16 @@ def moe_route(x, router_weight, ids, probs, *, renormalize=False, valid_tokens=N
     experts = _rows(router_weight, "router_weight")[0]
     top_k = _rows(ids, "ids")[1]
     _forward_only("moe_route", x, router_weight)
-    args = (_tensor(x, "x", _BF16, x.shape),
-            _tensor(router_weight, "router_weight", (torch.bfloat16, torch.float32), (experts, hidden)),
-            _TORCH[router_weight.dtype], _tensor(ids, "ids", _I32, (tokens, top_k)),
-            _tensor(probs, "probs", _F32, (tokens, top_k)), tokens, hidden, experts, top_k, int(bool(renormalize)),
-            _scalar(valid_tokens))
-    _call("block_moe_route", _device(x, router_weight, ids, probs, valid_tokens), stream, args, workspace,
-          moe_route_workspace(tokens, hidden, experts))
+    dev, rkind = x.get_device(), _kind(router_weight, "router_weight", (_BF16, _F32))
+    args = (_tensor(x, "x", _BF16, (tokens, hidden), dev),
+            _tensor(router_weight, "router_weight", rkind, (experts, hidden), dev), _TORCH[rkind],
+            _tensor(ids, "ids", _I32, (tokens, top_k), dev), _tensor(probs, "probs", _F32, (tokens, top_k), dev),
+            tokens, hidden, experts, top_k, bool(renormalize), _scalar(valid_tokens, dev))
+    _call("block_moe_route", x, stream, args, workspace, moe_route_workspace(tokens, hidden, experts))
     return ids, probs
 
 
-def _expert_shapes(x, w_up, w_down, activation, limit):
+def _expert_args(x, w_up, w_down, activation, limit, dev):
     tokens, hidden = _rows(x, "x")
     if activation not in EXPERT_ACTIVATIONS:
         raise ValueError(f"unknown expert activation {activation!r}")
@@ -305,9 +312,9 @@ def _expert_shapes(x, w_up, w_down, activation, limit):
     ups = 2 * inter if activation == "swiglu" else inter
     if activation == "swiglu" and not limit > 0:
         raise ValueError("limit must be positive (inf for none)")
-    return (tokens, hidden, inter, experts, _tensor(x, "x", _BF16, x.shape),
-            _tensor(w_up, "w_up", _BF16, (experts, ups, hidden)),
-            _tensor(w_down, "w_down", _BF16, (experts, hidden, inter)))
+    return (tokens, hidden, inter, experts, _tensor(x, "x", _BF16, (tokens, hidden), dev),
+            _tensor(w_up, "w_up", _BF16, (experts, ups, hidden), dev),
+            _tensor(w_down, "w_down", _BF16, (experts, hidden, inter), dev))
 
 
 def moe_experts(x, w_up, w_down, ids, probs, y, *, activation="swiglu", limit=math.inf, residual=None,
@@ -318,30 +325,32 @@ def moe_experts(x, w_up, w_down, ids, probs, y, *, activation="swiglu", limit=ma
     at ``limit``) or "squared_relu" (w_up [experts, inter, hidden]). An id outside the experts
     contributes nothing. x, weights and residual bf16; y bf16 or fp32; rows of y at or past
     ``valid_tokens`` are left as they were."""
-    tokens, hidden, inter, experts, px, pu, pd = _expert_shapes(x, w_up, w_down, activation, limit)
+    dev = x.get_device()
+    tokens, hidden, inter, experts, px, pu, pd = _expert_args(x, w_up, w_down, activation, limit, dev)
     top_k = _rows(ids, "ids")[1]
     _forward_only("moe_experts", x, w_up, w_down, probs, residual)
-    args = (px, pu, pd, _tensor(ids, "ids", _I32, (tokens, top_k)), _tensor(probs, "probs", _F32, (tokens, top_k)),
-            _tensor(residual, "residual", _BF16, x.shape), _tensor(y, "y", (torch.bfloat16, torch.float32), x.shape),
-            _TORCH[y.dtype], tokens, hidden, inter, experts, top_k, EXPERT_ACTIVATIONS[activation], float(limit),
-            _scalar(valid_tokens))
-    _call("block_moe_experts", _device(x, w_up, w_down, ids, probs, residual, y, valid_tokens), stream, args,
-          workspace, moe_experts_workspace(tokens, hidden, inter, experts, top_k))
+    ykind = _kind(y, "y", (_BF16, _F32))
+    args = (px, pu, pd, _tensor(ids, "ids", _I32, (tokens, top_k), dev),
+            _tensor(probs, "probs", _F32, (tokens, top_k), dev),
+            _tensor(residual, "residual", _BF16, (tokens, hidden), dev), _tensor(y, "y", ykind, (tokens, hidden), dev),
+            _TORCH[ykind], tokens, hidden, inter, experts, top_k, EXPERT_ACTIVATIONS[activation], limit,
+            _scalar(valid_tokens, dev))
+    _call("block_moe_experts", x, stream, args, workspace, moe_experts_workspace(tokens, hidden, inter, experts, top_k))
     return y
 
 
 def moe_layer(x, router_weight, w_up, w_down, y, ids, probs, *, activation="swiglu", limit=math.inf,
               renormalize=False, residual=None, valid_tokens=None, workspace=None, stream=None):
     """``moe_route`` into ids and probs, then ``moe_experts`` with them into y, in one call."""
-    tokens, hidden, inter, experts, px, pu, pd = _expert_shapes(x, w_up, w_down, activation, limit)
+    dev = x.get_device()
+    tokens, hidden, inter, experts, px, pu, pd = _expert_args(x, w_up, w_down, activation, limit, dev)
     top_k = _rows(ids, "ids")[1]
     _forward_only("moe_layer", x, router_weight, w_up, w_down, residual)
-    args = (px, _tensor(router_weight, "router_weight", (torch.bfloat16, torch.float32), (experts, hidden)),
-            _TORCH[router_weight.dtype], pu, pd, _tensor(residual, "residual", _BF16, x.shape),
-            _tensor(y, "y", (torch.bfloat16, torch.float32), x.shape), _TORCH[y.dtype],
-            _tensor(ids, "ids", _I32, (tokens, top_k)), _tensor(probs, "probs", _F32, (tokens, top_k)),
-            tokens, hidden, inter, experts, top_k, int(bool(renormalize)), EXPERT_ACTIVATIONS[activation],
-            float(limit), _scalar(valid_tokens))
-    _call("block_moe_layer", _device(x, router_weight, w_up, w_down, residual, y, ids, probs, valid_tokens), stream,
-          args, workspace, moe_layer_workspace(tokens, hidden, inter, experts, top_k))
+    rkind, ykind = _kind(router_weight, "router_weight", (_BF16, _F32)), _kind(y, "y", (_BF16, _F32))
+    args = (px, _tensor(router_weight, "router_weight", rkind, (experts, hidden), dev), _TORCH[rkind], pu, pd,
+            _tensor(residual, "residual", _BF16, (tokens, hidden), dev), _tensor(y, "y", ykind, (tokens, hidden), dev),
+            _TORCH[ykind], _tensor(ids, "ids", _I32, (tokens, top_k), dev),
+            _tensor(probs, "probs", _F32, (tokens, top_k), dev), tokens, hidden, inter, experts, top_k,
+            bool(renormalize), EXPERT_ACTIVATIONS[activation], limit, _scalar(valid_tokens, dev))
+    _call("block_moe_layer", x, stream, args, workspace, moe_layer_workspace(tokens, hidden, inter, experts, top_k))
     return y
