@@ -156,6 +156,40 @@ __global__ __launch_bounds__(kMaxExperts) void route_choose_kernel(const double 
     }
 }
 
+// The same choice by one wave for a token of up to 64 experts (the same bits): lane = expert,
+// keys: 64 of the wave's own. Slots beyond top_k lanes are not written.
+__device__ __forceinline__ void choose_in_wave(const double *partial, int t, int tokens, int experts, int parts,
+                                               int top_k, int renormalize, uint64_t *keys, int *ids, float *probs)
+{
+    const int e = lane_id();
+    const double *mine = partial + (int64_t)t * experts + (e < experts ? e : 0);
+    const int64_t part = (int64_t)tokens * experts;
+    double v = 0.0;
+#pragma unroll 8
+    for (int s = 0; s < parts; ++s)
+        v += mine[s * part];
+    const uint64_t key = order_key(v);
+    keys[e] = key;
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    int rank = 0;
+#pragma unroll 8
+    for (int j = 0; j < experts; ++j)
+        rank += keys[j] > key || (keys[j] == key && j < e);
+    if (e >= experts)
+        rank = experts;
+    const int first = __builtin_ctzll(__ballot(rank == 0));
+    const uint64_t bits = __builtin_bit_cast(uint64_t, v);
+    const unsigned lo = __builtin_amdgcn_readlane((int)(unsigned)bits, first);
+    const unsigned hi = __builtin_amdgcn_readlane((int)(unsigned)(bits >> 32), first);
+    const double top = __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+    const float w = e < experts ? expf((float)(v - top)) : 0.0f;
+    const float sum = wave_sum(renormalize && rank >= top_k ? 0.0f : w);
+    if (rank < top_k) {
+        ids[t * top_k + rank] = e;
+        probs[t * top_k + rank] = w / sum;
+    }
+}
+
 // ---------------------------------------------------------------------------
 // Experts
 // ---------------------------------------------------------------------------
@@ -206,12 +240,25 @@ struct UpArgs {
     const int *valid;
     int tokens, hidden, inter, experts, top_k, by_pair;
     float limit;
+    // set where the choice of experts is made here (by every workgroup for itself; the first
+    // one writes it out): the router's partial logits
+    const double *partial;
+    int parts, renormalize;
+    int *ids_out;
+    float *probs_out;
 };
+
+// The choice is made in the up kernel for up to this many tokens (one a wave) and experts
+// (one a lane), and workgroups of that kernel: each of them then takes about 1.5 us longer,
+// against a kernel of its own of 2 to 3.6 us and its launch. (Where the workgroups come in
+// several rounds they pay it in each: one token of 7168 x 2048, 1024 workgroups, +4.2 us.)
+constexpr int kChooseTokens = 4, kChooseExperts = 64, kChooseGroups = 512;
 
 constexpr int kUpWaves = 4;
 
 template <int ACT, int G>
-__device__ __forceinline__ void up_pass(const UpArgs &a, int e, int i0, const uint16_t *list, int n, u32x4 *shared)
+__device__ __forceinline__ void up_pass(const UpArgs &a, const float *probs, int e, int i0, const uint16_t *list, int n,
+                                        u32x4 *shared)
 {
     constexpr int RT = ACT == ACT_SWIGLU ? 2 : 1;  // gate and up, or the one product
     constexpr int DEPTH = G == 1 ? 3 : 2;
@@ -258,7 +305,7 @@ __device__ __forceinline__ void up_pass(const UpArgs &a, int e, int i0, const ui
         const int s = g * 16 + lane % 16;
         if (s < n && i < a.inter) {
             const int pair = list[s];
-            const float v = (ACT == ACT_SWIGLU ? swiglu(z[0], z[RT - 1], a.limit) : squared_relu(z[0])) * a.probs[pair];
+            const float v = (ACT == ACT_SWIGLU ? swiglu(z[0], z[RT - 1], a.limit) : squared_relu(z[0])) * probs[pair];
             uint16_t hi, lo;
             split_bf16(v, hi, lo);
             uint16_t *at = a.h + h_at(pair, a.inter, i);
@@ -272,24 +319,42 @@ __device__ __forceinline__ void up_pass(const UpArgs &a, int e, int i0, const ui
 // blockIdx.y: a pair (by_pair: it stands for its expert if no earlier pair has the same), or
 // an expert, whichever is fewer. G: groups of 16 tokens that share one read of the weights;
 // an expert with more tokens reads them again.
-template <int ACT, int G>
+template <int ACT, int G, bool CHOOSE>
 __global__ __launch_bounds__(kUpWaves * 64) void moe_up_kernel(UpArgs a)
 {
     constexpr int RT = ACT == ACT_SWIGLU ? 2 : 1;
     __shared__ u32x4 shared[kUpWaves * kStage<RT, G>];  // the waves' stages, then their sums
     __shared__ uint16_t list[kMaxPairs];
     __shared__ int count;
-    const int pairs = live_tokens(a.valid, a.tokens) * a.top_k;
+    const int live = live_tokens(a.valid, a.tokens), pairs = live * a.top_k;
+    const int *ids = a.ids;
+    const float *probs = a.probs;
+    if constexpr (CHOOSE) {
+        __shared__ uint64_t keys[kChooseTokens][64];
+        __shared__ int chosen[kChooseTokens * 64];
+        __shared__ float weights[kChooseTokens * 64];
+        static_assert(kChooseTokens == kUpWaves, "a token a wave");
+        const int t = wave_in_block();
+        if (t < live)
+            choose_in_wave(a.partial, t, a.tokens, a.experts, a.parts, a.top_k, a.renormalize, keys[t], chosen, weights);
+        __syncthreads();
+        if (blockIdx.x == 0 && blockIdx.y == 0 && (int)threadIdx.x < pairs) {
+            a.ids_out[threadIdx.x] = chosen[threadIdx.x];
+            a.probs_out[threadIdx.x] = weights[threadIdx.x];
+        }
+        ids = chosen;
+        probs = weights;
+    }
     int e = blockIdx.y;
     if (a.by_pair) {
         if (e >= pairs)
             return;
-        e = a.ids[e];
+        e = ids[e];
         if (e < 0 || e >= a.experts)
             return;
     }
     if (wave_in_block() == 0) {
-        const int n = list_pairs(a.ids, pairs, e, list);
+        const int n = list_pairs(ids, pairs, e, list);
         if (lane_id() == 0)
             count = n;
     }
@@ -301,11 +366,11 @@ __global__ __launch_bounds__(kUpWaves * 64) void moe_up_kernel(UpArgs a)
     for (int p = 0; p < n; p += G * 16) {
         const int m = n - p < G * 16 ? n - p : G * 16;
         if (G == 1 || m <= 16)
-            up_pass<ACT, 1>(a, e, i0, list + p, m, shared);
+            up_pass<ACT, 1>(a, probs, e, i0, list + p, m, shared);
         else if (G == 2 || m <= 32)
-            up_pass<ACT, G < 2 ? 1 : 2>(a, e, i0, list + p, m, shared);
+            up_pass<ACT, G < 2 ? 1 : 2>(a, probs, e, i0, list + p, m, shared);
         else
-            up_pass<ACT, G>(a, e, i0, list + p, m, shared);
+            up_pass<ACT, G>(a, probs, e, i0, list + p, m, shared);
     }
 }
 
@@ -634,25 +699,29 @@ int64_t route_bytes(const RouteSizes &s)
     return s.tokens > 0 ? round_up(route_parts(s) * s.tokens * s.experts * 8, 16) : 0;
 }
 
-block_status_t route(const uint16_t *x, const void *router, block_dtype_t rdt, int *ids, float *probs,
-                     const RouteSizes &s, int top_k, int renormalize, const int *valid, void *ws, hipStream_t st)
+block_status_t route_logits(const uint16_t *x, const void *router, block_dtype_t rdt, const RouteSizes &s,
+                            const int *valid, void *ws, hipStream_t st)
 {
     double *partial = static_cast<double *>(ws);
     const char *xc = reinterpret_cast<const char *>(x), *rc = static_cast<const char *>(router);
     const dim3 grid((unsigned)ceil_div(s.experts, kRouteTile), (unsigned)ceil_div(s.tokens, kRouteTile),
                     (unsigned)route_parts(s)),
         threads(kRouteWaves * 64);
-    block_status_t r;
     if (rdt == BLOCK_FP32)
-        r = launch(route_logits_kernel<DT_F32>, grid, threads, 0, st, xc, rc, partial, (int)s.tokens, (int)s.hidden,
-                   s.experts, route_part(s), valid);
-    else
-        r = launch(route_logits_kernel<DT_BF16>, grid, threads, 0, st, xc, rc, partial, (int)s.tokens, (int)s.hidden,
-                   s.experts, route_part(s), valid);
-    if (r)
+        return launch(route_logits_kernel<DT_F32>, grid, threads, 0, st, xc, rc, partial, (int)s.tokens, (int)s.hidden,
+                      s.experts, route_part(s), valid);
+    return launch(route_logits_kernel<DT_BF16>, grid, threads, 0, st, xc, rc, partial, (int)s.tokens, (int)s.hidden,
+                  s.experts, route_part(s), valid);
+}
+
+block_status_t route(const uint16_t *x, const void *router, block_dtype_t rdt, int *ids, float *probs,
+                     const RouteSizes &s, int top_k, int renormalize, const int *valid, void *ws, hipStream_t st)
+{
+    if (const block_status_t r = route_logits(x, router, rdt, s, valid, ws, st))
         return r;
     return launch(route_choose_kernel, dim3((unsigned)s.tokens), dim3((unsigned)round_up(s.experts, 64)), 0, st,
-                  partial, ids, probs, (int)s.tokens, s.experts, (int)route_parts(s), top_k, renormalize, valid);
+                  static_cast<const double *>(ws), ids, probs, (int)s.tokens, s.experts, (int)route_parts(s), top_k,
+                  renormalize, valid);
 }
 
 struct ExpertSizes {
@@ -726,11 +795,14 @@ int token_groups(const ExpertSizes &s, int group)
 template <int ACT>
 block_status_t launch_up(const UpArgs &u, int groups, dim3 grid, hipStream_t st)
 {
+    const dim3 threads(kUpWaves * 64);
+    if (u.partial)
+        return launch(moe_up_kernel<ACT, 1, true>, grid, threads, 0, st, u);
     if (groups == 1)
-        return launch(moe_up_kernel<ACT, 1>, grid, dim3(kUpWaves * 64), 0, st, u);
+        return launch(moe_up_kernel<ACT, 1, false>, grid, threads, 0, st, u);
     if (groups == 2)
-        return launch(moe_up_kernel<ACT, 2>, grid, dim3(kUpWaves * 64), 0, st, u);
-    return launch(moe_up_kernel<ACT, 4>, grid, dim3(kUpWaves * 64), 0, st, u);
+        return launch(moe_up_kernel<ACT, 2, false>, grid, threads, 0, st, u);
+    return launch(moe_up_kernel<ACT, 4, false>, grid, threads, 0, st, u);
 }
 
 template <int YDT>
@@ -760,11 +832,23 @@ block_status_t launch_down_many(const DownArgs &d, int groups, int shares, dim3 
                   st, d, partial, shares);
 }
 
+// A choice of experts still to be made, in the up kernel.
+struct Choice {
+    const double *partial;
+    int parts, renormalize;
+    int *ids;
+    float *probs;
+};
+
 block_status_t experts(const uint16_t *x, const uint16_t *w_up, const uint16_t *w_down, const int *ids,
-                       const float *probs, const uint16_t *residual, void *y, block_dtype_t ydt, const ExpertSizes &s,
-                       block_act_t act, float limit, const int *valid, void *ws, hipStream_t st)
+                       const float *probs, const Choice *choice, const uint16_t *residual, void *y, block_dtype_t ydt,
+                       const ExpertSizes &s, block_act_t act, float limit, const int *valid, void *ws, hipStream_t st)
 {
     UpArgs u = {};
+    if (choice) {
+        u.partial = choice->partial, u.parts = choice->parts, u.renormalize = choice->renormalize;
+        u.ids_out = choice->ids, u.probs_out = choice->probs;
+    }
     u.x = x, u.w = w_up, u.ids = ids, u.probs = probs, u.h = static_cast<uint16_t *>(ws), u.valid = valid;
     u.tokens = (int)s.tokens, u.hidden = (int)s.hidden, u.inter = (int)s.inter, u.experts = s.experts;
     u.top_k = s.top_k, u.limit = limit;
@@ -867,7 +951,8 @@ block_status_t block_moe_experts(const uint16_t *x, const uint16_t *w_up, const 
                            {residual, n * 2},
                            {valid_tokens, 4}}))
         return BLOCK_ERR_INVALID_ARG;
-    return experts(x, w_up, w_down, ids, probs, residual, y, y_dtype, s, act, limit, valid_tokens, workspace, stream);
+    return experts(x, w_up, w_down, ids, probs, nullptr, residual, y, y_dtype, s, act, limit, valid_tokens, workspace,
+                   stream);
 }
 
 int64_t block_moe_layer_workspace(int64_t tokens, int64_t hidden, int64_t inter, int n_experts, int top_k)
@@ -910,11 +995,20 @@ block_status_t block_moe_layer(const uint16_t *x, const void *router_weight, blo
                            {residual, n * 2},
                            {valid_tokens, 4}}))
         return BLOCK_ERR_INVALID_ARG;
+    void *space = static_cast<char *>(workspace) + route_need;
+    const int64_t pairs = tokens * top_k;
+    if (tokens <= kChooseTokens && n_experts <= kChooseExperts &&
+        ceil_div(inter, 16) * (pairs < n_experts ? pairs : n_experts) <= kChooseGroups) {
+        if (const block_status_t r = route_logits(x, router_weight, router_dtype, rs, valid_tokens, workspace, stream))
+            return r;
+        const Choice c = {static_cast<const double *>(workspace), (int)route_parts(rs), renormalize, ids, probs};
+        return experts(x, w_up, w_down, ids, probs, &c, residual, y, y_dtype, s, act, limit, valid_tokens, space, stream);
+    }
     if (const block_status_t r = route(x, router_weight, router_dtype, ids, probs, rs, top_k, renormalize,
                                        valid_tokens, workspace, stream))
         return r;
-    return experts(x, w_up, w_down, ids, probs, residual, y, y_dtype, s, act, limit, valid_tokens,
-                   static_cast<char *>(workspace) + route_need, stream);
+    return experts(x, w_up, w_down, ids, probs, nullptr, residual, y, y_dtype, s, act, limit, valid_tokens, space,
+                   stream);
 }
 
 }  // extern "C"
