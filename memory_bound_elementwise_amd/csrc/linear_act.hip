@@ -1,7 +1,7 @@
 // y = act(x W^T + bias) + residual, for AMD Instinct MI355X (gfx950). C ABI declared in
 // block/moe_block.h.
 //
-// Two shapes of the same product. Up to 64 rows of x it is a stream of W: a workgroup takes
+// Two shapes of the same product. Up to 32 rows of x it is a stream of W: a workgroup takes
 // 16 rows of W, its waves split k, and their sums meet in LDS. More rows are tiled for the
 // matrix cores with both operands staged through LDS. Bias, activation and residual are
 // applied to the fp32 sums in registers, and each output is rounded once.
@@ -69,7 +69,7 @@ __global__ __launch_bounds__(WAVES * 64) void linear_few_kernel(Args a)
     __shared__ u32x4 shared[WAVES * kStage<1, G>];
     const int lane = lane_id(), wave = wave_in_block();
     const int c0 = blockIdx.x * 16;
-    constexpr int DEPTH = G == 4 ? 2 : 3;
+    constexpr int DEPTH = G == 2 ? 3 : 2;
     const int there = a.n - c0 < 16 ? a.n - c0 : 16;
     const uint32_t row_bytes = (uint32_t)a.k * 2u;
     const rsrc_t w[1] = {make_rsrc(a.w + (int64_t)c0 * a.k, (uint32_t)there * row_bytes)};
@@ -109,6 +109,15 @@ __global__ __launch_bounds__(WAVES * 64) void linear_few_kernel(Args a)
 // ---------------------------------------------------------------------------
 typedef __attribute__((address_space(3))) void shared_void;
 
+// The largest divisor of n up to most.
+constexpr int most_dividing(int n, int most)
+{
+    int d = most < n ? most : n;
+    while (n % d)
+        --d;
+    return d;
+}
+
 // Waits for the wave's loads into shared memory and its reads of it, then for the workgroup.
 // (Loads into shared memory count as loads from memory: a fence need not wait for them.)
 // Nothing is moved across.
@@ -137,8 +146,9 @@ __global__ __launch_bounds__(WM * WN * 64) void linear_tile_kernel(Args a, int t
                                                                    float *partial)
 {
     constexpr int W = WM * WN, FM = TM / WM / 16, FN = TN / WN / 16;
-    constexpr int kGroups = (TM + TN) / 8 / W;  // loads of a wave a step, of 8 rows each
-    static_assert((TM + TN) % (8 * W) == 0 && TM % (8 * kGroups) == 0, "");
+    // half of the waves load x, half W: loads of a wave a step, of 8 rows each
+    constexpr int kLoadsX = TM / 8 / (W / 2), kLoadsW = TN / 8 / (W / 2);
+    static_assert(TM % (4 * W) == 0 && TN % (4 * W) == 0 && kLoadsX <= kLoadsW, "");
     constexpr int kBuffer = (TM + TN) * 8;  // 16-byte chunks
     // one object each: the compiler then knows that a load into one does not touch the other
     __shared__ u32x4 s0[kBuffer], s1[kBuffer];
@@ -159,8 +169,9 @@ __global__ __launch_bounds__(WM * WN * 64) void linear_tile_kernel(Args a, int t
     const uint32_t row_bytes = (uint32_t)a.k * 2u;
     const int rows = a.m - r0 < TM ? a.m - r0 : TM, cols = a.n - c0 < TN ? a.n - c0 : TN;
     // a wave loads rows of x or rows of W (rows past the end read zeros)
-    const int chunk = lane % 8 ^ lane / 8, group0 = wave * kGroups;
-    const bool loads_x = group0 * 8 < TM;
+    const bool loads_x = wave < W / 2;
+    const int chunk = lane % 8 ^ lane / 8;
+    const int group0 = loads_x ? wave * kLoadsX : TM / 8 + (wave - W / 2) * kLoadsW;
     const rsrc_t from = make_rsrc(loads_x ? a.x + (int64_t)r0 * a.k : a.w + (int64_t)c0 * a.k,
                                   (uint32_t)(loads_x ? rows : cols) * row_bytes);
     const uint32_t base = (uint32_t)((group0 - (loads_x ? 0 : TM / 8)) * 8 + lane / 8) * row_bytes + chunk * 16;
@@ -171,9 +182,11 @@ __global__ __launch_bounds__(WM * WN * 64) void linear_tile_kernel(Args a, int t
         const int k = step * kLineK;
         const bool in = step < last && k + chunk * 8 < a.k;  // past the last step: zeros
 #pragma unroll
-        for (int g = 0; g < kGroups; ++g)
+        for (int i = 0; i < kLoadsW; ++i) {
+            const int g = i < kLoadsX || !loads_x ? i : kLoadsX - 1;  // rather twice than a branch
             __builtin_amdgcn_raw_ptr_buffer_load_lds(from, (shared_void *)(to + (group0 + g) * 64), 16,
                                                      in ? base + (uint32_t)g * 8u * row_bytes : kNowhere, k * 2, 0, 0);
+        }
         __builtin_amdgcn_sched_barrier(0);
     };
     f32x4 acc[FM][FN];
@@ -232,7 +245,7 @@ __global__ __launch_bounds__(WM * WN * 64) void linear_tile_kernel(Args a, int t
     // acc[i][j][e] is row wm + 16 i + lane % 16, column wn + 16 j + 4 (lane / 16) + e. Through
     // shared memory, kRows rows at a time, into rows of eight columns a lane.
     constexpr int kCols = FN * 16, kChunks = kCols / 4, kOwn = kBuffer * 2 / W;  // 16-byte chunks of a wave
-    constexpr int kFit = kOwn / kChunks, kRows = kFit < FM * 16 ? kFit : FM * 16;
+    constexpr int kRows = 16 * most_dividing(FM, kOwn / kChunks / 16);
     u32x4 *const own = wave < W / 2 ? s0 + wave * kOwn : s1 + (wave - W / 2) * kOwn;
     const int lanes_a_row = kCols / 8, my_row = lane / lanes_a_row, my_col = lane % lanes_a_row * 8;
 #pragma unroll
@@ -288,7 +301,7 @@ __global__ __launch_bounds__(256) void linear_join_kernel(Args a, int parts, con
 // ---------------------------------------------------------------------------
 // Host
 // ---------------------------------------------------------------------------
-constexpr int kFewRows = 64;
+constexpr int kFewRows = 32;
 
 bool good_sizes(int64_t m, int64_t n, int64_t k)
 {
@@ -296,31 +309,42 @@ bool good_sizes(int64_t m, int64_t n, int64_t k)
            n * k <= ((int64_t)1 << 36) && m * n <= ((int64_t)1 << 36) && m * k <= ((int64_t)1 << 36);
 }
 
-// How a product of more than 64 rows is cut: the tile, and the parts of k.
+// How a product of many rows is cut: tiles of rows x cols, and the parts of k.
 struct Plan {
-    int tile;   // 256, 128 or 64, square
+    int rows, cols;
     int parts;
 };
 
+int64_t tile_count(int64_t m, int64_t n, const Plan &p) { return ceil_div(m, p.rows) * ceil_div(n, p.cols); }
+
+// The largest square tile that leaves work for most of the 256 CUs; of the largest ones, the
+// height whose rounds over the CUs cost least (6720 x 4096: 432 tiles of 256 x 256 take two
+// rounds and fill 84% of them, 480 of 224 x 256 94%). Tiles of 64 that are still too few for
+// two workgroups a CU share their k.
 Plan plan(int64_t m, int64_t n, int64_t k)
 {
-    auto tiles = [&](int t) { return ceil_div(m, t) * ceil_div(n, t); };
-    const int64_t steps = ceil_div(k, kLineK);
-    int tile = 256;
-    while (tile > 64 && tiles(tile) < 192)
-        tile /= 2;
-    int64_t parts = 1;
-    while (tile == 64 && parts < 16 && tiles(tile) * parts * 2 <= 512 && parts * 16 <= steps)
-        parts *= 2;
-    return {tile, (int)parts};
+    Plan p = {256, 256, 1};
+    while (p.rows > 64 && tile_count(m, n, p) < 192)
+        p.rows = p.cols = p.rows / 2;
+    if (p.rows == 256) {
+        auto cost = [&](int rows) { return ceil_div(tile_count(m, n, {rows, 256, 1}), 256) * rows; };
+        if (cost(224) < cost(p.rows))
+            p.rows = 224;
+        if (cost(192) < cost(p.rows))
+            p.rows = 192;
+    }
+    const int64_t steps = ceil_div(k, kLineK), tiles = tile_count(m, n, p);
+    while (p.rows == 64 && p.parts < 16 && tiles * p.parts * 2 <= 512 && p.parts * 16 < steps)
+        p.parts *= 2;
+    return p;
 }
 
-template <int DT, int T, int WM, int WN>
+template <int DT, int TM, int TN, int WM, int WN>
 block_status_t run_tiles(const Args &a, int parts, float *partial, hipStream_t st)
 {
-    const int tm = (int)ceil_div(a.m, T), tn = (int)ceil_div(a.n, T);
+    const int tm = (int)ceil_div(a.m, TM), tn = (int)ceil_div(a.n, TN);
     const int64_t blocks = ceil_div((int64_t)tm * tn * parts, 8) * 8;
-    return launch(linear_tile_kernel<DT, T, T, WM, WN>, dim3((unsigned)blocks), dim3(WM * WN * 64), 0, st, a, tm, tn,
+    return launch(linear_tile_kernel<DT, TM, TN, WM, WN>, dim3((unsigned)blocks), dim3(WM * WN * 64), 0, st, a, tm, tn,
                   parts, partial);
 }
 
@@ -331,18 +355,20 @@ block_status_t run(const Args &a, float *partial, hipStream_t st)
         const dim3 grid((unsigned)ceil_div(a.n, 16));
         if (a.m <= 16)
             return launch(linear_few_kernel<DT, 1, 16>, grid, dim3(1024), 0, st, a);
-        if (a.m <= 32)
-            return launch(linear_few_kernel<DT, 2, 8>, grid, dim3(512), 0, st, a);
-        return launch(linear_few_kernel<DT, 4, 8>, grid, dim3(512), 0, st, a);
+        return launch(linear_few_kernel<DT, 2, 8>, grid, dim3(512), 0, st, a);
     }
     const Plan p = plan(a.m, a.n, a.k);
     block_status_t s;
-    if (p.tile == 256)
-        s = run_tiles<DT, 256, 2, 4>(a, p.parts, partial, st);
-    else if (p.tile == 128)
-        s = run_tiles<DT, 128, 2, 2>(a, p.parts, partial, st);
+    if (p.rows == 256)
+        s = run_tiles<DT, 256, 256, 2, 4>(a, p.parts, partial, st);
+    else if (p.rows == 224)
+        s = run_tiles<DT, 224, 256, 2, 4>(a, p.parts, partial, st);
+    else if (p.rows == 192)
+        s = run_tiles<DT, 192, 256, 2, 4>(a, p.parts, partial, st);
+    else if (p.rows == 128)
+        s = run_tiles<DT, 128, 128, 2, 2>(a, p.parts, partial, st);
     else
-        s = run_tiles<DT, 64, 2, 2>(a, p.parts, partial, st);
+        s = run_tiles<DT, 64, 64, 2, 2>(a, p.parts, partial, st);
     if (s || p.parts == 1)
         return s;
     const int64_t blocks = ceil_div((int64_t)a.m * a.n, 2048);

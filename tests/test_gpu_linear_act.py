@@ -132,3 +132,16 @@ def test_same_bits_streams_and_capture():
             torch.cuda.synchronize()
             again = linear_act(x, w, torch.empty_like(r), bias=b, activation="gelu", residual=r)
             assert torch.equal(y.view(torch.int16), again.view(torch.int16))
+
+
+@pytest.mark.parametrize("m,n,k", [(4090, 4088, 72), (3100, 4104, 136), (4600, 4096, 40), (1500, 2056, 200), (6720, 1408, 24)])
+def test_many_tiles(m, n, k):
+    """Enough tiles for every tile size and height, ragged on every side; the 64-bit product
+    runs on the GPU (float64 matmul)."""
+    say(f"[linear] m {m} n {n} k {k}")
+    for dt, act in (("bf16", "silu"), ("f16", "none")):
+        x, w, b, r = _inputs(m, n, k, dt, m)
+        y = _run(x, w, b, r, act)
+        wide = [t.to(DEV).double() for t in (x, w, b, r)]
+        v, bound, _ = ref.linear_act(wide[0], wide[1], wide[2], act, wide[3], x.dtype)
+        ref.check(y, v.cpu(), bound.cpu(), f"linear {m}x{n}x{k} {dt} {act}")
