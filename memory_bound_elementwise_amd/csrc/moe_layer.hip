@@ -554,10 +554,9 @@ __device__ __forceinline__ void down_many_pass(const DownArgs &a, const rsrc_t (
     }
 }
 
-template <int YDT, int G>
-__global__ __launch_bounds__(kDownWaves<G> * 64) void moe_down_many_kernel(DownArgs a, float *partial)
+template <int YDT, int G, int W>
+__global__ __launch_bounds__(W * 64) void moe_down_many_kernel(DownArgs a, float *partial)
 {
-    constexpr int W = kDownWaves<G>;
     extern __shared__ f32x4 dynamic[];  // [waves][tokens][kManyCols] fp32
     __shared__ int ids[kMaxPairs];
     __shared__ int first[kMaxExperts], count[kMaxExperts];
@@ -805,27 +804,52 @@ block_status_t launch_up(const UpArgs &u, int groups, dim3 grid, hipStream_t st)
     return launch(moe_up_kernel<ACT, 4, false>, grid, threads, 0, st, u);
 }
 
+template <int YDT, int G>
+block_status_t launch_few(const DownArgs &d, dim3 grid, uint32_t lds, hipStream_t st)
+{
+    constexpr int W = kDownWaves<G>;
+    // stages, ids, the waves' lists, the pairs' sums (at most kMaxPairs times their parts)
+    static_assert(W * kStage<1, G> * 16 + kMaxPairs * 4 + W * kMaxPairs * 2 + kMaxPairs * 64 <= 160 * 1024,
+                  "shared memory of a workgroup");
+    return launch(moe_down_kernel<YDT, G>, grid, dim3(W * 64), lds, st, d);
+}
+
 template <int YDT>
 block_status_t launch_down(const DownArgs &d, int groups, dim3 grid, uint32_t lds, hipStream_t st)
 {
     if (groups == 1)
-        return launch(moe_down_kernel<YDT, 1>, grid, dim3(kDownWaves<1> * 64), lds, st, d);
+        return launch_few<YDT, 1>(d, grid, lds, st);
     if (groups == 2)
-        return launch(moe_down_kernel<YDT, 2>, grid, dim3(kDownWaves<2> * 64), lds, st, d);
-    return launch(moe_down_kernel<YDT, 4>, grid, dim3(kDownWaves<4> * 64), lds, st, d);
+        return launch_few<YDT, 2>(d, grid, lds, st);
+    return launch_few<YDT, 4>(d, grid, lds, st);
+}
+
+// Shared memory of a workgroup: each wave has a stage and a row of kManyCols sums a token, so
+// more than 64 tokens leave room for four waves.
+int many_waves(const ExpertSizes &s, int groups) { return groups == 4 || s.tokens > 64 ? 4 : 8; }
+
+template <int YDT, int G, int W>
+block_status_t launch_many(const DownArgs &d, dim3 grid, float *partial, hipStream_t st)
+{
+    // stages, the lists of pairs (18.1 KB), the sums
+    constexpr int kStatic = W * kStage<kManyTiles, G> * 16 + 18 * 1024 + 128;
+    constexpr int kSums = W * (W == 8 ? 64 : kManyTokens) * kManyCols * 4;
+    static_assert(kStatic + kSums <= 160 * 1024, "shared memory of a workgroup");
+    return launch(moe_down_many_kernel<YDT, G, W>, grid, dim3(W * 64), (uint32_t)(W * d.tokens * kManyCols * 4), st, d,
+                  partial);
 }
 
 template <int YDT>
-block_status_t launch_down_many(const DownArgs &d, int groups, int shares, dim3 grid, uint32_t lds, float *partial,
+block_status_t launch_down_many(const DownArgs &d, int groups, int waves, int shares, dim3 grid, float *partial,
                                 hipStream_t st)
 {
     block_status_t r;
-    if (groups == 1)
-        r = launch(moe_down_many_kernel<YDT, 1>, grid, dim3(kDownWaves<1> * 64), lds, st, d, partial);
+    if (groups == 4)
+        r = launch_many<YDT, 4, 4>(d, grid, partial, st);
     else if (groups == 2)
-        r = launch(moe_down_many_kernel<YDT, 2>, grid, dim3(kDownWaves<2> * 64), lds, st, d, partial);
+        r = waves == 8 ? launch_many<YDT, 2, 8>(d, grid, partial, st) : launch_many<YDT, 2, 4>(d, grid, partial, st);
     else
-        r = launch(moe_down_many_kernel<YDT, 4>, grid, dim3(kDownWaves<4> * 64), lds, st, d, partial);
+        r = waves == 8 ? launch_many<YDT, 1, 8>(d, grid, partial, st) : launch_many<YDT, 1, 4>(d, grid, partial, st);
     if (r || shares == 1)
         return r;
     return launch(moe_combine_kernel<YDT>, dim3((unsigned)ceil_div((int64_t)d.tokens * d.hidden, 1024)), dim3(256), 0,
@@ -864,12 +888,11 @@ block_status_t experts(const uint16_t *x, const uint16_t *w_up, const uint16_t *
     d.tokens = u.tokens, d.hidden = u.hidden, d.inter = u.inter, d.experts = u.experts, d.top_k = u.top_k;
     const int groups = token_groups(s, 8), shares = down_shares(s);
     if (shares > 0) {
-        const int waves = groups == 4 ? kDownWaves<4> : kDownWaves<1>;
-        const uint32_t lds = (uint32_t)(waves * s.tokens * kManyCols * 4);
+        const int waves = many_waves(s, groups);
         const dim3 tiles((unsigned)ceil_div(s.hidden, kManyCols * waves), (unsigned)shares);
         float *partial = reinterpret_cast<float *>(static_cast<char *>(ws) + expert_space(s).h);
-        return ydt == BLOCK_FP32 ? launch_down_many<DT_F32>(d, groups, shares, tiles, lds, partial, st)
-                                 : launch_down_many<DT_BF16>(d, groups, shares, tiles, lds, partial, st);
+        return ydt == BLOCK_FP32 ? launch_down_many<DT_F32>(d, groups, waves, shares, tiles, partial, st)
+                                 : launch_down_many<DT_BF16>(d, groups, waves, shares, tiles, partial, st);
     }
     d.parts = down_parts(s);
     const uint32_t lds = (uint32_t)(pairs * d.parts * 64);

@@ -210,7 +210,12 @@ def layer_norm_bwd(grad_y, x, weight, mean, rstd, grad_x, grad_weight=None, grad
 
 
 class LayerNorm(torch.autograd.Function):
-    """Layer norm over the last axis, saving x and its fp32 statistics."""
+    """Layer norm over the last axis, saving x and its fp32 statistics.
+
+    Its backward is not captured into a HIP graph when it ends in leaves (parameters): autograd
+    hands a leaf's gradient over on the stream on which the leaf was first used, and where an
+    eager graph of the same leaf is alive that stream is drawn into the capture, which then
+    ends the process. A captured step calls ``layer_norm_fwd`` and ``layer_norm_bwd``."""
 
     @staticmethod
     def forward(ctx, x, weight=None, bias=None, eps=1e-5):
@@ -225,6 +230,10 @@ class LayerNorm(torch.autograd.Function):
     @staticmethod
     @once_differentiable
     def backward(ctx, grad_y):
+        if torch.cuda.is_current_stream_capturing() and any(
+                type(node).__name__ == "AccumulateGrad" for node, _ in ctx.next_functions):
+            raise RuntimeError("LayerNorm's backward into leaf tensors cannot be captured into a graph: call "
+                               "layer_norm_fwd and layer_norm_bwd in the captured step")
         flat, weight, mean, rstd = ctx.saved_tensors
         grad_x = torch.empty_like(flat) if ctx.needs_input_grad[0] else None
         grad_weight = torch.empty_like(weight) if ctx.needs_input_grad[1] else None

@@ -139,7 +139,9 @@ def test_experts(tokens, hidden, inter, act):
 
 
 @pytest.mark.parametrize("tokens,experts,top_k", [(1, 1, 1), (1, 64, 8), (64, 2, 2), (130, 2, 1), (128, 8, 8),
-                                                  (1024, 3, 1), (33, 33, 31), (7, 1024, 5)])
+                                                  (1024, 3, 1), (33, 33, 31), (7, 1024, 5), (128, 256, 1),
+                                                  (65, 40, 2), (100, 128, 3), (128, 64, 8), (90, 12, 2),
+                                                  (129, 64, 4), (64, 64, 8), (32, 4, 4)])
 def test_experts_counts(tokens, experts, top_k):
     """One expert for every token (several reads of its weights), more experts than pairs, the
     largest number of pairs."""
@@ -147,7 +149,8 @@ def test_experts_counts(tokens, experts, top_k):
     _check_experts(tokens, 40, 24, experts, top_k, "squared_relu", dtype=torch.float32, residual=False)
 
 
-@pytest.mark.parametrize("tokens,hidden,inter", [(1, 2056, 1032), (3, 7168, 256), (20, 256, 2048), (2, 64, 4104)])
+@pytest.mark.parametrize("tokens,hidden,inter", [(1, 2056, 1032), (3, 7168, 256), (20, 256, 2048), (2, 64, 4104),
+                                                  (70, 1032, 136)])
 def test_experts_long(tokens, hidden, inter):
     _check_experts(tokens, hidden, inter, 4, 2, "swiglu", limit=7.0)
     _check_experts(tokens, hidden, inter, 4, 2, "squared_relu", dtype=torch.float32)
@@ -170,20 +173,30 @@ def test_ids_outside_repeated_and_none():
     assert torch.equal(_experts(x, wu, wd, none, probs, residual=r).cpu(), r)
 
 
-@pytest.mark.parametrize("valid", [-1, 0, 1, 5, 11, 50])
-@pytest.mark.parametrize("experts", [3, 200])
-def test_experts_valid_tokens(valid, experts):
+@pytest.mark.parametrize("valid", [-1, 0, 1, 5, 11, 50, 79, 200])
+@pytest.mark.parametrize("tokens,experts", [(11, 3), (11, 200), (80, 16), (150, 8)])
+def test_experts_valid_tokens(valid, tokens, experts):
     g = torch.Generator().manual_seed(8)
-    x = _normal(g, 11, 64)
+    x = _normal(g, tokens, 64)
     wu, wd = _weights(g, experts, 64, 72, "swiglu")
-    ids = torch.randint(0, experts, (11, 2), generator=g, dtype=torch.int32)
-    probs = torch.rand(11, 2, generator=g)
-    n = min(max(valid, 0), 11)
+    ids = torch.randint(0, experts, (tokens, 2), generator=g, dtype=torch.int32)
+    probs = torch.rand(tokens, 2, generator=g)
+    n = min(max(valid, 0), tokens)
     whole = _experts(x, wu, wd, ids, probs)
     # what lies behind the last token is not read: ids far outside, NaN
     ids[n:], probs[n:], x[n:] = 1 << 30, float("nan"), float("nan")
     y = _experts(x, wu, wd, ids, probs, valid_tokens=torch.tensor([valid], dtype=torch.int32, device=DEV))
     assert torch.equal(y[:n], whole[:n]) and (y[n:] == 77).all()
+
+
+def test_repeated_ids_of_many_tokens():
+    """The same expert twice in a token, next to each other in its list, in the form for many."""
+    ids = torch.randint(-1, 5, (70, 4), generator=torch.Generator().manual_seed(3), dtype=torch.int32)
+    ids[::3, 1] = ids[::3, 0]
+    ids[5] = 2
+    ids[6] = -1
+    for dtype in (BF, torch.float32):
+        _check_experts(70, 72, 136, 4, 4, "swiglu", 7.0, dtype, True, ids)
 
 
 def test_not_finite_tokens_and_weights():
