@@ -197,6 +197,7 @@ __global__ __launch_bounds__(1024) void layer_norm_fwd_wide_kernel(const char *x
 // row of each at its end; layer_norm_partials_kernel adds those. A row's successor is loaded
 // while the row is summed. part: fp32 [gridDim.x][2][cols] or null.
 constexpr int kBwdWaves = 8;
+constexpr int kBwdParts = 256;  // one workgroup a CU, so one partial row a CU
 
 template <int DT, int WDT, int WPR, int CH, bool EVEN>
 __global__ __launch_bounds__(kBwdWaves * 64) void layer_norm_bwd_kernel(const char *gy, const char *x,
@@ -396,11 +397,17 @@ __global__ __launch_bounds__(1024) void layer_norm_partials_kernel(const float *
     const int slice = threadIdx.x / N, i = threadIdx.x % N;
     const int64_t j = (int64_t)blockIdx.x * N + i;
     const int64_t n = 2 * (int64_t)cols;
+    // at most kBwdParts partial rows, so a fixed number of loads, all under way at once
+    float v[kBwdParts / kSlices];
+#pragma unroll
+    for (int k = 0; k < kBwdParts / kSlices; ++k) {
+        const int p = slice + k * kSlices;
+        v[k] = j < n && p < parts ? part[p * n + j] : 0.0f;
+    }
     float t = 0.0f;
-    if (j < n)
-#pragma unroll 16
-        for (int p = slice; p < parts; p += kSlices)
-            t += part[p * n + j];
+#pragma unroll
+    for (int k = 0; k < kBwdParts / kSlices; ++k)
+        t += v[k];
     sums[slice][i] = t;
     __syncthreads();
     if (slice == 0 && j < n) {
@@ -420,7 +427,6 @@ constexpr int64_t kMaxCols = 1 << 20;
 constexpr int64_t kMaxHeld = 16384;  // columns of a row that is held in registers
 constexpr int64_t kMaxElems = (int64_t)1 << 48;
 constexpr int64_t kMaxGrid = 1 << 22;  // times 1024 threads: a dispatch counts work-items in 32 bits
-constexpr int kBwdParts = 256;         // one workgroup a CU, so one partial row a CU
 constexpr int kFwdWaves = 256 * 8;     // two a SIMD: 31.2 us for 6720 x 7168 bf16; three 32.1, four 36
 
 int elem_size(block_dtype_t d) { return d == BLOCK_FP32 ? 4 : 2; }

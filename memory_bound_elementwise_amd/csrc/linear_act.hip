@@ -286,13 +286,14 @@ __global__ __launch_bounds__(256) void linear_join_kernel(Args a, int parts, con
 {
     const int64_t all = (int64_t)a.m * a.n;
     for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8; i < all; i += (int64_t)gridDim.x * 2048) {
-        float z[8], f[8];
-        widen8<DT_F32>(load8<DT_F32>(reinterpret_cast<const char *>(partial + i), 0, 8), z);
-        for (int p = 1; p < parts; ++p) {
-            widen8<DT_F32>(load8<DT_F32>(reinterpret_cast<const char *>(partial + p * all + i), 0, 8), f);
+        float z[8] = {};
+        for (int p = 0; p < parts; p += 2) {  // a power of two, at least 2; two loads at a time
+            float f0[8], f1[8];
+            widen8<DT_F32>(load8<DT_F32>(reinterpret_cast<const char *>(partial + p * all + i), 0, 8), f0);
+            widen8<DT_F32>(load8<DT_F32>(reinterpret_cast<const char *>(partial + (p + 1) * all + i), 0, 8), f1);
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-                z[e] += f[e];
+                z[e] = z[e] + f0[e] + f1[e];
         }
         finish8<DT>(a, (int)(i / a.n), (int)(i % a.n), z);
     }

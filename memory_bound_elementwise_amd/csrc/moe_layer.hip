@@ -61,15 +61,35 @@ __global__ __launch_bounds__(kRouteWaves * 64) void route_logits_kernel(const ch
     const char *xr = x + (int64_t)t * hidden * 2, *wr = router + (int64_t)e * hidden * kSize<RDT>;
     const int first = blockIdx.z * part_k, last = first + part_k < hidden ? first + part_k : hidden;
     f64x4 acc = {0.0, 0.0, 0.0, 0.0};
-#pragma unroll 4
-    for (int k = first + wave * kRouteStep; k < last; k += kRouteWaves * kRouteStep) {
-        const int n = k + k8 < last ? last : 0;  // an octet past the part: zeros
-        float a[8], b[8];
-        widen8<DT_BF16>(load8<DT_BF16>(xr, k + k8, n), a);
-        widen8<RDT>(load8<RDT>(wr, k + k8, n), b);
+    constexpr int kAhead = 4;  // steps whose loads go out together
+    for (int k = first + wave * kRouteStep; k < last; k += kAhead * kRouteWaves * kRouteStep) {
+        Raw8<DT_BF16> xa[kAhead];
+        Raw8<RDT> wa[kAhead];
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            acc = __builtin_amdgcn_mfma_f64_16x16x4f64((double)b[j], (double)a[j], acc, 0, 0, 0);
+        for (int u = 0; u < kAhead; ++u) {
+            const int at = k + u * kRouteWaves * kRouteStep + k8;
+            const int from = at < last ? at : 0;
+            xa[u].v[0] = *reinterpret_cast<const u32x4 *>(xr + from * 2);
+#pragma unroll
+            for (int v = 0; v < kSize<RDT> / 2; ++v)
+                wa[u].v[v] = reinterpret_cast<const u32x4 *>(wr + (int64_t)from * kSize<RDT>)[v];
+        }
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            const int at = k + u * kRouteWaves * kRouteStep;
+            if (at >= last)
+                break;
+            if (at + kRouteStep > last && at + k8 >= last) {  // an octet past the part read the row's first: zeros
+                xa[u] = Raw8<DT_BF16>{};
+                wa[u] = Raw8<RDT>{};
+            }
+            float a[8], b[8];
+            widen8<DT_BF16>(xa[u], a);
+            widen8<RDT>(wa[u], b);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                acc = __builtin_amdgcn_mfma_f64_16x16x4f64((double)b[j], (double)a[j], acc, 0, 0, 0);
+        }
     }
 #pragma unroll
     for (int r = 0; r < 4; ++r)
@@ -87,6 +107,81 @@ __global__ __launch_bounds__(kRouteWaves * 64) void route_logits_kernel(const ch
         partial[((int64_t)blockIdx.z * tokens + t0 + i) * experts + e0 + c] = sum;
 }
 
+// The same for up to kRouteFew tokens, where a matrix instruction of 16 would idle: the octet's
+// products in the vector unit, the four octets of an expert joined across the wave.
+constexpr int kRouteFew = 4;
+
+template <int RDT>
+__global__ __launch_bounds__(kRouteWaves * 64) void route_logits_few_kernel(const char *x, const char *router,
+                                                                            double *partial, int tokens, int hidden,
+                                                                            int experts, int part_k, const int *valid)
+{
+    __shared__ double joined[kRouteWaves][kRouteFew][16];
+    const int lane = lane_id(), wave = wave_in_block(), i = lane % 16, k8 = lane / 16 * 8;
+    const int e0 = blockIdx.x * kRouteTile, live = live_tokens(valid, tokens);
+    if (live == 0)
+        return;
+    const int e = e0 + i < experts ? e0 + i : experts - 1;  // past the last: the last one again, not stored
+    const char *wr = router + (int64_t)e * hidden * kSize<RDT>;
+    const int first = blockIdx.z * part_k, last = first + part_k < hidden ? first + part_k : hidden;
+    double acc[kRouteFew] = {};
+    constexpr int kAhead = 2;  // steps whose loads go out together
+    for (int k = first + wave * kRouteStep; k < last; k += kAhead * kRouteWaves * kRouteStep) {
+        Raw8<DT_BF16> xa[kAhead][kRouteFew];
+        Raw8<RDT> wa[kAhead];
+        bool in[kAhead];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            const int at = k + u * kRouteWaves * kRouteStep + k8;
+            in[u] = at < last;  // an octet past the part: the row's first instead, not counted
+            const int from = in[u] ? at : 0;
+#pragma unroll
+            for (int v = 0; v < kSize<RDT> / 2; ++v)
+                wa[u].v[v] = reinterpret_cast<const u32x4 *>(wr + (int64_t)from * kSize<RDT>)[v];
+#pragma unroll
+            for (int t = 0; t < kRouteFew; ++t)
+                xa[u][t].v[0] = *reinterpret_cast<const u32x4 *>(x + ((int64_t)(t < live ? t : 0) * hidden + from) * 2);
+        }
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            if (k + u * kRouteWaves * kRouteStep >= last)
+                break;
+            float b[8];
+            widen8<RDT>(wa[u], b);
+#pragma unroll
+            for (int t = 0; t < kRouteFew; ++t) {
+                if (t >= live)
+                    break;
+                float a[8];
+                widen8<DT_BF16>(xa[u][t], a);
+                double sum = 0.0;
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    sum = __builtin_fma((double)a[j], (double)b[j], sum);
+                acc[t] += in[u] ? sum : 0.0;
+            }
+        }
+    }
+#pragma unroll
+    for (int t = 0; t < kRouteFew; ++t) {
+        double v = acc[t];
+        v += __shfl_xor(v, 16);
+        v += __shfl_xor(v, 32);
+        if (lane < 16)
+            joined[wave][t][i] = v;
+    }
+    __syncthreads();
+    if (wave > 0)
+        return;
+    const int t = lane / 16;  // one token a quarter of the wave
+    double sum = 0.0;
+#pragma unroll
+    for (int w = 0; w < kRouteWaves; ++w)
+        sum += joined[w][t][i];
+    if (t < live && e0 + i < experts)
+        partial[((int64_t)blockIdx.z * tokens + t) * experts + e0 + i] = sum;
+}
+
 // A double as an unsigned integer in the same order; +0 and -0 alike, NaN above all.
 __device__ __forceinline__ uint64_t order_key(double v)
 {
@@ -94,6 +189,23 @@ __device__ __forceinline__ uint64_t order_key(double v)
         return ~(uint64_t)0;
     const uint64_t b = __builtin_bit_cast(uint64_t, v + 0.0);
     return b >> 63 ? ~b : b | (uint64_t)1 << 63;
+}
+
+// The sum of a logit's parts in order, eight loads at a time (a loop of single loads waits
+// for each: 3 us for seven).
+__device__ __forceinline__ double sum_parts(const double *mine, int64_t part, int parts)
+{
+    double v = 0.0;
+    for (int s = 0; s < parts; s += 8) {
+        double p[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            p[i] = mine[(s + i < parts ? s + i : 0) * part];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            v += s + i < parts ? p[i] : 0.0;
+    }
+    return v;
 }
 
 // One workgroup a token, a thread an expert: its logit is the sum of its parts in order, its
@@ -114,10 +226,7 @@ __global__ __launch_bounds__(kMaxExperts) void route_choose_kernel(const double 
         return;
     const double *mine = partial + (int64_t)t * experts + (e < experts ? e : 0);
     const int64_t part = (int64_t)tokens * experts;
-    double v = 0.0;
-#pragma unroll 8
-    for (int s = 0; s < parts; ++s)
-        v += mine[s * part];
+    const double v = sum_parts(mine, part, parts);
     const uint64_t key = order_key(v);
     keys[e] = key;
     if (e == 0)
@@ -164,10 +273,7 @@ __device__ __forceinline__ void choose_in_wave(const double *partial, int t, int
     const int e = lane_id();
     const double *mine = partial + (int64_t)t * experts + (e < experts ? e : 0);
     const int64_t part = (int64_t)tokens * experts;
-    double v = 0.0;
-#pragma unroll 8
-    for (int s = 0; s < parts; ++s)
-        v += mine[s * part];
+    const double v = sum_parts(mine, part, parts);
     const uint64_t key = order_key(v);
     keys[e] = key;
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
@@ -657,9 +763,12 @@ __global__ __launch_bounds__(256) void moe_combine_kernel(DownArgs a, const floa
     const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4, all = (int64_t)a.tokens * a.hidden;
     if (i >= (int64_t)live_tokens(a.valid, a.tokens) * a.hidden)
         return;
-    f32x4 v = *reinterpret_cast<const f32x4 *>(partial + i);
-    for (int p = 1; p < parts; ++p)
-        v += *reinterpret_cast<const f32x4 *>(partial + p * all + i);
+    f32x4 v = {0, 0, 0, 0};
+    for (int p = 0; p < parts; p += 2) {  // a power of two, at least 2; two loads at a time
+        const f32x4 a0 = *reinterpret_cast<const f32x4 *>(partial + p * all + i);
+        const f32x4 a1 = *reinterpret_cast<const f32x4 *>(partial + (p + 1) * all + i);
+        v = v + a0 + a1;
+    }
 #pragma unroll
     for (int j = 0; j < 4; ++j)
         finish_row<YDT>(a, i + j, v[j]);
@@ -706,11 +815,13 @@ block_status_t route_logits(const uint16_t *x, const void *router, block_dtype_t
     const dim3 grid((unsigned)ceil_div(s.experts, kRouteTile), (unsigned)ceil_div(s.tokens, kRouteTile),
                     (unsigned)route_parts(s)),
         threads(kRouteWaves * 64);
-    if (rdt == BLOCK_FP32)
-        return launch(route_logits_kernel<DT_F32>, grid, threads, 0, st, xc, rc, partial, (int)s.tokens, (int)s.hidden,
-                      s.experts, route_part(s), valid);
-    return launch(route_logits_kernel<DT_BF16>, grid, threads, 0, st, xc, rc, partial, (int)s.tokens, (int)s.hidden,
-                  s.experts, route_part(s), valid);
+    auto run = [&](auto kernel) {
+        return launch(kernel, grid, threads, 0, st, xc, rc, partial, (int)s.tokens, (int)s.hidden, s.experts,
+                      route_part(s), valid);
+    };
+    if (s.tokens <= kRouteFew)
+        return rdt == BLOCK_FP32 ? run(route_logits_few_kernel<DT_F32>) : run(route_logits_few_kernel<DT_BF16>);
+    return rdt == BLOCK_FP32 ? run(route_logits_kernel<DT_F32>) : run(route_logits_kernel<DT_BF16>);
 }
 
 block_status_t route(const uint16_t *x, const void *router, block_dtype_t rdt, int *ids, float *probs,
