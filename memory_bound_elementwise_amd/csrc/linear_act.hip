@@ -69,7 +69,6 @@ __global__ __launch_bounds__(WAVES * 64) void linear_few_kernel(Args a)
     __shared__ u32x4 shared[WAVES * kStage<1, G>];
     const int lane = lane_id(), wave = wave_in_block();
     const int c0 = blockIdx.x * 16;
-    constexpr int DEPTH = G == 2 ? 3 : 2;
     const int there = a.n - c0 < 16 ? a.n - c0 : 16;
     const uint32_t row_bytes = (uint32_t)a.k * 2u;
     const rsrc_t w[1] = {make_rsrc(a.w + (int64_t)c0 * a.k, (uint32_t)there * row_bytes)};
@@ -84,7 +83,7 @@ __global__ __launch_bounds__(WAVES * 64) void linear_few_kernel(Args a)
             const int r = g * 16 + p * 8 + lane / 8;
             col[g][p] = r < a.m ? (uint32_t)r * row_bytes + lane % 8 * 16 : kNowhere;
         }
-    stream_products<DT, 1, G, DEPTH, 1>(acc, w, row_bytes, x, col, a.k, wave * kLineK, WAVES * kLineK,
+    stream_products<DT, 1, G, 1>(acc, w, row_bytes, x, col, a.k, wave * kLineK, WAVES * kLineK,
                                         shared + wave * kStage<1, G>);
     __syncthreads();  // the sums take the place of the stages
     f32x4 *joined = reinterpret_cast<f32x4 *>(shared);
@@ -137,7 +136,11 @@ __device__ __forceinline__ void wait_and_sync()
 // the 16 lanes whose reads of an operand go together fall into different banks. A load's
 // lanes fill shared memory in order, so the exchange is made in the addresses they read.
 // (Four buffers of 32 k reach further ahead but ask the cache for half lines: 9 TB/s of
-// requests were the limit, 413 us for 6720 x 7168 x 4096 where this takes XXX.)
+// requests were the limit, 413 us for 6720 x 7168 x 4096 in tiles of 256 x 256 where this
+// takes 385, and 343 to 376 in tiles of 224 x 256: 1.1 PFLOP/s, 75% of the library's product
+// alone. What bounds it now is shared memory, which the eight waves read three quarters of
+// the time, and power: the clock falls to 1.85 GHz. Four waves of 128 x 128 read a third
+// less, but one wave a SIMD hides nothing: 520 us.)
 // Operands are read from shared memory half a step before their products, which leaves one
 // barrier a step and no product waiting for a read.
 //   parts > 1: the sums over one of `parts` ranges of k, to partial [parts][m][n] in fp32.

@@ -367,7 +367,6 @@ __device__ __forceinline__ void up_pass(const UpArgs &a, const float *probs, int
                                         u32x4 *shared)
 {
     constexpr int RT = ACT == ACT_SWIGLU ? 2 : 1;  // gate and up, or the one product
-    constexpr int DEPTH = G == 1 ? 3 : 2;
     const int lane = lane_id(), wave = wave_in_block();
     const int there = a.inter - i0 < 16 ? a.inter - i0 : 16;
     const uint32_t row_bytes = (uint32_t)a.hidden * 2u;
@@ -386,7 +385,7 @@ __device__ __forceinline__ void up_pass(const UpArgs &a, const float *probs, int
         }
     f32x4 acc[RT][G];
     clear(acc);
-    stream_products<DT_BF16, RT, G, DEPTH, 1>(acc, w, row_bytes, x, col, a.hidden, wave * kLineK,
+    stream_products<DT_BF16, RT, G, 1>(acc, w, row_bytes, x, col, a.hidden, wave * kLineK,
                                               kUpWaves * kLineK, shared + wave * kStage<RT, G>);
     __syncthreads();  // the sums take the place of the stages
     f32x4 *joined = reinterpret_cast<f32x4 *>(shared);
@@ -519,14 +518,13 @@ template <int G>
 __device__ __forceinline__ void down_pass(const DownArgs &a, const rsrc_t (&w)[1], const uint16_t *list, int n, int part,
                                           float *sums, u32x4 *stage)
 {
-    constexpr int DEPTH = G == 1 ? 4 : (G == 2 ? 3 : 2);
     const int lane = lane_id();
     const rsrc_t h = make_rsrc(a.h, (uint32_t)(a.tokens * a.top_k) * (uint32_t)a.inter * 4u);
     uint32_t col[G][2];
     h_columns(a, list, n, col);
     f32x4 acc[1][G];
     clear(acc);
-    stream_products<DT_BF16, 1, G, DEPTH, 2>(acc, w, (uint32_t)a.inter * 2u, h, col, a.inter, part * kLineK,
+    stream_products<DT_BF16, 1, G, 2>(acc, w, (uint32_t)a.inter * 2u, h, col, a.inter, part * kLineK,
                                              a.parts * kLineK, stage);
 #pragma unroll
     for (int g = 0; g < G; ++g) {
@@ -633,7 +631,6 @@ template <int G>
 __device__ __forceinline__ void down_many_pass(const DownArgs &a, const rsrc_t (&w)[kManyTiles], const rsrc_t &h,
                                                const uint16_t *list, int n, float *mine, u32x4 *stage)
 {
-    constexpr int DEPTH = G == 1 ? 4 : (G == 2 ? 3 : 2);
     const int lane = lane_id();
     uint32_t col[G][2];
     h_columns(a, list, n, col);
@@ -645,7 +642,7 @@ __device__ __forceinline__ void down_many_pass(const DownArgs &a, const rsrc_t (
     }
     f32x4 acc[kManyTiles][G];
     clear(acc);
-    stream_products<DT_BF16, kManyTiles, G, DEPTH, 2>(acc, w, (uint32_t)a.inter * 2u, h, col, a.inter, 0, kLineK, stage);
+    stream_products<DT_BF16, kManyTiles, G, 2>(acc, w, (uint32_t)a.inter * 2u, h, col, a.inter, 0, kLineK, stage);
 #pragma unroll
     for (int g = 0; g < G; ++g) {
 #pragma unroll
@@ -875,7 +872,7 @@ int down_parts(const ExpertSizes &s)
     const int64_t pairs = s.tokens * s.top_k;
     const int64_t units = pairs < s.experts ? pairs : s.experts;
     int parts = 1;
-    while (units * parts < 16 && pairs * parts * 2 <= kMaxPairs && parts * 4 * kLineK <= s.inter)
+    while (units * parts < 8 && pairs * parts * 2 <= kMaxPairs && parts * 4 * kLineK <= s.inter)
         parts *= 2;
     return parts;
 }

@@ -34,9 +34,10 @@ constexpr int kStage = (RT + G) * 128;  // in 16-byte chunks
 // 16 lanes share made it the limit (470 MB: 5.9 TB/s, and 3.8 with 8 tokens an expert). So
 // rows are read eight at a time, 128 bytes each, 8 neighbouring lanes a line, which may then
 // bypass the caches (nontemporal, 6.8 TB/s), and turn into operands on the way through
-// shared memory. DEPTH steps of loads are in flight; waves and depth together have to cover
-// about 2 us of memory latency (64 KB a CU).
-template <int DT, int RT, int G, int DEPTH, int TERMS>
+// shared memory. Two steps of loads are in flight a wave; 12 to 16 waves a CU make that the
+// 64 KB that cover 2 us of latency. (Three or four steps: up product of one token 70 -> 71.5
+// us, down 40 -> 44; one step: 74, 41.)
+template <int DT, int RT, int G, int TERMS>
 __device__ __forceinline__ void stream_products(f32x4 (&acc)[RT][G], const rsrc_t (&w)[RT], uint32_t row_bytes,
                                                 rsrc_t x, const uint32_t (&col)[G][2], int K, int first, int stride,
                                                 u32x4 *stage)
@@ -104,6 +105,7 @@ __device__ __forceinline__ void stream_products(f32x4 (&acc)[RT][G], const rsrc_
         }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     };
+    constexpr int DEPTH = 2;
     Buf buf[DEPTH];
 #pragma unroll
     for (int d = 0; d < DEPTH; ++d)
