@@ -14,6 +14,7 @@ one, allocated on that stream, so that its memory is not reused before the work 
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 import threading
@@ -84,6 +85,9 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
         return lib
 
 
+_by_size = functools.lru_cache(maxsize=1024)  # workspace sizes, functions of sizes alone
+
+
 def _tensor(t, name, dtype, shape, dev):
     """Address of a tensor that is checked against one dtype, shape and device (None for an
     absent one). The checks are one expression: a decoding step's launches take a few
@@ -113,7 +117,7 @@ def _call(fn, x, stream, args, workspace=None, need=None):
     if not x.is_cuda:
         raise ValueError("tensors must live on the GPU")
     index = x.get_device()
-    if index != torch.cuda.current_device():
+    if index != _current_device():
         with torch.cuda.device(index):
             return _call(fn, x, stream, args, workspace, need)
     if stream is None:
@@ -150,12 +154,15 @@ def _current_stream(index):
 
 if hasattr(torch._C, "_cuda_getCurrentRawStream"):  # the same handle without a Stream object
     _current_stream = torch._C._cuda_getCurrentRawStream
+# x is a GPU tensor by then, so torch.cuda is initialised
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _rows(x, name):
-    if x.dim() != 2:
+    shape = x.shape
+    if len(shape) != 2:
         raise ValueError(f"{name} must be 2-D")
-    return x.shape
+    return shape
 
 
 _ANY = tuple(_TORCH)
@@ -185,6 +192,7 @@ def layer_norm_fwd(x, weight, bias, y, mean=None, rstd=None, *, eps=1e-5, stream
     return y
 
 
+@_by_size
 def layer_norm_bwd_workspace(rows: int, cols: int) -> int:
     return (_lib or load_library()).block_layer_norm_bwd_workspace(rows, cols)
 
@@ -246,6 +254,7 @@ class LayerNorm(torch.autograd.Function):
 # ---------------------------------------------------------------------------
 # Matrix product with an epilogue
 # ---------------------------------------------------------------------------
+@_by_size
 def linear_act_workspace(m: int, n: int, k: int) -> int:
     return (_lib or load_library()).block_linear_act_workspace(m, n, k)
 
@@ -269,21 +278,26 @@ def linear_act(x, weight, y, *, bias=None, activation=None, residual=None, works
 
 
 def _forward_only(name, *tensors):
-    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
-        raise RuntimeError(f"{name} has no backward pass: call it under torch.no_grad()")
+    if torch.is_grad_enabled():
+        for t in tensors:
+            if t is not None and t.requires_grad:
+                raise RuntimeError(f"{name} has no backward pass: call it under torch.no_grad()")
 
 
 # ---------------------------------------------------------------------------
 # Router and experts
 # ---------------------------------------------------------------------------
+@_by_size
 def moe_route_workspace(tokens: int, hidden: int, experts: int) -> int:
     return (_lib or load_library()).block_moe_route_workspace(tokens, hidden, experts)
 
 
+@_by_size
 def moe_experts_workspace(tokens: int, hidden: int, inter: int, experts: int, top_k: int) -> int:
     return (_lib or load_library()).block_moe_experts_workspace(tokens, hidden, inter, experts, top_k)
 
 
+@_by_size
 def moe_layer_workspace(tokens: int, hidden: int, inter: int, experts: int, top_k: int) -> int:
     return (_lib or load_library()).block_moe_layer_workspace(tokens, hidden, inter, experts, top_k)
 
