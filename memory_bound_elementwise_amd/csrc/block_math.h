@@ -54,6 +54,24 @@ __device__ __forceinline__ float activate(int act, float z)
     return z;
 }
 
+// The same on eight values, decided once.
+__device__ __forceinline__ void activate8(int act, float (&z)[8])
+{
+    if (act == ACT_SQUARED_RELU) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            z[i] = squared_relu(z[i]);
+    } else if (act == ACT_SILU) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            z[i] = silu(z[i]);
+    } else if (act == ACT_GELU) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            z[i] = activate(ACT_GELU, z[i]);
+    }
+}
+
 // silu(min(gate, L)) * clamp(up, -L, L); minimum and maximum keep NaN.
 __device__ __forceinline__ float swiglu(float gate, float up, float limit)
 {

@@ -34,30 +34,28 @@ __device__ __forceinline__ void finish(const Args &a, int row, int col, float z)
     store1<DT>(a.y, at, z);
 }
 
-// Eight neighbouring columns at once (col and n multiples of 8).
+// Eight neighbouring columns at once (col and n multiples of 8), with the bias and the residual
+// there.
 template <int DT>
-__device__ __forceinline__ void finish8(const Args &a, int row, int col, float (&z)[8])
+__device__ __forceinline__ void finish8(const Args &a, int row, int col, float (&z)[8], const Raw8<DT> &bias,
+                                        const Raw8<DT> &residual)
 {
     float f[8];
     if (a.bias) {
-        widen8<DT>(load8<DT>(reinterpret_cast<const char *>(a.bias), col, a.n), f);
+        widen8<DT>(bias, f);
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             z[i] += f[i];
     }
-    if (a.act != ACT_NONE) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            z[i] = activate(a.act, z[i]);
-    }
-    const int64_t at = (int64_t)row * a.n;
+    activate8(a.act, z);
     if (a.residual) {
-        widen8<DT>(load8<DT>(reinterpret_cast<const char *>(a.residual + at), col, a.n), f);
+        widen8<DT>(residual, f);
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             z[i] += f[i];
     }
-    store8<DT>(reinterpret_cast<char *>(a.y + at), col, a.n, z);
+    // past the caches, which the operands need (6720 x 7168 x 4096: 357 us against 377)
+    __builtin_nontemporal_store(narrow8<DT>(z).v[0], reinterpret_cast<u32x4 *>(a.y + (int64_t)row * a.n + col));
 }
 
 // ---------------------------------------------------------------------------
@@ -137,10 +135,10 @@ __device__ __forceinline__ void wait_and_sync()
 // lanes fill shared memory in order, so the exchange is made in the addresses they read.
 // (Four buffers of 32 k reach further ahead but ask the cache for half lines: 9 TB/s of
 // requests were the limit, 413 us for 6720 x 7168 x 4096 in tiles of 256 x 256 where this
-// takes 385, and 343 to 376 in tiles of 224 x 256: 1.1 PFLOP/s, 75% of the library's product
-// alone. What bounds it now is shared memory, which the eight waves read three quarters of
-// the time, and power: the clock falls to 1.85 GHz. Four waves of 128 x 128 read a third
-// less, but one wave a SIMD hides nothing: 520 us.)
+// takes 385; with tiles of 224 x 256 and the epilogue's loads together 325 to 357: 1.2 PFLOP/s,
+// 81% of the library's product alone. What bounds it now is shared memory, which the eight waves read three quarters of
+// the time, and power: the clock falls to 1.85 GHz. Four waves of 112 x 128 read a third
+// less, but one wave a SIMD hides less: no faster, even with loads of W two steps ahead.)
 // Operands are read from shared memory half a step before their products, which leaves one
 // barrier a step and no product waiting for a read.
 //   parts > 1: the sums over one of `parts` ranges of k, to partial [parts][m][n] in fp32.
@@ -183,12 +181,12 @@ __global__ __launch_bounds__(WM * WN * 64) void linear_tile_kernel(Args a, int t
     const int first = (int)((int64_t)steps * part / parts), last = (int)((int64_t)steps * (part + 1) / parts);
     auto load = [&](u32x4 *to, int step) {
         const int k = step * kLineK;
-        const bool in = step < last && k + chunk * 8 < a.k;  // past the last step: zeros
+        const uint32_t at = step < last && k + chunk * 8 < a.k ? base : kNowhere;  // past the last step: zeros
 #pragma unroll
         for (int i = 0; i < kLoadsW; ++i) {
             const int g = i < kLoadsX || !loads_x ? i : kLoadsX - 1;  // rather twice than a branch
             __builtin_amdgcn_raw_ptr_buffer_load_lds(from, (shared_void *)(to + (group0 + g) * 64), 16,
-                                                     in ? base + (uint32_t)g * 8u * row_bytes : kNowhere, k * 2, 0, 0);
+                                                     at + (uint32_t)g * 8u * row_bytes, k * 2, 0, 0);
         }
         __builtin_amdgcn_sched_barrier(0);
     };
@@ -244,13 +242,31 @@ __global__ __launch_bounds__(WM * WN * 64) void linear_tile_kernel(Args a, int t
         step(s0, s1, t);
         step(s1, s0, t + 1);
     }
+    // What a lane adds at the end, its rows of the residual all together: one after another in
+    // the loop over rows, each a round trip to memory, they cost 20 us (348 against 328 for
+    // 6720 x 7168 x 4096, two tiles a CU one after the other).
+    constexpr int kLanes = FN * 2, kTogether = 64 / kLanes, kOuts = FM * 16 / kTogether;  // lanes a row of eights
+    int late = lane;
+    asm volatile("" : "+v"(late));  // computed here, not kept over the loop
+    const int my_row = late / kLanes, my_col = late % kLanes * 8, col = c0 + wn + my_col;
+    Raw8<DT> bias, residual[kOuts];
+    if (a.bias && col < a.n)
+        bias = load8<DT>(reinterpret_cast<const char *>(a.bias), col, a.n);
+    if (a.residual && parts == 1) {
+        const rsrc_t from_r = make_rsrc(a.residual + (int64_t)r0 * a.n, (uint32_t)rows * (uint32_t)a.n * 2u);
+#pragma unroll
+        for (int i = 0; i < kOuts; ++i) {
+            const uint32_t row = wm + i * kTogether + my_row;  // rows past the end read zeros
+            residual[i].v[0] = __builtin_amdgcn_raw_buffer_load_b128(
+                from_r, col < a.n ? (row * (uint32_t)a.n + col) * 2u : kNowhere, 0, 0);
+        }
+    }
     wait_and_sync();  // the last loads, of nothing, also write shared memory
     // acc[i][j][e] is row wm + 16 i + lane % 16, column wn + 16 j + 4 (lane / 16) + e. Through
     // shared memory, kRows rows at a time, into rows of eight columns a lane.
     constexpr int kCols = FN * 16, kChunks = kCols / 4, kOwn = kBuffer * 2 / W;  // 16-byte chunks of a wave
     constexpr int kRows = 16 * most_dividing(FM, kOwn / kChunks / 16);
     u32x4 *const own = wave < W / 2 ? s0 + wave * kOwn : s1 + (wave - W / 2) * kOwn;
-    const int lanes_a_row = kCols / 8, my_row = lane / lanes_a_row, my_col = lane % lanes_a_row * 8;
 #pragma unroll
     for (int i0 = 0; i0 < FM; i0 += kRows / 16) {
 #pragma unroll
@@ -261,9 +277,9 @@ __global__ __launch_bounds__(WM * WN * 64) void linear_tile_kernel(Args a, int t
                 own[row * kChunks + (j * 4 + q ^ row % kChunks)] = __builtin_bit_cast(u32x4, acc[i0 + i][j]);
             }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-#pragma unroll 1
-        for (int r = my_row; r < kRows; r += 64 / lanes_a_row) {
-            const int row = r0 + wm + i0 * 16 + r, col = c0 + wn + my_col;
+#pragma unroll
+        for (int t = 0; t < kRows / kTogether; ++t) {
+            const int r = t * kTogether + my_row, row = r0 + wm + i0 * 16 + r;
             float z[8];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -277,7 +293,7 @@ __global__ __launch_bounds__(WM * WN * 64) void linear_tile_kernel(Args a, int t
             if (parts > 1)
                 store8<DT_F32>(reinterpret_cast<char *>(partial + ((int64_t)part * a.m + row) * a.n), col, a.n, z);
             else
-                finish8<DT>(a, row, col, z);
+                finish8<DT>(a, row, col, z, bias, residual[i0 * 16 / kTogether + t]);
         }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     }
@@ -298,7 +314,13 @@ __global__ __launch_bounds__(256) void linear_join_kernel(Args a, int parts, con
             for (int e = 0; e < 8; ++e)
                 z[e] = z[e] + f0[e] + f1[e];
         }
-        finish8<DT>(a, (int)(i / a.n), (int)(i % a.n), z);
+        const int row = (int)(i / a.n), col = (int)(i % a.n);
+        Raw8<DT> bias, residual;
+        if (a.bias)
+            bias = load8<DT>(reinterpret_cast<const char *>(a.bias), col, a.n);
+        if (a.residual)
+            residual = load8<DT>(reinterpret_cast<const char *>(a.residual + i), 0, 8);
+        finish8<DT>(a, row, col, z, bias, residual);
     }
 }
 
