@@ -145,6 +145,12 @@ struct Row {
         }
         return load8<DT>(p, j, n);
     }
+    // One fp32 value (rows of DT_F32).
+    __device__ __forceinline__ float load1(int j) const
+    {
+        static_assert(DT == DT_F32 && EVEN, "");
+        return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rsrc, (uint32_t)j * 4u, 0, 0));
+    }
     __device__ __forceinline__ void store(int j, const float (&f)[8]) const
     {
         if constexpr (EVEN) {
