@@ -137,7 +137,7 @@ __device__ __forceinline__ void wait_and_sync()
 // requests were the limit, 413 us for 6720 x 7168 x 4096 in tiles of 256 x 256 where this
 // takes 385; with tiles of 224 x 256 and the epilogue's loads together 325 to 357: 1.2 PFLOP/s,
 // 81% of the library's product alone. What bounds it now is shared memory, which the eight
-// waves read three quarters of the time, and power: the clock falls to 1.85 GHz. Four waves of
+// waves read three quarters of the time, and power: the clock falls to 1.8 GHz. Four waves of
 // 112 x 128 read a third less, but one wave a SIMD hides less: no faster, even with loads of W
 // two steps ahead.)
 // Operands are read from shared memory half a step before their products, which leaves one
