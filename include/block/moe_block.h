@@ -126,7 +126,7 @@ block_status_t block_moe_route(const uint16_t *x, const void *router_weight, blo
  * The expert products of a few tokens. For token t, slot j with e = ids[t, j] in 0 ..
  * experts-1 (any other id contributes nothing; the same id twice contributes twice):
  *     z = x[t] w_up[e]^T                                      fp32
- *     h = act(z) * probs[t, j]                                fp32, then two bf16 terms (16 bits)
+ *     h = act(z) * probs[t, j]                                fp32 (three bf16 terms, which keep its 24 bits)
  *     y[t] = residual[t] + sum over j of h w_down[e]^T        fp32, one rounding
  * BLOCK_ACT_SWIGLU: w_up is [experts, 2 inter, hidden], gate rows first, and act(z) =
  * silu(min(gate, limit)) * clamp(up, -limit, limit); limit > 0, +inf for none; NaN propagates.

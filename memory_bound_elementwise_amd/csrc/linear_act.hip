@@ -64,7 +64,7 @@ __device__ __forceinline__ void finish8(const Args &a, int row, int col, float (
 template <int DT, int G, int WAVES>
 __global__ __launch_bounds__(WAVES * 64) void linear_few_kernel(Args a)
 {
-    __shared__ u32x4 shared[WAVES * kStage<1, G>];
+    __shared__ u32x4 shared[WAVES * kStage<1, G, false>];
     const int lane = lane_id(), wave = wave_in_block();
     const int c0 = blockIdx.x * 16;
     const int there = a.n - c0 < 16 ? a.n - c0 : 16;
@@ -81,8 +81,8 @@ __global__ __launch_bounds__(WAVES * 64) void linear_few_kernel(Args a)
             const int r = g * 16 + p * 8 + lane / 8;
             col[g][p] = r < a.m ? (uint32_t)r * row_bytes + lane % 8 * 16 : kNowhere;
         }
-    stream_products<DT, 1, G, 1>(acc, w, row_bytes, x, col, a.k, wave * kLineK, WAVES * kLineK,
-                                        shared + wave * kStage<1, G>);
+    stream_products<DT, 1, G, false>(acc, w, row_bytes, x, col, a.k, wave * kLineK, WAVES * kLineK,
+                                     shared + wave * kStage<1, G, false>);
     __syncthreads();  // the sums take the place of the stages
     f32x4 *joined = reinterpret_cast<f32x4 *>(shared);
 #pragma unroll

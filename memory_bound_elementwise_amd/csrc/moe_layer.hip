@@ -4,7 +4,7 @@
 // For a few tokens the cost is reading each chosen expert's weights once. Two kernels:
 //   up    one workgroup a (chosen expert, 16 columns of the activation): its waves split the
 //         hidden axis, the activation and the probability are applied to the joined sums,
-//         and h goes to the workspace as two bf16 terms.
+//         and h goes to the workspace in fp32.
 //   down  one workgroup 16 columns of the output: its waves take the chosen experts in turn
 //         and leave each (token, slot)'s 16 values in LDS; a token's values are then added in
 //         slot order, so no atomics are needed and the bits never change.
@@ -315,34 +315,11 @@ __device__ __forceinline__ int list_pairs(const int *ids, int pairs, int e, uint
     return n;
 }
 
-// h as a sum of two bf16: the first cut off after 8 bits, the second the rest rounded to 8,
-// so h keeps 16 bits (one bf16 alone would cost about what the output's own rounding
-// costs). An infinity or NaN is the first term alone.
-__device__ __forceinline__ void split_bf16(float h, uint16_t &hi, uint16_t &lo)
-{
-    const unsigned b = __float_as_uint(h);
-    if ((b & 0x7f800000u) == 0x7f800000u) {
-        hi = (uint16_t)pack_bf16x2(h, h);
-        lo = 0;
-        return;
-    }
-    hi = (uint16_t)(b >> 16);
-    const float rest = h - __uint_as_float(b & 0xffff0000u);
-    lo = (uint16_t)pack_bf16x2(rest, rest);
-}
-
-// Where h[pair][i] is in the workspace: rows of inter, eight first terms and then their
-// eight second terms in turn, so that both are one lane's neighbouring 16 bytes.
-__device__ __forceinline__ int64_t h_at(int64_t pair, int inter, int i)
-{
-    return pair * 2 * inter + (i / 8) * 16 + i % 8;
-}
-
 struct UpArgs {
     const uint16_t *x, *w;
     const int *ids;
     const float *probs;
-    uint16_t *h;
+    float *h;  // [pairs][inter]
     const int *valid;
     int tokens, hidden, inter, experts, top_k, by_pair;
     float limit;
@@ -385,8 +362,8 @@ __device__ __forceinline__ void up_pass(const UpArgs &a, const float *probs, int
         }
     f32x4 acc[RT][G];
     clear(acc);
-    stream_products<DT_BF16, RT, G, 1>(acc, w, row_bytes, x, col, a.hidden, wave * kLineK,
-                                              kUpWaves * kLineK, shared + wave * kStage<RT, G>);
+    stream_products<DT_BF16, RT, G, false>(acc, w, row_bytes, x, col, a.hidden, wave * kLineK,
+                                           kUpWaves * kLineK, shared + wave * kStage<RT, G, false>);
     __syncthreads();  // the sums take the place of the stages
     f32x4 *joined = reinterpret_cast<f32x4 *>(shared);
 #pragma unroll
@@ -411,11 +388,7 @@ __device__ __forceinline__ void up_pass(const UpArgs &a, const float *probs, int
         if (s < n && i < a.inter) {
             const int pair = list[s];
             const float v = (ACT == ACT_SWIGLU ? swiglu(z[0], z[RT - 1], a.limit) : squared_relu(z[0])) * probs[pair];
-            uint16_t hi, lo;
-            split_bf16(v, hi, lo);
-            uint16_t *at = a.h + h_at(pair, a.inter, i);
-            at[0] = hi;
-            at[8] = lo;
+            a.h[(int64_t)pair * a.inter + i] = v;
         }
     }
     __syncthreads();
@@ -428,7 +401,7 @@ template <int ACT, int G, bool CHOOSE>
 __global__ __launch_bounds__(kUpWaves * 64) void moe_up_kernel(UpArgs a)
 {
     constexpr int RT = ACT == ACT_SWIGLU ? 2 : 1;
-    __shared__ u32x4 shared[kUpWaves * kStage<RT, G>];  // the waves' stages, then their sums
+    __shared__ u32x4 shared[kUpWaves * kStage<RT, G, false>];  // the waves' stages, then their sums
     __shared__ uint16_t list[kMaxPairs];
     __shared__ int count;
     const int live = live_tokens(a.valid, a.tokens), pairs = live * a.top_k;
@@ -480,7 +453,8 @@ __global__ __launch_bounds__(kUpWaves * 64) void moe_up_kernel(UpArgs a)
 }
 
 struct DownArgs {
-    const uint16_t *h, *w, *residual;
+    const float *h;  // [pairs][inter]
+    const uint16_t *w, *residual;
     const int *ids;
     char *y;
     const int *valid;
@@ -512,8 +486,7 @@ __device__ __forceinline__ void h_columns(const DownArgs &a, const uint16_t *lis
         }
 }
 
-// The two terms of h take a column each: a group is 8 pairs, columns 0-7 their first terms and
-// 8-15 their second ones, joined after the sums.
+// A group is 8 pairs, whose products take two columns each (stream_products), joined after the sums.
 template <int G>
 __device__ __forceinline__ void down_pass(const DownArgs &a, const rsrc_t (&w)[1], const uint16_t *list, int n, int part,
                                           float *sums, u32x4 *stage)
@@ -524,14 +497,14 @@ __device__ __forceinline__ void down_pass(const DownArgs &a, const rsrc_t (&w)[1
     h_columns(a, list, n, col);
     f32x4 acc[1][G];
     clear(acc);
-    stream_products<DT_BF16, 1, G, 2>(acc, w, (uint32_t)a.inter * 2u, h, col, a.inter, part * kLineK,
-                                             a.parts * kLineK, stage);
+    stream_products<DT_BF16, 1, G, true>(acc, w, (uint32_t)a.inter * 2u, h, col, a.inter, part * kLineK,
+                                         a.parts * kLineK, stage);
 #pragma unroll
     for (int g = 0; g < G; ++g) {
         f32x4 v = acc[0][g];
 #pragma unroll
         for (int r = 0; r < 4; ++r)
-            v[r] += dpp<0x128>(v[r]);  // row_ror:8: the other term's column
+            v[r] += dpp<0x128>(v[r]);  // row_ror:8: the other column of the pair
         const int s = g * 8 + lane % 8;
         if (s < n && lane % 16 < 8)
             *reinterpret_cast<f32x4 *>(sums + (list[s] * a.parts + part) * 16 + lane / 16 * 4) = v;
@@ -545,7 +518,7 @@ __global__ __launch_bounds__(kDownWaves<G> * 64) void moe_down_kernel(DownArgs a
     extern __shared__ f32x4 dynamic[];  // [pairs][parts][16] fp32
     __shared__ int ids[kMaxPairs];
     __shared__ uint16_t lists[W][kMaxPairs];
-    __shared__ u32x4 stages[W * kStage<1, G>];
+    __shared__ u32x4 stages[W * kStage<1, G, true>];
     float *sums = reinterpret_cast<float *>(dynamic);
     const int wave = wave_in_block(), tid = threadIdx.x;
     const int live = live_tokens(a.valid, a.tokens), pairs = live * a.top_k;
@@ -569,7 +542,7 @@ __global__ __launch_bounds__(kDownWaves<G> * 64) void moe_down_kernel(DownArgs a
             continue;
         const rsrc_t w[1] = {
             make_rsrc(a.w + ((int64_t)e * a.hidden + c0) * a.inter, (uint32_t)there * (uint32_t)a.inter * 2u)};
-        u32x4 *stage = stages + wave * kStage<1, G>;
+        u32x4 *stage = stages + wave * kStage<1, G, true>;
         for (int q = 0; q < n; q += G * 8) {
             const int m = n - q < G * 8 ? n - q : G * 8;
             if (G == 1 || m <= 8)
@@ -597,7 +570,7 @@ __global__ __launch_bounds__(kDownWaves<G> * 64) void moe_down_kernel(DownArgs a
     }
 }
 
-// The down product where the chosen experts' tokens are many: h (two terms of every pair) is
+// The down product where the chosen experts' tokens are many: h (fp32, every pair's) is
 // then as large a stream as the weights if each workgroup of 16 columns reads all of it. Here
 // a workgroup takes 128 columns and every gridDim.y-th chosen expert, a wave 16 of the
 // columns; the waves walk the same h at the same time, so all but one find it in the L1
@@ -642,7 +615,7 @@ __device__ __forceinline__ void down_many_pass(const DownArgs &a, const rsrc_t (
     }
     f32x4 acc[kManyTiles][G];
     clear(acc);
-    stream_products<DT_BF16, kManyTiles, G, 2>(acc, w, (uint32_t)a.inter * 2u, h, col, a.inter, 0, kLineK, stage);
+    stream_products<DT_BF16, kManyTiles, G, true>(acc, w, (uint32_t)a.inter * 2u, h, col, a.inter, 0, kLineK, stage);
 #pragma unroll
     for (int g = 0; g < G; ++g) {
 #pragma unroll
@@ -650,7 +623,7 @@ __device__ __forceinline__ void down_many_pass(const DownArgs &a, const rsrc_t (
             f32x4 v = acc[i][g];
 #pragma unroll
             for (int r = 0; r < 4; ++r)
-                v[r] += dpp<0x128>(v[r]);  // row_ror:8: the other term's column
+                v[r] += dpp<0x128>(v[r]);  // row_ror:8: the other column of the pair
             add_to_tokens(v, token[g], g * 8 + lane % 8 < n && lane % 16 < 8, mine + i * 16);
         }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
@@ -664,9 +637,9 @@ __global__ __launch_bounds__(W * 64) void moe_down_many_kernel(DownArgs a, float
     __shared__ int ids[kMaxPairs];
     __shared__ int first[kMaxExperts], count[kMaxExperts];
     __shared__ uint16_t units[kMaxPairs], starts[kMaxPairs], list[kMaxPairs];
-    __shared__ u32x4 stages[W * kStage<kManyTiles, G>];
+    __shared__ u32x4 stages[W * kStage<kManyTiles, G, true>];
     __shared__ int unit_count;
-    u32x4 *stage = stages + wave_in_block() * kStage<kManyTiles, G>;
+    u32x4 *stage = stages + wave_in_block() * kStage<kManyTiles, G, true>;
     const int lane = lane_id(), wave = wave_in_block(), tid = threadIdx.x;
     const int live = live_tokens(a.valid, a.tokens), pairs = live * a.top_k;
     float *mine = reinterpret_cast<float *>(dynamic) + wave * a.tokens * kManyCols;
@@ -917,7 +890,7 @@ block_status_t launch_few(const DownArgs &d, dim3 grid, uint32_t lds, hipStream_
 {
     constexpr int W = kDownWaves<G>;
     // stages, ids, the waves' lists, the pairs' sums (at most kMaxPairs times their parts)
-    static_assert(W * kStage<1, G> * 16 + kMaxPairs * 4 + W * kMaxPairs * 2 + kMaxPairs * 64 <= 160 * 1024,
+    static_assert(W * kStage<1, G, true> * 16 + kMaxPairs * 4 + W * kMaxPairs * 2 + kMaxPairs * 64 <= 160 * 1024,
                   "shared memory of a workgroup");
     return launch(moe_down_kernel<YDT, G>, grid, dim3(W * 64), lds, st, d);
 }
@@ -940,7 +913,7 @@ template <int YDT, int G, int W>
 block_status_t launch_many(const DownArgs &d, dim3 grid, float *partial, hipStream_t st)
 {
     // stages, the lists of pairs (18.1 KB), the sums
-    constexpr int kStatic = W * kStage<kManyTiles, G> * 16 + 18 * 1024 + 128;
+    constexpr int kStatic = W * kStage<kManyTiles, G, true> * 16 + 18 * 1024 + 128;
     constexpr int kSums = W * (W == 8 ? 64 : kManyTokens) * kManyCols * 4;
     static_assert(kStatic + kSums <= 160 * 1024, "shared memory of a workgroup");
     return launch(moe_down_many_kernel<YDT, G, W>, grid, dim3(W * 64), (uint32_t)(W * d.tokens * kManyCols * 4), st, d,
@@ -981,7 +954,7 @@ block_status_t experts(const uint16_t *x, const uint16_t *w_up, const uint16_t *
         u.partial = choice->partial, u.parts = choice->parts, u.renormalize = choice->renormalize;
         u.ids_out = choice->ids, u.probs_out = choice->probs;
     }
-    u.x = x, u.w = w_up, u.ids = ids, u.probs = probs, u.h = static_cast<uint16_t *>(ws), u.valid = valid;
+    u.x = x, u.w = w_up, u.ids = ids, u.probs = probs, u.h = static_cast<float *>(ws), u.valid = valid;
     u.tokens = (int)s.tokens, u.hidden = (int)s.hidden, u.inter = (int)s.inter, u.experts = s.experts;
     u.top_k = s.top_k, u.limit = limit;
     const int64_t pairs = s.tokens * s.top_k;

@@ -13,20 +13,46 @@ constexpr int kLineK = 64;  // 16-bit elements of a 128-byte line
 // zeros (tensors of these products stay below 2^31 bytes a resource).
 constexpr uint32_t kNowhere = 0x80000000u;
 
-// Shared memory of one wave: 128 bytes of each of 16 rows a tile, and of the columns 128 bytes
-// of 16 or 256 of 8 a group.
-template <int RT, int G>
-constexpr int kStage = (RT + G) * 128;  // in 16-byte chunks
+// Shared memory of one wave, in 16-byte chunks: 128 bytes of each of 16 rows a tile, and of the
+// columns 128 bytes of 16 a group, or (WIDE) three terms of 8 for one group at a time.
+template <int RT, int G, bool WIDE>
+constexpr int kStage = RT * 128 + (WIDE ? 192 : G * 128);
 
-// acc[i][g] += 16 rows of W (tile i) times the 16 columns of group g, over k = first, first +
+// An fp32 value as three bf16, h = 2 a + b + c, each in the upper half of its word: 2 a its first 8
+// bits, b the next 8, c the rest, so nothing is lost (but below 2^-102, where c runs out of
+// exponents). An infinity or NaN is a alone.
+__device__ __forceinline__ void three_terms(float h, unsigned &a, unsigned &b, unsigned &c)
+{
+    const float first = __uint_as_float(__float_as_uint(h) & 0xffff0000u);
+    const float rest = __builtin_isfinite(h) ? h - first : 0.0f;
+    a = __float_as_uint(first * 0.5f);
+    b = __float_as_uint(rest) & 0xffff0000u;
+    c = __float_as_uint(rest - __uint_as_float(b));
+}
+
+// Four values' terms, four 16-bit words each.
+__device__ __forceinline__ void three_terms(const u32x4 &h, u32x2 (&term)[3])
+{
+    unsigned t[3][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        three_terms(__uint_as_float(h[i]), t[0][i], t[1][i], t[2][i]);
+#pragma unroll
+    for (int k = 0; k < 3; ++k)
+        term[k] = u32x2{__builtin_amdgcn_perm(t[k][1], t[k][0], 0x07060302u),
+                        __builtin_amdgcn_perm(t[k][3], t[k][2], 0x07060302u)};
+}
+
+// acc[i][g] += 16 rows of W (tile i) times the columns of group g, over k = first, first +
 // stride, ... (a step is 64 k; k at and past K count as zeros). All in bytes:
 //   w[i]      resource of tile i: its rows that exist, row_bytes apart (others read zeros)
 //   x, col    resource of the columns, and where the lane's part of them starts in it:
-//     TERMS 1   column 16 g + 8 p + lane / 8, at its octet lane % 8, in col[g][p]
-//     TERMS 2   pair 8 g + 4 p + lane / 16, at its octet lane % 16 / 2 and term lane % 2; the
-//               terms of a value are two columns, j and j + 8 of pair j, and eight first
-//               terms lie before their eight second ones
-// stage: kStage<RT, G> chunks of shared memory of the wave's own; the wave needs no barrier.
+//     16-bit  16 columns a group: column 16 g + 8 p + lane / 8, at its octet lane % 8, in col[g][p]
+//     WIDE    8 columns of fp32 a group: column 8 g + 4 p + lane / 16, at its four lane % 16. They
+//             become three bf16 terms here. Two instructions take them: column j of acc adds
+//             a twice, column j + 8 b and c (sums of 16 and 24 bits, so products with one
+//             weight are exact); the caller joins the two
+// stage: kStage<RT, G, WIDE> chunks of shared memory of the wave's own; the wave needs no barrier.
 //
 // What bounds it is the rate of the address unit, then memory. The matrix operand's own
 // shape (lane 16 q + i holds row i) sends neighbouring lanes to different lines: such a load
@@ -37,7 +63,7 @@ constexpr int kStage = (RT + G) * 128;  // in 16-byte chunks
 // shared memory. Two steps of loads are in flight a wave; 12 to 16 waves a CU make that the
 // 64 KB that cover 2 us of latency. (Three or four steps: up product of one token 70 -> 71.5
 // us, down 40 -> 44; one step: 74, 41.)
-template <int DT, int RT, int G, int TERMS>
+template <int DT, int RT, int G, bool WIDE>
 __device__ __forceinline__ void stream_products(f32x4 (&acc)[RT][G], const rsrc_t (&w)[RT], uint32_t row_bytes,
                                                 rsrc_t x, const uint32_t (&col)[G][2], int K, int first, int stride,
                                                 u32x4 *stage)
@@ -48,7 +74,7 @@ __device__ __forceinline__ void stream_products(f32x4 (&acc)[RT][G], const rsrc_
     const int lane = lane_id();
     const int row = lane / 8, chunk = lane % 8;
     const uint32_t row0 = row * row_bytes + chunk * 16, row1 = row0 + 8 * row_bytes;
-    const int kw = chunk * 8, kx = TERMS == 1 ? kw : lane % 16 / 2 * 8;
+    const int kw = chunk * 8, kx = WIDE ? lane % 16 * 4 : kw;
     auto fetch = [&](Buf &buf, int k) {
         const bool in = k < K - kw, inx = k < K - kx;
 #pragma unroll
@@ -60,50 +86,94 @@ __device__ __forceinline__ void stream_products(f32x4 (&acc)[RT][G], const rsrc_
         for (int g = 0; g < G; ++g)
 #pragma unroll
             for (int p = 0; p < 2; ++p)
-                buf.x[g][p] = __builtin_amdgcn_raw_buffer_load_b128(x, inx ? col[g][p] : kNowhere, k * 2 * TERMS, 0);
+                buf.x[g][p] = __builtin_amdgcn_raw_buffer_load_b128(x, inx ? col[g][p] : kNowhere, k * (WIDE ? 4 : 2), 0);
     };
     // chunk c of a row lies at c ^ (row % 8), so that eight lanes that read one chunk of eight
     // rows, or write a row, fall into different banks
     u32x4 *const xs = stage + RT * 128;
     const int put_w = row * 8 + (chunk ^ row);
-    const int put_x0 = TERMS == 1 ? put_w : lane / 16 * 16 + (lane % 16 ^ lane / 16);
-    const int put_x1 = TERMS == 1 ? put_w + 64 : 64 + lane / 16 * 16 + (lane % 16 ^ (4 + lane / 16));
     const int i16 = lane % 16, q = lane / 16;
-    int get_w[2], get_x[2];
+    int get[2], get_next[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-        get_w[h] = i16 * 8 + ((4 * h + q) ^ i16 % 8);
-        get_x[h] = TERMS == 1 ? get_w[h] : i16 % 8 * 16 + (((4 * h + q) * 2 + i16 / 8) ^ i16 % 8);
+        get[h] = i16 * 8 + ((4 * h + q) ^ i16 % 8);
+        get_next[h] = get[h] + (i16 < 8 ? 0 : 64);  // WIDE: a again, or c
     }
+    // WIDE, in half chunks: a term of eight columns takes the place of eight rows
+    const int put_x0 = q * 16 + (i16 / 2 ^ q) * 2 + lane % 2, put_x1 = (4 + q) * 16 + (i16 / 2 ^ (4 + q)) * 2 + lane % 2;
     auto multiply = [&](const Buf &buf) {
 #pragma unroll
         for (int i = 0; i < RT; ++i) {
             stage[i * 128 + put_w] = buf.w[i][0];
             stage[i * 128 + 64 + put_w] = buf.w[i][1];
         }
+        if constexpr (!WIDE) {
 #pragma unroll
-        for (int g = 0; g < G; ++g) {
-            xs[g * 128 + put_x0] = buf.x[g][0];
-            xs[g * 128 + put_x1] = buf.x[g][1];
+            for (int g = 0; g < G; ++g) {
+                xs[g * 128 + put_w] = buf.x[g][0];
+                xs[g * 128 + 64 + put_w] = buf.x[g][1];
+            }
         }
         // the lanes of a wave run together and its accesses to shared memory stay in order;
         // the fence keeps the compiler from moving them across
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        if constexpr (WIDE) {
+            u32x4 a[RT][2];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            u32x4 b[G];
+            for (int i = 0; i < RT; ++i)
 #pragma unroll
-            for (int g = 0; g < G; ++g)
-                b[g] = xs[g * 128 + get_x[h]];
+                for (int h = 0; h < 2; ++h)
+                    a[i][h] = stage[i * 128 + get[h]];
+            // a group's products are made when the next one's reads are on their way
+            u32x2 *const halves = reinterpret_cast<u32x2 *>(xs);
+            u32x4 b[2][2][2];
+            auto products = [&](int g) __attribute__((always_inline)) {
 #pragma unroll
-            for (int i = 0; i < RT; ++i) {
-                const u32x4 a = stage[i * 128 + get_w[h]];
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+#pragma unroll
+                        for (int i = 0; i < RT; ++i)
+                            acc[i][g] = mfma16<DT>(a[i][h], b[g % 2][h][k], acc[i][g]);
+            };
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+                u32x2 t0[3], t1[3];
+                three_terms(buf.x[g][0], t0);
+                three_terms(buf.x[g][1], t1);
+#pragma unroll
+                for (int k = 0; k < 3; ++k) {
+                    halves[k * 128 + put_x0] = t0[k];
+                    halves[k * 128 + put_x1] = t1[k];
+                }
+                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    b[g % 2][h][0] = xs[get[h]];
+                    b[g % 2][h][1] = xs[get_next[h]];
+                }
+                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+                if (g > 0)
+                    products(g - 1);
+            }
+            products(G - 1);
+        } else {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                u32x4 b[G];
 #pragma unroll
                 for (int g = 0; g < G; ++g)
-                    acc[i][g] = mfma16<DT>(a, b[g], acc[i][g]);
+                    b[g] = xs[g * 128 + get[h]];
+#pragma unroll
+                for (int i = 0; i < RT; ++i) {
+                    const u32x4 a = stage[i * 128 + get[h]];
+#pragma unroll
+                    for (int g = 0; g < G; ++g)
+                        acc[i][g] = mfma16<DT>(a, b[g], acc[i][g]);
+                }
             }
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         }
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     };
     constexpr int DEPTH = 2;
     Buf buf[DEPTH];
