@@ -388,7 +388,7 @@ __device__ __forceinline__ void up_pass(const UpArgs &a, const float *probs, int
         if (s < n && i < a.inter) {
             const int pair = list[s];
             const float v = (ACT == ACT_SWIGLU ? swiglu(z[0], z[RT - 1], a.limit) : squared_relu(z[0])) * probs[pair];
-            a.h[(int64_t)pair * a.inter + i] = v;
+            a.h[(int64_t)pair * a.inter + i] = v + 0.0f;  // no -0: three_terms
         }
     }
     __syncthreads();

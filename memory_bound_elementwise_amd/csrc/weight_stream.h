@@ -18,16 +18,23 @@ constexpr uint32_t kNowhere = 0x80000000u;
 template <int RT, int G, bool WIDE>
 constexpr int kStage = RT * 128 + (WIDE ? 192 : G * 128);
 
-// An fp32 value as three bf16, h = 2 a + b + c, each in the upper half of its word: 2 a its first 8
-// bits, b the next 8, c the rest, so nothing is lost (but below 2^-102, where c runs out of
-// exponents). An infinity or NaN is a alone.
+// The largest number of eight bits below |v|, with v's sign; +0 for +0.
+__device__ __forceinline__ float eight_bits_below(float v)
+{
+    return __uint_as_float(__builtin_elementwise_sub_sat(__float_as_uint(v), 1u) & 0xffff0000u);
+}
+
+// An fp32 value (not -0) as three bf16, h = 2 a + b + c, each in the upper half of its word: 2 a its
+// first 8 bits, b the next 8, c the rest, so nothing is lost (but below 2^-102, where c runs out
+// of exponents). Each is cut off below the value, not at it, so that none is zero unless h is: a
+// zero term times an infinite weight would make a NaN of an infinity. All have h's sign. Of an
+// infinity c is one, of a NaN all three are.
 __device__ __forceinline__ void three_terms(float h, unsigned &a, unsigned &b, unsigned &c)
 {
-    const float first = __uint_as_float(__float_as_uint(h) & 0xffff0000u);
-    const float rest = __builtin_isfinite(h) ? h - first : 0.0f;
+    const float first = eight_bits_below(h), rest = h - first, second = eight_bits_below(rest);
     a = __float_as_uint(first * 0.5f);
-    b = __float_as_uint(rest) & 0xffff0000u;
-    c = __float_as_uint(rest - __uint_as_float(b));
+    b = __float_as_uint(second);
+    c = __float_as_uint(rest - second);
 }
 
 // Four values' terms, four 16-bit words each.

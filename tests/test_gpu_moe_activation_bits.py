@@ -96,3 +96,45 @@ def test_fp32_output(tokens, experts, slots, hidden, inter, act):
                     torch.empty(tokens, hidden, dtype=torch.float32, device=DEV), activation=act, limit=1.5)
     v, bound = _experts64(x.double(), wu.double(), wd.double(), ids, probs.double(), act, 1.5)
     ref.check(y, v, bound, "fp32 output")
+
+
+@pytest.mark.parametrize("tokens,experts,slots", FORMS)
+def test_infinite_weights_and_activations(tokens, experts, slots):
+    """An infinite weight of the down product gives an infinity of the activation's sign (NaN for
+    an activation of 0), however few bits the activation has; an infinite activation likewise."""
+    say(f"[infinite weights] {tokens} tokens, {experts} experts, {slots} slots")
+    width, inf = 72, float("inf")
+    g = torch.Generator().manual_seed(tokens)
+    ids = _ids(tokens, experts, slots, g)
+    probs = torch.tensor([1.0, -0.5, 1.0 / 3, -2.0 ** -20])[torch.randint(0, 4, (tokens, slots), generator=g)]
+    x = torch.zeros(tokens, width, dtype=BF)
+    x[:, 0] = 1.0
+    wu = torch.zeros(experts, width, width, dtype=BF)
+    wu[:, :, 0] = torch.randint(-1, 4, (experts, width), generator=g).to(BF)
+    wd = torch.randn(experts, width, width, generator=g).to(BF)
+    rows = torch.arange(0, width, 3)
+    wd[:, rows, torch.randint(0, width, (len(rows),), generator=g)] = inf
+    wd[:, rows[::2], 5] = -inf
+
+    def both(w_up, p):
+        y = moe_experts(x.to(DEV), w_up.to(DEV), wd.to(DEV), ids.to(DEV), p.to(DEV),
+                        torch.empty(tokens, width, dtype=torch.float32, device=DEV), activation="squared_relu").cpu()
+        at = ids.argmax(1)
+        z = w_up[ids.gather(1, at[:, None])[:, 0].long(), :, 0].double().clamp(min=0)
+        h = z * z * p.gather(1, at[:, None]).double()
+        w = wd[ids.gather(1, at[:, None])[:, 0].long()].double()
+        # elementwise in 64 bits; a sum with infinities of both signs, or 0 times one, is NaN
+        want = (w * h[:, None, :]).sum(2)
+        assert torch.equal(torch.isnan(y), torch.isnan(want))
+        there = torch.isinf(want)
+        assert torch.equal(torch.where(there, y.double(), 0.0), torch.where(there, want, 0.0))
+        assert torch.isfinite(y[torch.isfinite(want)]).all()
+        return want
+
+    want = both(wu, probs)
+    assert torch.isinf(want).any() or tokens == 1
+    positive = wu.clone()
+    positive[:, :, 0] = positive[:, :, 0].clamp(min=1)
+    assert torch.isinf(both(positive, probs)).any()
+    wd = wd.nan_to_num(posinf=1.0, neginf=1.0).abs() + 1
+    assert torch.isinf(both(positive, probs * inf)).all()
