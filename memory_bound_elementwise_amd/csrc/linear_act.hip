@@ -71,7 +71,7 @@ __global__ __launch_bounds__(WAVES * 64) void linear_few_kernel(Args a)
     const uint32_t row_bytes = (uint32_t)a.k * 2u;
     const rsrc_t w[1] = {make_rsrc(a.w + (int64_t)c0 * a.k, (uint32_t)there * row_bytes)};
     const rsrc_t x = make_rsrc(a.x, (uint32_t)a.m * row_bytes);
-    uint32_t col[G][2];
+    uint32_t col[2 * G];
     f32x4 acc[1][G];
     clear(acc);
 #pragma unroll
@@ -79,7 +79,7 @@ __global__ __launch_bounds__(WAVES * 64) void linear_few_kernel(Args a)
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
             const int r = g * 16 + p * 8 + lane / 8;
-            col[g][p] = r < a.m ? (uint32_t)r * row_bytes + lane % 8 * 16 : kNowhere;
+            col[2 * g + p] = r < a.m ? (uint32_t)r * row_bytes + lane % 8 * 16 : kNowhere;
         }
     stream_products<DT, 1, G, false>(acc, w, row_bytes, x, col, a.k, wave * kLineK, WAVES * kLineK,
                                      shared + wave * kStage<1, G, false>);

@@ -352,13 +352,13 @@ __device__ __forceinline__ void up_pass(const UpArgs &a, const float *probs, int
     for (int r = 0; r < RT; ++r)
         w[r] = make_rsrc(a.w + (((int64_t)e * RT + r) * a.inter + i0) * a.hidden, (uint32_t)there * row_bytes);
     const rsrc_t x = make_rsrc(a.x, (uint32_t)a.tokens * row_bytes);
-    uint32_t col[G][2];
+    uint32_t col[2 * G];
 #pragma unroll
     for (int g = 0; g < G; ++g)
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
             const int s = g * 16 + p * 8 + lane / 8;
-            col[g][p] = s < n ? (uint32_t)(list[s] / a.top_k) * row_bytes + lane % 8 * 16 : kNowhere;
+            col[2 * g + p] = s < n ? (uint32_t)(list[s] / a.top_k) * row_bytes + lane % 8 * 16 : kNowhere;
         }
     f32x4 acc[RT][G];
     clear(acc);
@@ -473,17 +473,17 @@ __device__ __forceinline__ void finish_row(const DownArgs &a, int64_t at, float 
 template <int G>
 constexpr int kDownWaves = G == 4 ? 4 : 8;
 
-template <int G>
-__device__ __forceinline__ void h_columns(const DownArgs &a, const uint16_t *list, int n, uint32_t (&col)[G][2])
+// A lane's columns of h: load i of the wave that is `wave`-th of SHARE takes pairs 4 (wave + i SHARE) ..+4.
+template <int LOADS>
+__device__ __forceinline__ void h_columns(const DownArgs &a, const uint16_t *list, int n, int wave, int share,
+                                          uint32_t (&col)[LOADS])
 {
     const int lane = lane_id();
 #pragma unroll
-    for (int g = 0; g < G; ++g)
-#pragma unroll
-        for (int p = 0; p < 2; ++p) {
-            const int s = g * 8 + p * 4 + lane / 16;
-            col[g][p] = s < n ? (uint32_t)list[s] * (uint32_t)a.inter * 4u + lane % 16 * 16 : kNowhere;
-        }
+    for (int i = 0; i < LOADS; ++i) {
+        const int s = (wave + i * share) * 4 + lane / 16;
+        col[i] = s < n ? (uint32_t)list[s] * (uint32_t)a.inter * 4u + lane % 16 * 16 : kNowhere;
+    }
 }
 
 // A group is 8 pairs, whose products take two columns each (stream_products), joined after the sums.
@@ -493,8 +493,8 @@ __device__ __forceinline__ void down_pass(const DownArgs &a, const rsrc_t (&w)[1
 {
     const int lane = lane_id();
     const rsrc_t h = make_rsrc(a.h, (uint32_t)(a.tokens * a.top_k) * (uint32_t)a.inter * 4u);
-    uint32_t col[G][2];
-    h_columns(a, list, n, col);
+    uint32_t col[2 * G];
+    h_columns(a, list, n, 0, 1, col);
     f32x4 acc[1][G];
     clear(acc);
     stream_products<DT_BF16, 1, G, true>(acc, w, (uint32_t)a.inter * 2u, h, col, a.inter, part * kLineK,
@@ -572,10 +572,11 @@ __global__ __launch_bounds__(kDownWaves<G> * 64) void moe_down_kernel(DownArgs a
 
 // The down product where the chosen experts' tokens are many: h (fp32, every pair's) is
 // then as large a stream as the weights if each workgroup of 16 columns reads all of it. Here
-// a workgroup takes 128 columns and every gridDim.y-th chosen expert, a wave 16 of the
-// columns; the waves walk the same h at the same time, so all but one find it in the L1
-// cache. A wave adds each token's values in LDS, expert by expert in one order. With
-// gridDim.y > 1 the workgroups leave fp32 partial rows for moe_combine_kernel.
+// a wave takes 32 columns, a workgroup of four or eight waves 128 or 256 of them and every
+// gridDim.y-th chosen expert; the waves walk the same h together and share its loads where an
+// expert has more than eight tokens (stream_products). A wave adds up all its experts' products
+// in its own LDS rows, in the order of their first pair, and writes one partial row of y a
+// token; moe_combine_kernel adds the shares in order.
 constexpr int kManyTokens = 128, kManyPairs = 128;
 constexpr int kManyWaves = 1024;
 constexpr int kManyTiles = 2, kManyCols = 16 * kManyTiles;  // a wave's columns
@@ -600,13 +601,15 @@ __device__ __forceinline__ void add_to_tokens(const f32x4 &v, int token, bool li
     }
 }
 
-template <int G>
+template <int G, int W>
 __device__ __forceinline__ void down_many_pass(const DownArgs &a, const rsrc_t (&w)[kManyTiles], const rsrc_t &h,
-                                               const uint16_t *list, int n, float *mine, u32x4 *stage)
+                                               const uint16_t *list, int n, float *mine, u32x4 *stage, u32x4 *terms,
+                                               int set_chunks)
 {
     const int lane = lane_id();
-    uint32_t col[G][2];
-    h_columns(a, list, n, col);
+    constexpr int kShare = G == 1 ? 1 : W;
+    uint32_t col[kOwnLoads<G, kShare>];
+    h_columns(a, list, n, kShare > 1 ? wave_in_block() : 0, kShare, col);
     int token[G];
 #pragma unroll
     for (int g = 0; g < G; ++g) {
@@ -615,7 +618,8 @@ __device__ __forceinline__ void down_many_pass(const DownArgs &a, const rsrc_t (
     }
     f32x4 acc[kManyTiles][G];
     clear(acc);
-    stream_products<DT_BF16, kManyTiles, G, true>(acc, w, (uint32_t)a.inter * 2u, h, col, a.inter, 0, kLineK, stage);
+    stream_products<DT_BF16, kManyTiles, G, true, kShare>(acc, w, (uint32_t)a.inter * 2u, h, col, a.inter, 0, kLineK, stage,
+                                                     terms, set_chunks);
 #pragma unroll
     for (int g = 0; g < G; ++g) {
 #pragma unroll
@@ -637,9 +641,9 @@ __global__ __launch_bounds__(W * 64) void moe_down_many_kernel(DownArgs a, float
     __shared__ int ids[kMaxPairs];
     __shared__ int first[kMaxExperts], count[kMaxExperts];
     __shared__ uint16_t units[kMaxPairs], starts[kMaxPairs], list[kMaxPairs];
-    __shared__ u32x4 stages[W * kStage<kManyTiles, G, true>];
+    __shared__ u32x4 stages[W * kStage<kManyTiles, 1, true>], terms[G > 1 ? 2 * G * kTerms : 1];
     __shared__ int unit_count;
-    u32x4 *stage = stages + wave_in_block() * kStage<kManyTiles, G, true>;
+    u32x4 *stage = stages + wave_in_block() * kStage<kManyTiles, 1, true>;
     const int lane = lane_id(), wave = wave_in_block(), tid = threadIdx.x;
     const int live = live_tokens(a.valid, a.tokens), pairs = live * a.top_k;
     float *mine = reinterpret_cast<float *>(dynamic) + wave * a.tokens * kManyCols;
@@ -689,9 +693,7 @@ __global__ __launch_bounds__(W * 64) void moe_down_many_kernel(DownArgs a, float
     for (int u = blockIdx.y + wave * step; u < n_units; u += W * step)
         list_pairs(ids, pairs, ids[units[u]], list + starts[u]);
     __syncthreads();
-    const int c0 = (blockIdx.x * W + wave) * kManyCols;
-    if (c0 >= a.hidden)
-        return;
+    const int c0 = (blockIdx.x * W + wave) * kManyCols;  // past the end: no rows of W, but its part of h
     const rsrc_t h = make_rsrc(a.h, (uint32_t)(a.tokens * a.top_k) * (uint32_t)a.inter * 4u);
     for (int u = blockIdx.y; u < n_units; u += step) {
         const int e = __builtin_amdgcn_readfirstlane(ids[units[u]]);
@@ -707,11 +709,11 @@ __global__ __launch_bounds__(W * 64) void moe_down_many_kernel(DownArgs a, float
         for (int p = 0; p < n; p += G * 8) {
             const int m = n - p < G * 8 ? n - p : G * 8;
             if (G == 1 || m <= 8)
-                down_many_pass<1>(a, w, h, l + p, m, mine, stage);
+                down_many_pass<1, W>(a, w, h, l + p, m, mine, stage, terms, G * kTerms);
             else if (G == 2 || m <= 16)
-                down_many_pass<G < 2 ? 1 : 2>(a, w, h, l + p, m, mine, stage);
+                down_many_pass<G < 2 ? 1 : 2, W>(a, w, h, l + p, m, mine, stage, terms, G * kTerms);
             else
-                down_many_pass<G>(a, w, h, l + p, m, mine, stage);
+                down_many_pass<G, W>(a, w, h, l + p, m, mine, stage, terms, G * kTerms);
         }
     }
     for (int i = lane; i < live * kManyCols; i += 64) {
@@ -913,7 +915,7 @@ template <int YDT, int G, int W>
 block_status_t launch_many(const DownArgs &d, dim3 grid, float *partial, hipStream_t st)
 {
     // stages, the lists of pairs (18.1 KB), the sums
-    constexpr int kStatic = W * kStage<kManyTiles, G, true> * 16 + 18 * 1024 + 128;
+    constexpr int kStatic = (W * kStage<kManyTiles, 1, true> + (G > 1 ? 2 * G * kTerms : 1)) * 16 + 18 * 1024 + 128;
     constexpr int kSums = W * (W == 8 ? 64 : kManyTokens) * kManyCols * 4;
     static_assert(kStatic + kSums <= 160 * 1024, "shared memory of a workgroup");
     return launch(moe_down_many_kernel<YDT, G, W>, grid, dim3(W * 64), (uint32_t)(W * d.tokens * kManyCols * 4), st, d,

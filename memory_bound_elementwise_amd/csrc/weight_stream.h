@@ -14,9 +14,13 @@ constexpr int kLineK = 64;  // 16-bit elements of a 128-byte line
 constexpr uint32_t kNowhere = 0x80000000u;
 
 // Shared memory of one wave, in 16-byte chunks: 128 bytes of each of 16 rows a tile, and of the
-// columns 128 bytes of 16 a group, or (WIDE) three terms of 8 for one group at a time.
+// columns 128 bytes of 16 a group, or (WIDE) three terms of 8 for one group at a time. Waves that
+// share their columns have two sets of every group's terms together, and a stage for rows each.
+constexpr int kTerms = 192;
+template <int G, int SHARE>
+constexpr int kOwnLoads = (2 * G + SHARE - 1) / SHARE;  // a wave's loads of columns a step
 template <int RT, int G, bool WIDE>
-constexpr int kStage = RT * 128 + (WIDE ? 192 : G * 128);
+constexpr int kStage = RT * 128 + (WIDE ? kTerms : G * 128);
 
 // The largest number of eight bits below |v|, with v's sign; +0 for +0.
 __device__ __forceinline__ float eight_bits_below(float v)
@@ -60,6 +64,12 @@ __device__ __forceinline__ void three_terms(const u32x4 &h, u32x2 (&term)[3])
 //             a twice, column j + 8 b and c (sums of 16 and 24 bits, so products with one
 //             weight are exact); the caller joins the two
 // stage: kStage<RT, G, WIDE> chunks of shared memory of the wave's own; the wave needs no barrier.
+// SHARE > 1 (WIDE): that many waves, all of the workgroup, call it together with the same columns
+// and k. Each loads and cuts up its part of them, 4 columns at a time in turn, into terms (two sets
+// of set_chunks); there is one barrier a step. stage is then for rows alone, RT * 128 chunks.
+// (Down product of 7168 x 2048, 8 of 64 experts, each wave for itself and shared: 128 tokens, four
+// waves a CU, 635 and 526 us, 465 with four steps in flight; 64 tokens, eight waves, 324 and 312.
+// With one group a step the barrier costs more: 2048 x 1408, 32 tokens, 87 and 103.)
 //
 // What bounds it is the rate of the address unit, then memory. The matrix operand's own
 // shape (lane 16 q + i holds row i) sends neighbouring lanes to different lines: such a load
@@ -70,13 +80,15 @@ __device__ __forceinline__ void three_terms(const u32x4 &h, u32x2 (&term)[3])
 // shared memory. Two steps of loads are in flight a wave; 12 to 16 waves a CU make that the
 // 64 KB that cover 2 us of latency. (Three or four steps: up product of one token 70 -> 71.5
 // us, down 40 -> 44; one step: 74, 41.)
-template <int DT, int RT, int G, bool WIDE>
+template <int DT, int RT, int G, bool WIDE, int SHARE = 1>
 __device__ __forceinline__ void stream_products(f32x4 (&acc)[RT][G], const rsrc_t (&w)[RT], uint32_t row_bytes,
-                                                rsrc_t x, const uint32_t (&col)[G][2], int K, int first, int stride,
-                                                u32x4 *stage)
+                                                rsrc_t x, const uint32_t (&col)[kOwnLoads<G, SHARE>], int K, int first,
+                                                int stride, u32x4 *stage, u32x4 *terms = nullptr, int set_chunks = 0)
 {
+    static_assert(WIDE || SHARE == 1, "");
+    constexpr int kLoads = kOwnLoads<G, SHARE>;
     struct Buf {
-        u32x4 w[RT][2], x[G][2];
+        u32x4 w[RT][2], x[kLoads];
     };
     const int lane = lane_id();
     const int row = lane / 8, chunk = lane % 8;
@@ -90,10 +102,8 @@ __device__ __forceinline__ void stream_products(f32x4 (&acc)[RT][G], const rsrc_
             buf.w[i][1] = __builtin_amdgcn_raw_buffer_load_b128(w[i], in ? row1 : kNowhere, k * 2, kLoadAux);
         }
 #pragma unroll
-        for (int g = 0; g < G; ++g)
-#pragma unroll
-            for (int p = 0; p < 2; ++p)
-                buf.x[g][p] = __builtin_amdgcn_raw_buffer_load_b128(x, inx ? col[g][p] : kNowhere, k * (WIDE ? 4 : 2), 0);
+        for (int i = 0; i < kLoads; ++i)
+            buf.x[i] = __builtin_amdgcn_raw_buffer_load_b128(x, inx ? col[i] : kNowhere, k * (WIDE ? 4 : 2), 0);
     };
     // chunk c of a row lies at c ^ (row % 8), so that eight lanes that read one chunk of eight
     // rows, or write a row, fall into different banks
@@ -108,17 +118,61 @@ __device__ __forceinline__ void stream_products(f32x4 (&acc)[RT][G], const rsrc_
     }
     // WIDE, in half chunks: a term of eight columns takes the place of eight rows
     const int put_x0 = q * 16 + (i16 / 2 ^ q) * 2 + lane % 2, put_x1 = (4 + q) * 16 + (i16 / 2 ^ (4 + q)) * 2 + lane % 2;
-    auto multiply = [&](const Buf &buf) {
+    const int wave = SHARE > 1 ? wave_in_block() : 0;
+    auto multiply = [&](const Buf &buf, int set) {
 #pragma unroll
         for (int i = 0; i < RT; ++i) {
             stage[i * 128 + put_w] = buf.w[i][0];
             stage[i * 128 + 64 + put_w] = buf.w[i][1];
         }
+        if constexpr (SHARE > 1) {
+            u32x4 *const now = terms + set * set_chunks;
+            u32x2 *const halves = reinterpret_cast<u32x2 *>(now);
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) {
+                const int load = wave + i * SHARE;  // of 2 G: four columns each
+                if (load >= 2 * G)
+                    break;
+                u32x2 t[3];
+                three_terms(buf.x[i], t);
+#pragma unroll
+                for (int k = 0; k < 3; ++k)
+                    halves[load / 2 * (2 * kTerms) + k * 128 + (load % 2 ? put_x1 : put_x0)] = t[k];
+            }
+            // Everyone's terms of this step are there. Those of the next go into the other set, and
+            // into this one again only after the next barrier, which a wave reaches when its reads
+            // below have come. Loads from memory go on.
+            __builtin_amdgcn_sched_barrier(0);
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0)
+            __builtin_amdgcn_s_barrier();
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            __builtin_amdgcn_sched_barrier(0);
+            u32x4 a[RT][2];
+#pragma unroll
+            for (int i = 0; i < RT; ++i)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    a[i][h] = stage[i * 128 + get[h]];
+#pragma unroll
+            for (int g = 0; g < G; ++g)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const u32x4 b = now[g * kTerms + get[h]], c = now[g * kTerms + get_next[h]];
+#pragma unroll
+                    for (int i = 0; i < RT; ++i) {
+                        acc[i][g] = mfma16<DT>(a[i][h], b, acc[i][g]);
+                        acc[i][g] = mfma16<DT>(a[i][h], c, acc[i][g]);
+                    }
+                }
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            return;
+        }
         if constexpr (!WIDE) {
 #pragma unroll
             for (int g = 0; g < G; ++g) {
-                xs[g * 128 + put_w] = buf.x[g][0];
-                xs[g * 128 + 64 + put_w] = buf.x[g][1];
+                xs[g * 128 + put_w] = buf.x[2 * g];
+                xs[g * 128 + 64 + put_w] = buf.x[2 * g + 1];
             }
         }
         // the lanes of a wave run together and its accesses to shared memory stay in order;
@@ -146,8 +200,8 @@ __device__ __forceinline__ void stream_products(f32x4 (&acc)[RT][G], const rsrc_
 #pragma unroll
             for (int g = 0; g < G; ++g) {
                 u32x2 t0[3], t1[3];
-                three_terms(buf.x[g][0], t0);
-                three_terms(buf.x[g][1], t1);
+                three_terms(buf.x[2 * g], t0);
+                three_terms(buf.x[2 * g + 1], t1);
 #pragma unroll
                 for (int k = 0; k < 3; ++k) {
                     halves[k * 128 + put_x0] = t0[k];
@@ -182,15 +236,16 @@ __device__ __forceinline__ void stream_products(f32x4 (&acc)[RT][G], const rsrc_
             __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         }
     };
-    constexpr int DEPTH = 2;
+    // steps of loads in flight: four where four waves have the CU to themselves
+    constexpr int DEPTH = SHARE == 4 ? 4 : 2;
     Buf buf[DEPTH];
 #pragma unroll
     for (int d = 0; d < DEPTH; ++d)
         fetch(buf[d], first + d * stride);
-    for (int k = first; k < K;) {
+    for (int k = first; k < K;) {  // whole turns of an even depth, so calls use the sets in turn too
 #pragma unroll
         for (int d = 0; d < DEPTH; ++d) {
-            multiply(buf[d]);
+            multiply(buf[d], d % 2);
             fetch(buf[d], k + DEPTH * stride);  // past K: loads nothing
             k += stride;
         }

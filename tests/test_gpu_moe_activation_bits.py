@@ -138,3 +138,34 @@ def test_infinite_weights_and_activations(tokens, experts, slots):
     assert torch.isinf(both(positive, probs)).any()
     wd = wd.nan_to_num(posinf=1.0, neginf=1.0).abs() + 1
     assert torch.isinf(both(positive, probs * inf)).all()
+
+
+@pytest.mark.parametrize("tokens,experts,slots", [(64, 16, 4), (64, 64, 8), (128, 64, 8), (128, 16, 2)])
+def test_same_bits_where_waves_share(tokens, experts, slots):
+    """The waves of a workgroup share the activations' loads: every call gives the same bits, and
+    a token with one expert the same whatever its place among the others."""
+    say(f"[same bits] {tokens} tokens, {experts} experts, {slots} slots")
+    hidden, inter = 2056, 1032
+    g = torch.Generator(device=DEV).manual_seed(tokens + slots)
+    x = torch.randn(tokens, hidden, generator=g, device=DEV).to(BF)
+    wu = (torch.randn(experts, 2 * inter, hidden, generator=g, device=DEV) * 2 * hidden ** -0.5).to(BF)
+    wd = (torch.randn(experts, hidden, inter, generator=g, device=DEV) * inter ** -0.5).to(BF)
+    # one expert a token in its first slot, so that a row is one expert's sum alone
+    ids = torch.full((tokens, slots), -1, dtype=torch.int32, device=DEV)
+    ids[:, 0] = torch.randint(0, experts, (tokens,), generator=g, device=DEV, dtype=torch.int32)
+    probs = torch.rand(tokens, slots, generator=g, device=DEV)
+
+    def call(rows):
+        return moe_experts(x[rows], wu, wd, ids[rows], probs[rows],
+                           torch.empty(len(x[rows]), hidden, dtype=torch.float32, device=DEV), limit=7.0)
+
+    want = call(slice(None))
+    for _ in range(10):
+        assert torch.equal(call(slice(None)), want)
+    order = torch.randperm(tokens, generator=g, device=DEV)
+    assert torch.equal(call(order), want[order])
+    # every slot taken
+    ids[:] = torch.randint(0, experts, ids.shape, generator=g, device=DEV, dtype=torch.int32)
+    want = call(slice(None))
+    for _ in range(10):
+        assert torch.equal(call(slice(None)), want)
