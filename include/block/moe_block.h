@@ -64,7 +64,9 @@ typedef enum block_act BLOCK_ENUM_BASE {
  * Layer norm of each row, statistics and arithmetic in fp32, one rounding per output:
  *     mean = (1/C) sum_j x_j     rstd = 1 / sqrt((1/C) sum_j (x_j - mean)^2 + eps)
  *     y_j  = (x_j - mean) rstd weight_j + bias_j
- * The variance is summed about the mean, so an offset common to a row costs no digits.
+ * The variance is summed about the mean, and the mean corrected by the mean deviation from it, so
+ * an offset common to a row costs digits only in mean's own rounding (a constant row is its
+ * bias) until the offset nears 10^6 deviations.
  *   x, y: [rows, cols] of dtype; weight, bias: [cols] of weight_dtype (dtype or
  *   BLOCK_FP32), each may be NULL (1 and 0); mean, rstd: fp32 [rows], both or neither NULL.
  *   rows >= 0, 1 <= cols <= 2^20, any width; rows * cols <= 2^48; eps >= 0 and finite.
