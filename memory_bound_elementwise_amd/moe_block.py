@@ -217,8 +217,17 @@ def layer_norm_bwd(grad_y, x, weight, mean, rstd, grad_x, grad_weight=None, grad
     return grad_x, grad_weight, grad_bias
 
 
+def _aligned(t):
+    """t, or a copy of it where it is not contiguous or does not start at 16 bytes, as the kernels
+    want it (a slice of a tensor whose rows have an odd length may start anywhere)."""
+    if t is None:
+        return None
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
 class LayerNorm(torch.autograd.Function):
-    """Layer norm over the last axis, saving x and its fp32 statistics.
+    """Layer norm over the last axis, saving x and its fp32 statistics. Any strides and offsets.
 
     Its backward is not captured into a HIP graph when it ends in leaves (parameters): autograd
     hands a leaf's gradient over on the stream on which the leaf was first used, and where an
@@ -227,7 +236,8 @@ class LayerNorm(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, x, weight=None, bias=None, eps=1e-5):
-        flat = x.contiguous().view(-1, x.shape[-1])
+        flat = _aligned(x).view(-1, x.shape[-1])
+        weight, bias = _aligned(weight), _aligned(bias)
         mean = torch.empty(flat.shape[0], dtype=torch.float32, device=x.device)
         rstd = torch.empty_like(mean)
         y = layer_norm_fwd(flat, weight, bias, torch.empty_like(flat), mean, rstd, eps=eps)
@@ -247,7 +257,7 @@ class LayerNorm(torch.autograd.Function):
         grad_weight = torch.empty_like(weight) if ctx.needs_input_grad[1] else None
         grad_bias = (torch.empty(flat.shape[1], dtype=ctx.bias_dtype, device=flat.device)
                      if ctx.needs_input_grad[2] else None)
-        layer_norm_bwd(grad_y.contiguous().view(flat.shape), flat, weight, mean, rstd, grad_x, grad_weight, grad_bias)
+        layer_norm_bwd(_aligned(grad_y).view(flat.shape), flat, weight, mean, rstd, grad_x, grad_weight, grad_bias)
         return None if grad_x is None else grad_x.view(grad_y.shape), grad_weight, grad_bias, None
 
 
