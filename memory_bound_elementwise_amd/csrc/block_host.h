@@ -58,6 +58,9 @@ block_status_t launch(void (*kernel)(P...), dim3 grid, dim3 threads, uint32_t ld
     }(static_cast<P>(args)...);
 }
 
+// The most workgroups of so many threads: a dispatch counts its work-items in 32 bits.
+constexpr int64_t max_groups(int threads) { return 0xffffffffu / (unsigned)threads; }
+
 constexpr int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 constexpr int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
 

@@ -154,10 +154,12 @@ __global__ __launch_bounds__(BLOCK) void layer_norm_fwd_kernel(const char *x, co
     }
 }
 
+constexpr int kWideThreads = 1024;
+
 // Rows of any width: one workgroup of 16 waves a row, which it reads three times (the
 // second and third time from cache).
 template <int DT, int WDT>
-__global__ __launch_bounds__(1024) void layer_norm_fwd_wide_kernel(const char *x, const char *weight,
+__global__ __launch_bounds__(kWideThreads) void layer_norm_fwd_wide_kernel(const char *x, const char *weight,
                                                                    const char *bias, char *y, float *mean,
                                                                    float *rstd, int64_t rows, int cols, float eps)
 {
@@ -361,7 +363,7 @@ __global__ __launch_bounds__(kBwdWaves * 64) void layer_norm_bwd_kernel(const ch
 
 // Rows of any width, grad_x only: one workgroup a row, which it reads twice.
 template <int DT, int WDT>
-__global__ __launch_bounds__(1024) void layer_norm_bwd_x_wide_kernel(const char *gy, const char *x,
+__global__ __launch_bounds__(kWideThreads) void layer_norm_bwd_x_wide_kernel(const char *gy, const char *x,
                                                                      const char *weight, const float *mean,
                                                                      const float *rstd, char *gx, int64_t rows,
                                                                      int cols)
@@ -469,7 +471,6 @@ __global__ __launch_bounds__(1024) void layer_norm_partials_kernel(const float *
 constexpr int64_t kMaxCols = 1 << 20;
 constexpr int64_t kMaxHeld = 16384;  // columns of a row that is held in registers
 constexpr int64_t kMaxElems = (int64_t)1 << 48;
-constexpr int64_t kMaxGrid = 1 << 22;  // times 1024 threads: a dispatch counts work-items in 32 bits
 constexpr int kFwdWaves = 256 * 8;     // two a SIMD: 31.2 us for 6720 x 7168 bf16; three 32.1, four 36
 constexpr int kFwdBlocks = 256;        // but a workgroup a CU: 2000 x 12000 bf16 21 us, with 128 36
 
@@ -506,6 +507,11 @@ int bwd_parts(int64_t rows, int64_t cols)
     return (int)(need < kBwdParts ? need : kBwdParts);
 }
 
+dim3 wide_grid(const Args &a)
+{
+    return dim3((unsigned)(a.rows < max_groups(kWideThreads) ? a.rows : max_groups(kWideThreads)));
+}
+
 template <int DT, int WDT, int WPR, int CH, int BLOCK, bool EVEN>
 block_status_t fwd_as(const Args &a)
 {
@@ -538,8 +544,8 @@ struct Fwd {
     {
         if (a.cols <= kMaxHeld)
             return a.cols % 8 == 0 ? held<true>(a) : held<false>(a);
-        return launch(layer_norm_fwd_wide_kernel<DT, WDT>, dim3((unsigned)(a.rows < kMaxGrid ? a.rows : kMaxGrid)),
-                      dim3(1024), 0, a.st, static_cast<const char *>(a.x), static_cast<const char *>(a.weight),
+        return launch(layer_norm_fwd_wide_kernel<DT, WDT>, wide_grid(a), dim3(kWideThreads), 0, a.st,
+                      static_cast<const char *>(a.x), static_cast<const char *>(a.weight),
                       static_cast<const char *>(a.bias), static_cast<char *>(a.y), a.mean_out, a.rstd_out, a.rows,
                       a.cols, a.eps);
     }
@@ -576,8 +582,8 @@ struct Bwd {
             return a.cols % 8 == 0 ? held<true>(a) : held<false>(a);
         block_status_t s = BLOCK_OK;
         if (a.gx)
-            s = launch(layer_norm_bwd_x_wide_kernel<DT, WDT>, dim3((unsigned)(a.rows < kMaxGrid ? a.rows : kMaxGrid)),
-                       dim3(1024), 0, a.st, static_cast<const char *>(a.gy), static_cast<const char *>(a.x),
+            s = launch(layer_norm_bwd_x_wide_kernel<DT, WDT>, wide_grid(a), dim3(kWideThreads), 0, a.st,
+                       static_cast<const char *>(a.gy), static_cast<const char *>(a.x),
                        static_cast<const char *>(a.weight), a.mean, a.rstd, static_cast<char *>(a.gx), a.rows, a.cols);
         if (s == BLOCK_OK && a.part)
             s = launch(layer_norm_bwd_w_wide_kernel<DT>, dim3((unsigned)ceil_div(a.cols, 2048), bwd_parts(a.rows, a.cols)),
