@@ -106,9 +106,10 @@ block_status_t block_linear_act(const void *x, const void *weight, const void *b
 
 /*
  * Router: logits = x router_weight^T in fp64 (so the choice between two experts is the one
- * exact arithmetic makes, down to a relative difference of 1e-15), then per token the top_k
- * largest in descending order, equal logits in increasing expert index, NaN before any
- * number, and their softmax weights in fp32:
+ * exact arithmetic makes, unless their logits differ by less than hidden 2^-53 of the sum of
+ * their terms' magnitudes), then per token the top_k largest in descending order, equal logits
+ * in increasing expert index, NaN before any number, and their softmax weights, in fp64 too and
+ * rounded once to fp32:
  *     probs = e^(l_i - l_max) / sum over all experts      (renormalize == 0)
  *     probs = e^(l_i - l_max) / sum over the chosen ones  (renormalize != 0)
  *   x: bf16 [tokens, hidden]; router_weight: [experts, hidden], bf16 or fp32 (router_dtype);

@@ -191,6 +191,37 @@ __device__ __forceinline__ uint64_t order_key(double v)
     return b >> 63 ? ~b : b | (uint64_t)1 << 63;
 }
 
+template <int kCtrl, int kRowMask = 0xf>
+__device__ __forceinline__ double dpp64(double v)
+{
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const int lo = __builtin_amdgcn_update_dpp(0, (int)(unsigned)b, kCtrl, kRowMask, 0xf, false);
+    const int hi = __builtin_amdgcn_update_dpp(0, (int)(unsigned)(b >> 32), kCtrl, kRowMask, 0xf, false);
+    return __builtin_bit_cast(double, (uint64_t)(unsigned)hi << 32 | (unsigned)lo);
+}
+
+// The value that lane `from` (the same in all lanes) holds.
+__device__ __forceinline__ double of_lane(double v, int from)
+{
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const unsigned lo = __builtin_amdgcn_readlane((int)(unsigned)b, from);
+    const unsigned hi = __builtin_amdgcn_readlane((int)(unsigned)(b >> 32), from);
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+
+// wave_sum in fp64. The softmax stays in fp64 until its weights are rounded: with the difference
+// of two logits rounded to fp32 a weight e^-d was off by d steps.
+__device__ __forceinline__ double wave_sum64(double v)
+{
+    v += dpp64<0xB1>(v);
+    v += dpp64<0x4E>(v);
+    v += dpp64<0x141>(v);
+    v += dpp64<0x140>(v);
+    v += dpp64<0x142, 0xa>(v);
+    v += dpp64<0x143, 0xc>(v);
+    return of_lane(v, 63);
+}
+
 // The sum of a logit's parts in order, eight loads at a time (a loop of single loads waits
 // for each: 3 us for seven).
 __device__ __forceinline__ double sum_parts(const double *mine, int64_t part, int parts)
@@ -217,7 +248,7 @@ __global__ __launch_bounds__(kMaxExperts) void route_choose_kernel(const double 
                                                                    int renormalize, const int *valid)
 {
     __shared__ uint64_t keys[kMaxExperts];
-    __shared__ float sums[kMaxExperts / 64];
+    __shared__ double sums[kMaxExperts / 64];
     __shared__ int holder[kMaxExperts];
     __shared__ int tied;
     __shared__ double top;
@@ -251,17 +282,17 @@ __global__ __launch_bounds__(kMaxExperts) void route_choose_kernel(const double 
     if (rank == 0)
         top = v;
     __syncthreads();
-    const float w = e < experts ? expf((float)(v - top)) : 0.0f;
-    float sum = wave_sum(renormalize && rank >= top_k ? 0.0f : w);
+    const double w = e < experts ? exp(v - top) : 0.0;
+    double sum = wave_sum64(renormalize && rank >= top_k ? 0.0 : w);
     if (lane == 0)
         sums[wave] = sum;
     __syncthreads();
-    sum = 0.0f;
+    sum = 0.0;
     for (int i = 0; i < (int)blockDim.x / 64; ++i)
         sum += sums[i];
     if (rank < top_k) {
         ids[(int64_t)t * top_k + rank] = e;
-        probs[(int64_t)t * top_k + rank] = w / sum;
+        probs[(int64_t)t * top_k + rank] = (float)(w / sum);
     }
 }
 
@@ -284,15 +315,11 @@ __device__ __forceinline__ void choose_in_wave(const double *partial, int t, int
     if (e >= experts)
         rank = experts;
     const int first = __builtin_ctzll(__ballot(rank == 0));
-    const uint64_t bits = __builtin_bit_cast(uint64_t, v);
-    const unsigned lo = __builtin_amdgcn_readlane((int)(unsigned)bits, first);
-    const unsigned hi = __builtin_amdgcn_readlane((int)(unsigned)(bits >> 32), first);
-    const double top = __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
-    const float w = e < experts ? expf((float)(v - top)) : 0.0f;
-    const float sum = wave_sum(renormalize && rank >= top_k ? 0.0f : w);
+    const double w = e < experts ? exp(v - of_lane(v, first)) : 0.0;
+    const double sum = wave_sum64(renormalize && rank >= top_k ? 0.0 : w);
     if (rank < top_k) {
         ids[t * top_k + rank] = e;
-        probs[t * top_k + rank] = w / sum;
+        probs[t * top_k + rank] = (float)(w / sum);
     }
 }
 
