@@ -755,7 +755,7 @@ __global__ __launch_bounds__(W * 64) void moe_down_many_kernel(DownArgs a, float
     }
 }
 
-// y = residual + the partial rows in order. A lane takes two neighbouring columns.
+// y = residual + the partial rows in order. A lane takes four neighbouring columns.
 template <int YDT>
 __global__ __launch_bounds__(256) void moe_combine_kernel(DownArgs a, const float *partial, int parts)
 {
@@ -853,8 +853,8 @@ block_status_t check_experts(const ExpertSizes &s, block_act_t act, float limit)
     return BLOCK_OK;
 }
 
-// Workgroups that share the chosen experts of one block of 128 output columns in the down
-// product, or 0 for the form of a few pairs.
+// Workgroups that share the chosen experts of one block of output columns in the down product,
+// or 0 for the form of a few pairs.
 int down_shares(const ExpertSizes &s);
 
 struct ExpertSpace {

@@ -3,8 +3,8 @@ a matrix product with bias, activation and residual in its epilogue, the router,
 expert layer for a few tokens.
 
 Argument marshalling only: tensors are checked for device, dtype, shape and contiguity and
-their device pointers and a HIP stream are handed to the C functions. No CPU or PyTorch
-fallback.
+their device pointers, which the C functions want at 16 bytes, and a HIP stream are handed over
+(``LayerNorm`` alone copies what lies otherwise). No CPU or PyTorch fallback.
 
 Every call runs on the tensors' own device and on ``stream`` (a ``torch.cuda.Stream`` or a
 raw handle; default: the current stream of that device). Where the C function needs a
@@ -177,7 +177,8 @@ def layer_norm_fwd(x, weight, bias, y, mean=None, rstd=None, *, eps=1e-5, stream
     """y = (x - mean) * rstd * weight + bias per row of x [rows, cols] (bf16, fp16 or fp32), in
     fp32 with one rounding. ``weight`` and ``bias``: [cols] of x's dtype or fp32 (one dtype for
     both), or None. ``mean`` and ``rstd`` (fp32 [rows], both or neither) take the statistics
-    that the backward needs."""
+    that the backward needs. Nothing is recorded for autograd, whatever the inputs require: the
+    gradients come from ``layer_norm_bwd``, or from ``LayerNorm``, which calls both."""
     shape = rows, cols = _rows(x, "x")
     dev, kind = x.get_device(), _kind(x, "x", _ANY)
     first = weight if weight is not None else bias
