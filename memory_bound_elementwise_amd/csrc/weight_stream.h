@@ -58,15 +58,15 @@ __device__ __forceinline__ void three_terms(const u32x4 &h, u32x2 (&term)[3])
 // stride, ... (a step is 64 k; k at and past K count as zeros). All in bytes:
 //   w[i]      resource of tile i: its rows that exist, row_bytes apart (others read zeros)
 //   x, col    resource of the columns, and where the lane's part of them starts in it:
-//     16-bit  16 columns a group: column 16 g + 8 p + lane / 8, at its octet lane % 8, in col[g][p]
-//     WIDE    8 columns of fp32 a group: column 8 g + 4 p + lane / 16, at its four lane % 16. They
-//             become three bf16 terms here. Two instructions take them: column j of acc adds
-//             a twice, column j + 8 b and c (sums of 16 and 24 bits, so products with one
-//             weight are exact); the caller joins the two
+//     16-bit  16 columns a group, two loads: column 8 i + lane / 8, at its octet lane % 8, in col[i]
+//     WIDE    8 columns of fp32 a group, two loads: column 4 i + lane / 16, at its four lane % 16.
+//             They become three bf16 terms here. Two instructions take them: column j of acc
+//             adds a twice, column j + 8 b and c (sums of 16 and 24 bits, so products with
+//             one weight are exact); the caller joins the two
 // stage: kStage<RT, G, WIDE> chunks of shared memory of the wave's own; the wave needs no barrier.
 // SHARE > 1 (WIDE): that many waves, all of the workgroup, call it together with the same columns
-// and k. Each loads and cuts up its part of them, 4 columns at a time in turn, into terms (two sets
-// of set_chunks); there is one barrier a step. stage is then for rows alone, RT * 128 chunks.
+// and k. Each loads and cuts up its part of them, 4 columns at a time in turn (load `wave` + i SHARE
+// of them in col[i]), into terms (two sets of set_chunks); there is one barrier a step. stage is then for rows alone, RT * 128 chunks.
 // (Down product of 7168 x 2048, 8 of 64 experts, each wave for itself and shared: 128 tokens, four
 // waves a CU, 635 and 526 us, 465 with four steps in flight; 64 tokens, eight waves, 324 and 312.
 // With one group a step the barrier costs more: 2048 x 1408, 32 tokens, 87 and 103.)
