@@ -7,6 +7,11 @@
  *   block_moe_route            router product, top-k choice and softmax weights
  *   block_moe_experts          the expert products, activation and combine for a few tokens
  *   block_moe_layer            block_moe_route and block_moe_experts in one call
+ *   block_moe_gate_fwd/_bwd    scores, choice of experts and weights from given logits, and their gradient
+ *   block_moe_route_gated      the router's product with the gate behind it
+ *   block_fp4_*                weights to 4 bits with group scales and back
+ *   block_linear_act_fp4       block_linear_act with such weights
+ *   block_moe_experts_fp4      block_moe_experts with such weights
  *
  * Conventions shared by every call:
  *   - Pointers are caller-owned DEVICE memory on the calling thread's current HIP device,
@@ -59,6 +64,8 @@ typedef enum block_act BLOCK_ENUM_BASE {
     BLOCK_ACT_SQUARED_RELU = 3,  /* max(z, 0)^2 */
     BLOCK_ACT_SWIGLU = 4         /* experts only: silu(min(gate, L)) * clamp(up, -L, L) */
 } block_act_t;
+
+typedef enum block_scores BLOCK_ENUM_BASE { BLOCK_SCORES_SOFTMAX = 0, BLOCK_SCORES_SIGMOID = 1 } block_scores_t;
 
 /*
  * Layer norm of each row, statistics and arithmetic in fp32, one rounding per output:
@@ -156,6 +163,112 @@ block_status_t block_moe_layer(const uint16_t *x, const void *router_weight, blo
                                int renormalize, block_act_t act, float limit,
                                const int32_t *valid_tokens, void *workspace,
                                int64_t workspace_bytes, hipStream_t stream);
+
+/*
+ * Gate: which experts a token goes to and with what weights, from its logits l:
+ *     s_i = 1 / (1 + e^-l_i)  (BLOCK_SCORES_SIGMOID)  or  e^(l_i - l_max) / sum_m e^(l_m - l_max)  (_SOFTMAX)
+ *     c_i = s_i + bias_i                                    what experts are ranked by
+ * The experts lie in `groups` groups of experts / groups neighbours. A group's worth is the sum of
+ * its group_top (1 or 2) largest c; the top_groups groups of largest worth are kept, and of their
+ * experts the top_k of largest c are chosen, in descending order. Weights carry no bias:
+ *     probs_j = scale s_j   or, with renormalize,   scale s_j / sum over the chosen s
+ * Scores, ranks and sums are formed in fp64, each weight is rounded once to fp32. Equal ranks go in
+ * increasing index, NaN before any number. An expert whose logit is -inf is masked: its score is 0
+ * and its rank -inf whatever its bias, so that it is chosen (with weight 0) only where too few
+ * others are left; where the chosen scores are all 0, so are the weights.
+ *   logits: [tokens, experts] of logits_dtype, any of block_dtype_t; bias: fp32 [experts] or NULL;
+ *   ids: int32 [tokens, top_k]; probs: fp32 [tokens, top_k].
+ *   valid_tokens: device int32 scalar or NULL (= tokens), clamped to 0 .. tokens; rows of ids and
+ *   probs at or past it are left as they were.
+ *   0 <= tokens <= 2^24; 1 <= experts <= 1024; 1 <= groups <= 64, a divisor of experts; 1 <=
+ *   top_groups <= groups; group_top <= experts / groups (where groups > 1); 1 <= top_k <= 64 and
+ *   <= top_groups (experts / groups); scale finite.
+ */
+block_status_t block_moe_gate_fwd(const void *logits, block_dtype_t logits_dtype, const float *bias, int32_t *ids,
+                                  float *probs, int64_t tokens, int experts, int top_k, block_scores_t scores,
+                                  int groups, int top_groups, int group_top, int renormalize, float scale,
+                                  const int32_t *valid_tokens, hipStream_t stream);
+
+/*
+ * Gradient of the gate's weights: grad_logits from grad_probs, with the choice held fixed (it has
+ * no gradient; neither has the bias). s and sums as in the forward pass, in fp64, one rounding.
+ * With g_j = scale grad_probs_j and p_j = s_j / sum over the chosen s:
+ *     d_j = g_j, or with renormalize (g_j - sum_m g_m p_m) / sum over the chosen s
+ *     grad_logits_i = s_i (1 - s_i) d_i                 (sigmoid; d_i = 0 where i was not chosen)
+ *     grad_logits_i = s_i (d_i - sum_j s_j d_j)         (softmax)
+ *   ids: as the forward wrote them; an id outside the experts contributes nothing, the same id
+ *   twice contributes twice. grad_logits: [tokens, experts] of logits_dtype, every element of a row
+ *   is written (zeros where all chosen scores are 0); rows at or past valid_tokens are left as
+ *   they were. Sizes as in the forward pass.
+ */
+block_status_t block_moe_gate_bwd(const void *logits, block_dtype_t logits_dtype, const int32_t *ids,
+                                  const float *grad_probs, void *grad_logits, int64_t tokens, int experts, int top_k,
+                                  block_scores_t scores, int renormalize, float scale, const int32_t *valid_tokens,
+                                  hipStream_t stream);
+
+/* block_moe_route's logits (fp64) with the gate behind them; sizes within the limits of both,
+ * workspace as block_moe_route_workspace tells. */
+block_status_t block_moe_route_gated(const uint16_t *x, const void *router_weight, block_dtype_t router_dtype,
+                                     const float *bias, int32_t *ids, float *probs, int64_t tokens, int64_t hidden,
+                                     int experts, int top_k, block_scores_t scores, int groups, int top_groups,
+                                     int group_top, int renormalize, float scale, const int32_t *valid_tokens,
+                                     void *workspace, int64_t workspace_bytes, hipStream_t stream);
+
+/*
+ * Weights in 4 bits with group scales, the open microscaling format: elements of a sign, two bits
+ * of exponent and one of mantissa (0, 0.5, 1, 1.5, 2, 3, 4, 6), a power of two 2^(b - 127) for
+ * each 32 neighbours of a row, b a byte, 255 for NaN. A weight's value is the element times the
+ * power, as a bf16: exact for b <= 252, an infinity where a larger b takes it past bf16's range.
+ * The kernels read matrices [n, k] laid out in tiles of 16 rows by 128 k, the rows and k past the
+ * end filled with zeros; matrices of one call follow each other:
+ *   codes   [matrices][ceil(n / 16)][ceil(k / 128)][64][4] 32-bit words: word j of lane 16 q + r
+ *           holds row r's elements k = 32 j + 8 q + 0 .. 7, the first in the lowest four bits
+ *   scales  [matrices][ceil(n / 16)][ceil(k / 128)][16][4] bytes: byte j of row r is that of the
+ *           elements k = 32 j .. 32 j + 31
+ * k a multiple of 32, 32 .. 2^20; 1 <= n <= 2^20; matrices <= 2^16; at most 2^25 tiles in a call.
+ * block_fp4_codes_bytes / _scales_bytes: bytes of one matrix (0 for sizes that are refused).
+ *
+ * quantize: weight [matrices, n, k] of any block_dtype_t. A group's power is the smallest with
+ *   max |w| < 7 2^power (at least 2^-127, at most 2^125), and each element the nearest one to w /
+ *   2^power, ties to the even code, past 6 to 6: |w - value| <= 2^power / 4 up to 2 2^power, / 2 up to
+ *   4 2^power, 2^power up to 7 2^power. A group of zeros has b = 127; one with an infinity or a NaN b = 255.
+ * pack: from the row-major form of checkpoints: elements [matrices, n, k / 2], two a byte, the
+ *   first in its lower half; exponents [matrices, n, k / 32].
+ * dequantize: the bf16 values, [matrices, n, k].
+ */
+int64_t block_fp4_codes_bytes(int64_t n, int64_t k);
+int64_t block_fp4_scales_bytes(int64_t n, int64_t k);
+block_status_t block_fp4_quantize(const void *weight, block_dtype_t dtype, uint8_t *codes, uint8_t *scales,
+                                  int64_t matrices, int64_t n, int64_t k, hipStream_t stream);
+block_status_t block_fp4_pack(const uint8_t *elements, const uint8_t *exponents, uint8_t *codes, uint8_t *scales,
+                              int64_t matrices, int64_t n, int64_t k, hipStream_t stream);
+block_status_t block_fp4_dequantize(const uint8_t *codes, const uint8_t *scales, uint16_t *weight, int64_t matrices,
+                                    int64_t n, int64_t k, hipStream_t stream);
+
+/*
+ * block_linear_act with x, bias, residual and y in bf16 and W [n, k] in 4 bits (one matrix).
+ * Products are exact, sums and epilogue fp32, one rounding. n a multiple of 8 and k of 32, within
+ * block_linear_act's limits. More than 64 rows multiply the weights' bf16 values, which go to the
+ * workspace; fewer read W once as it is and need no workspace.
+ */
+int64_t block_linear_act_fp4_workspace(int64_t m, int64_t n, int64_t k);
+block_status_t block_linear_act_fp4(const uint16_t *x, const uint8_t *codes, const uint8_t *scales,
+                                    const uint16_t *bias, const uint16_t *residual, uint16_t *y, int64_t m, int64_t n,
+                                    int64_t k, block_act_t act, void *workspace, int64_t workspace_bytes,
+                                    hipStream_t stream);
+
+/*
+ * block_moe_experts with the weights in 4 bits: up_* hold experts matrices [2 inter, hidden] (or
+ * [inter, hidden] for BLOCK_ACT_SQUARED_RELU), down_* experts matrices [hidden, inter]. hidden and
+ * inter multiples of 32, 32 .. 2^16; everything else as there.
+ */
+int64_t block_moe_experts_fp4_workspace(int64_t tokens, int64_t hidden, int64_t inter, int experts, int top_k);
+block_status_t block_moe_experts_fp4(const uint16_t *x, const uint8_t *up_codes, const uint8_t *up_scales,
+                                     const uint8_t *down_codes, const uint8_t *down_scales, const int32_t *ids,
+                                     const float *probs, const uint16_t *residual, void *y, block_dtype_t y_dtype,
+                                     int64_t tokens, int64_t hidden, int64_t inter, int experts, int top_k,
+                                     block_act_t act, float limit, const int32_t *valid_tokens, void *workspace,
+                                     int64_t workspace_bytes, hipStream_t stream);
 
 /* Static text for a status code. Never NULL. */
 const char *moe_block_status_string(block_status_t status);

@@ -35,7 +35,8 @@ LIBS = {
     "swiglu_probs": ["swiglu_probs.hip"],
     "moe_elementwise": ["moe_elementwise.hip"],
     "hbm_probe": ["hbm_probe.hip"],
-    "moe_block": ["block_common.hip", "layer_norm.hip", "linear_act.hip", "moe_layer.hip"],
+    "moe_block": ["block_common.hip", "layer_norm.hip", "linear_act.hip", "moe_layer.hip", "moe_gate.hip",
+                  "fp4_weights.hip", "fp4_products.hip"],
 }
 
 

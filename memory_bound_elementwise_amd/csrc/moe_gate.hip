@@ -1,0 +1,471 @@
+// The gate: scores of a token's experts, the choice among them and their weights, and its
+// gradient, for AMD Instinct MI355X (gfx950). C ABI declared in block/moe_block.h.
+//
+// A token's experts lie spread over L lanes of a wave, V a lane (expert i L + l in lane l), so a
+// wave holds 64 / L tokens. Scores are formed in fp64, as the choice is made between neighbouring
+// values; what has to be seen by other lanes goes through the wave's own shared memory, and no
+// kernel here has a barrier.
+#include <hip/hip_runtime.h>
+
+#include <stdint.h>
+
+#include <cmath>
+
+#include "gate.h"
+#include "route_device.h"
+
+namespace {
+
+using namespace block;
+
+constexpr int kWavesHere = 4;
+constexpr int SRC_PARTS = 3;  // beside the DT_ codes: fp64 partial sums
+
+// What order_key was made of.
+__device__ __forceinline__ double of_key(uint64_t k)
+{
+    return __builtin_bit_cast(double, k >> 63 ? k & ~((uint64_t)1 << 63) : ~k);
+}
+
+template <int kCtrl, int kRowMask = 0xf>
+__device__ __forceinline__ uint64_t dpp_u64(uint64_t v)
+{
+    return __builtin_bit_cast(uint64_t, dpp64<kCtrl, kRowMask>(__builtin_bit_cast(double, v)));
+}
+
+template <int kCtrl, int kRowMask = 0xf>
+__device__ __forceinline__ unsigned dpp_u32(unsigned v)
+{
+    return (unsigned)__builtin_amdgcn_update_dpp(0, (int)v, kCtrl, kRowMask, 0xf, false);
+}
+
+template <typename T>
+__device__ __forceinline__ T larger(T a, T b)
+{
+    return a > b ? a : b;
+}
+
+// Over the L = 16 or 64 lanes of a token, the same in each of them. (A lane that a masked step
+// leaves out compares with 0, the least of both.)
+template <int L>
+__device__ __forceinline__ uint64_t lanes_max(uint64_t v)
+{
+    v = larger(v, dpp_u64<0xB1>(v));
+    v = larger(v, dpp_u64<0x4E>(v));
+    v = larger(v, dpp_u64<0x141>(v));
+    v = larger(v, dpp_u64<0x140>(v));
+    if constexpr (L == 64) {
+        v = larger(v, dpp_u64<0x142, 0xa>(v));
+        v = larger(v, dpp_u64<0x143, 0xc>(v));
+        v = __builtin_bit_cast(uint64_t, of_lane(__builtin_bit_cast(double, v), 63));
+    }
+    return v;
+}
+
+template <int L>
+__device__ __forceinline__ unsigned lanes_max(unsigned v)
+{
+    v = larger(v, dpp_u32<0xB1>(v));
+    v = larger(v, dpp_u32<0x4E>(v));
+    v = larger(v, dpp_u32<0x141>(v));
+    v = larger(v, dpp_u32<0x140>(v));
+    if constexpr (L == 64) {
+        v = larger(v, dpp_u32<0x142, 0xa>(v));
+        v = larger(v, dpp_u32<0x143, 0xc>(v));
+        v = (unsigned)__builtin_amdgcn_readlane((int)v, 63);
+    }
+    return v;
+}
+
+template <int L>
+__device__ __forceinline__ double lanes_sum(double v)
+{
+    if constexpr (L == 64)
+        return wave_sum64(v);
+    v += dpp64<0xB1>(v);
+    v += dpp64<0x4E>(v);
+    v += dpp64<0x141>(v);
+    v += dpp64<0x140>(v);
+    return v;
+}
+
+// The wave's accesses to its shared memory stay in order; this keeps the compiler from moving
+// them across.
+__device__ __forceinline__ void wave_fence() { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront"); }
+
+__device__ __forceinline__ double sigmoid(double v) { return 1.0 / (1.0 + exp(-v)); }
+
+template <int SRC>
+__device__ __forceinline__ double logit(const void *logits, int64_t at, int64_t part, int parts)
+{
+    if constexpr (SRC == SRC_PARTS)
+        return sum_parts(static_cast<const double *>(logits) + at, part, parts);
+    else
+        return (double)load1<SRC>(logits, at);
+}
+
+// s = softmax(v) over a token's lanes; all zeros where every logit is -inf.
+template <int L, int V>
+__device__ __forceinline__ void softmax(const double (&v)[V], double (&s)[V])
+{
+    uint64_t top = 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        top = larger(top, order_key(v[i]));
+    const double m = of_key(lanes_max<L>(top));
+    double sum = 0.0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        s[i] = m == -INFINITY ? 0.0 : exp(v[i] - m);
+        sum += s[i];
+    }
+    sum = lanes_sum<L>(sum);
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        s[i] = sum == 0.0 ? 0.0 : s[i] / sum;
+}
+
+template <int SRC, int L, int V>
+__global__ __launch_bounds__(kWavesHere * 64) void gate_kernel(GateArgs a)
+{
+    constexpr int T = 64 / L;
+    __shared__ uint64_t tables[kWavesHere][T][L * V];
+    __shared__ uint64_t worths[kWavesHere][T][kGateGroups];
+    __shared__ int slots[kWavesHere][T][kGateSlots];
+    const GateRule r = a.rule;
+    const int lane = lane_id(), wave = wave_in_block(), l = lane % L, tl = lane / L;
+    const int first = ((int)blockIdx.x * kWavesHere + wave) * T, live = live_tokens(a.valid, a.tokens);
+    if (first >= live)
+        return;
+    const bool mine = first + tl < live;
+    const int t = mine ? first + tl : first;  // past the last token: the first one again, not stored
+    uint64_t *table = tables[wave][tl], *worth = worths[wave][tl];
+    int *slot = slots[wave][tl];
+    const int64_t row = (int64_t)t * a.experts, part = (int64_t)a.tokens * a.experts;
+
+    double v[V], s[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int e = i * L + l;
+        v[i] = e < a.experts ? logit<SRC>(a.logits, row + e, part, a.parts) : -INFINITY;
+    }
+    if (r.scores == BLOCK_SCORES_SIGMOID) {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            s[i] = sigmoid(v[i]);
+    } else {
+        softmax<L, V>(v, s);
+    }
+    uint64_t key[V];  // of the rank; 0, below every number's, for what cannot be chosen
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int e = i * L + l;
+        const double b = a.bias && e < a.experts ? (double)a.bias[e] : 0.0;
+        key[i] = e < a.experts ? order_key(v[i] == -INFINITY ? v[i] : s[i] + b) : 0;
+    }
+    if (r.groups > 1) {
+        const int size = a.experts / r.groups;
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            table[i * L + l] = key[i];
+        wave_fence();
+        for (int g = l; g < r.groups; g += L) {
+            uint64_t first_key = 0, second_key = 0;
+            for (int m = 0; m < size; ++m) {
+                const uint64_t k = table[g * size + m];
+                second_key = larger(second_key, k < first_key ? k : first_key);
+                first_key = larger(first_key, k);
+            }
+            const double w = of_key(first_key);
+            worth[g] = order_key(r.group_top == 2 ? w + of_key(second_key) : w);
+        }
+        wave_fence();
+        for (int g = l; g < r.groups; g += L) {
+            const uint64_t own = worth[g];
+            int before = 0;
+            for (int o = 0; o < r.groups; ++o)
+                before += worth[o] > own || (worth[o] == own && o < g);
+            slot[g] = before < r.top_groups;
+        }
+        wave_fence();
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int e = i * L + l;
+            if (e < a.experts && !slot[e / size])
+                key[i] = 0;
+        }
+        wave_fence();
+    }
+    for (int j = 0; j < r.top_k; ++j) {
+        uint64_t best = 0;
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            best = larger(best, key[i]);
+        best = lanes_max<L>(best);
+        unsigned from_end = 0;  // the lowest expert of the best, counted from the end
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            from_end = larger(from_end, key[i] == best ? (unsigned)(kGateExperts - (i * L + l)) : 0u);
+        const int e = kGateExperts - (int)lanes_max<L>(from_end);
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (i * L + l == e)
+                key[i] = 0;
+        if (l == 0)
+            slot[j] = e;
+    }
+    wave_fence();
+    double *score = reinterpret_cast<double *>(table);
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        score[i * L + l] = s[i];
+    wave_fence();
+    double sum = 0.0;
+    if (r.renormalize)
+        for (int j = 0; j < r.top_k; ++j)
+            sum += score[slot[j]];
+    for (int j = l; j < r.top_k; j += L) {
+        double p = score[slot[j]];
+        if (r.renormalize)
+            p = sum == 0.0 ? 0.0 : p / sum;
+        if (mine) {
+            a.ids[(int64_t)t * r.top_k + j] = slot[j];
+            a.probs[(int64_t)t * r.top_k + j] = (float)(p * (double)r.scale);
+        }
+    }
+}
+
+struct GateGradArgs {
+    const void *logits;
+    const int *ids;
+    const float *grad_probs;
+    void *grad_logits;
+    const int *valid;
+    int tokens, experts, top_k, scores, renormalize;
+    float scale;
+};
+
+// Gradient of the logits. With g_j = scale grad_probs_j and the chosen scores s_j:
+//     renormalised: p_j = s_j / sum s, v_j = p_j (g_j - sum g p), otherwise v_j = g_j s_j;
+//     sigmoid: v_j (1 - s_j) goes to expert ids_j. softmax: v_j does, and without
+//     renormalisation (DENSE) every expert loses s sum v.
+// Only DENSE reads logits that were not chosen.
+template <int DT, int L, int V, bool DENSE>
+__global__ __launch_bounds__(kWavesHere * 64) void gate_grad_kernel(GateGradArgs a)
+{
+    constexpr int T = 64 / L, Q = kGateSlots / L;
+    __shared__ double tables[kWavesHere][T][L * V];
+    __shared__ double values[kWavesHere][T][kGateSlots];
+    __shared__ int slots[kWavesHere][T][kGateSlots];
+    const int lane = lane_id(), wave = wave_in_block(), l = lane % L, tl = lane / L;
+    const int first = ((int)blockIdx.x * kWavesHere + wave) * T, live = live_tokens(a.valid, a.tokens);
+    if (first >= live)
+        return;
+    const bool mine = first + tl < live;
+    const int t = mine ? first + tl : first;
+    double *table = tables[wave][tl], *value = values[wave][tl];
+    int *slot = slots[wave][tl];
+    const int64_t row = (int64_t)t * a.experts;
+
+    double s[V];
+    if constexpr (DENSE) {
+        double v[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int e = i * L + l;
+            v[i] = e < a.experts ? (double)load1<DT>(a.logits, row + e) : -INFINITY;
+        }
+        softmax<L, V>(v, s);
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            table[i * L + l] = s[i];
+        wave_fence();
+    }
+    int id[Q];
+    double x[Q], g[Q];  // the slot's logit (DENSE: score), its gradient
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+        const int j = q * L + l;
+        id[q] = -1;
+        x[q] = -INFINITY;
+        g[q] = 0.0;
+        if (j < a.top_k) {
+            const int e = a.ids[(int64_t)t * a.top_k + j];
+            if (e >= 0 && e < a.experts) {
+                id[q] = e;
+                x[q] = DENSE ? table[e] : (double)load1<DT>(a.logits, row + e);
+                g[q] = (double)a.scale * (double)a.grad_probs[(int64_t)t * a.top_k + j];
+            }
+        }
+    }
+    wave_fence();
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        table[i * L + l] = 0.0;
+    double out[Q], dot = 0.0;
+    if constexpr (DENSE) {
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+            out[q] = id[q] < 0 ? 0.0 : g[q] * x[q];
+            dot += out[q];
+        }
+        dot = lanes_sum<L>(dot);
+    } else {
+        double p[Q];
+        if (a.scores == BLOCK_SCORES_SIGMOID) {
+#pragma unroll
+            for (int q = 0; q < Q; ++q)
+                p[q] = sigmoid(x[q]);
+        } else {
+            softmax<L, Q>(x, p);
+        }
+        if (a.renormalize) {
+            double sum = 0.0;
+#pragma unroll
+            for (int q = 0; q < Q; ++q)
+                sum += p[q];
+            sum = lanes_sum<L>(sum);
+#pragma unroll
+            for (int q = 0; q < Q; ++q) {
+                p[q] = sum == 0.0 ? 0.0 : p[q] / sum;
+                dot += id[q] < 0 ? 0.0 : g[q] * p[q];
+            }
+            dot = lanes_sum<L>(dot);
+        }
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+            out[q] = p[q] * (g[q] - dot);
+            if (a.scores == BLOCK_SCORES_SIGMOID)
+                out[q] *= sigmoid(-x[q]);
+        }
+    }
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+        slot[q * L + l] = id[q];
+        value[q * L + l] = out[q];
+    }
+    wave_fence();
+    // a lane adds to its own experts alone, in the order of the slots, so that the same id twice
+    // is neither a race nor a choice of order
+    for (int j = 0; j < a.top_k; ++j) {
+        const int e = slot[j];
+        if (e >= 0 && e % L == l)
+            table[e] += value[j];
+    }
+    wave_fence();
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int e = i * L + l;
+        if (mine && e < a.experts)
+            store1<DT>(a.grad_logits, row + e, (float)(table[e] - (DENSE ? s[i] * dot : 0.0)));
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Host
+// ---------------------------------------------------------------------------
+constexpr int kFewTokens = 1024;  // a wave each
+
+unsigned groups_of(int64_t tokens, int lanes) { return (unsigned)ceil_div(tokens, kWavesHere * (64 / lanes)); }
+
+template <int SRC>
+block_status_t run_gate(const GateArgs &a, hipStream_t st)
+{
+    const dim3 threads(kWavesHere * 64);
+    const unsigned few = groups_of(a.tokens, 64), many = groups_of(a.tokens, 16);
+    if (a.experts <= 64)
+        return a.tokens <= kFewTokens ? launch(gate_kernel<SRC, 64, 1>, dim3(few), threads, 0, st, a)
+                                      : launch(gate_kernel<SRC, 16, 4>, dim3(many), threads, 0, st, a);
+    if (a.experts <= 256)
+        return a.tokens <= kFewTokens ? launch(gate_kernel<SRC, 64, 4>, dim3(few), threads, 0, st, a)
+                                      : launch(gate_kernel<SRC, 16, 16>, dim3(many), threads, 0, st, a);
+    return launch(gate_kernel<SRC, 64, 16>, dim3(few), threads, 0, st, a);
+}
+
+template <int DT, bool DENSE>
+block_status_t run_gate_grad(const GateGradArgs &a, hipStream_t st)
+{
+    const dim3 threads(kWavesHere * 64);
+    const unsigned few = groups_of(a.tokens, 64), many = groups_of(a.tokens, 16);
+    if (a.experts <= 64)
+        return a.tokens <= kFewTokens ? launch(gate_grad_kernel<DT, 64, 1, DENSE>, dim3(few), threads, 0, st, a)
+                                      : launch(gate_grad_kernel<DT, 16, 4, DENSE>, dim3(many), threads, 0, st, a);
+    if (a.experts <= 256)
+        return a.tokens <= kFewTokens ? launch(gate_grad_kernel<DT, 64, 4, DENSE>, dim3(few), threads, 0, st, a)
+                                      : launch(gate_grad_kernel<DT, 16, 16, DENSE>, dim3(many), threads, 0, st, a);
+    return launch(gate_grad_kernel<DT, 64, 16, DENSE>, dim3(few), threads, 0, st, a);
+}
+
+template <int DT>
+block_status_t run_gate_grad(const GateGradArgs &a, hipStream_t st)
+{
+    return a.scores == BLOCK_SCORES_SOFTMAX && !a.renormalize ? run_gate_grad<DT, true>(a, st)
+                                                              : run_gate_grad<DT, false>(a, st);
+}
+
+bool good_tokens(int64_t tokens) { return tokens >= 0 && tokens <= (1 << 24); }
+
+int64_t size_of(block_dtype_t dt) { return dt == BLOCK_FP32 ? 4 : 2; }
+
+bool good_dtype(block_dtype_t dt) { return dt == BLOCK_BF16 || dt == BLOCK_FP16 || dt == BLOCK_FP32; }
+
+}  // namespace
+
+namespace block {
+
+block_status_t gate_of_parts(const GateArgs &a, hipStream_t stream) { return run_gate<SRC_PARTS>(a, stream); }
+
+}  // namespace block
+
+extern "C" {
+
+block_status_t block_moe_gate_fwd(const void *logits, block_dtype_t logits_dtype, const float *bias, int32_t *ids,
+                                  float *probs, int64_t tokens, int experts, int top_k, block_scores_t scores,
+                                  int groups, int top_groups, int group_top, int renormalize, float scale,
+                                  const int32_t *valid_tokens, hipStream_t stream)
+{
+    const GateRule rule = {top_k, (int)scores, groups, top_groups, group_top, renormalize, scale};
+    if (!good_tokens(tokens) || !good_gate(rule, experts) || !good_dtype(logits_dtype))
+        return BLOCK_ERR_INVALID_ARG;
+    if (tokens == 0)
+        return BLOCK_OK;
+    if (!logits || !ids || !probs)
+        return BLOCK_ERR_INVALID_ARG;
+    if (misaligned(logits, 16) || misaligned(bias, 4) || misaligned(ids, 4) || misaligned(probs, 4) ||
+        misaligned(valid_tokens, 4))
+        return BLOCK_ERR_ALIGNMENT;
+    if (any_overlap<2, 3>({{ids, tokens * top_k * 4}, {probs, tokens * top_k * 4}},
+                          {{logits, tokens * experts * size_of(logits_dtype)}, {bias, experts * (int64_t)4}, {valid_tokens, 4}}))
+        return BLOCK_ERR_INVALID_ARG;
+    const GateArgs a = {logits, bias, ids, probs, valid_tokens, (int)tokens, experts, 1, rule};
+    if (logits_dtype == BLOCK_FP32)
+        return run_gate<DT_F32>(a, stream);
+    return logits_dtype == BLOCK_BF16 ? run_gate<DT_BF16>(a, stream) : run_gate<DT_F16>(a, stream);
+}
+
+block_status_t block_moe_gate_bwd(const void *logits, block_dtype_t logits_dtype, const int32_t *ids,
+                                  const float *grad_probs, void *grad_logits, int64_t tokens, int experts, int top_k,
+                                  block_scores_t scores, int renormalize, float scale, const int32_t *valid_tokens,
+                                  hipStream_t stream)
+{
+    if (!good_tokens(tokens) || experts < 1 || experts > kGateExperts || top_k < 1 || top_k > kGateSlots ||
+        !good_gate_scores((int)scores, scale) || !good_dtype(logits_dtype))
+        return BLOCK_ERR_INVALID_ARG;
+    if (tokens == 0)
+        return BLOCK_OK;
+    if (!logits || !ids || !grad_probs || !grad_logits)
+        return BLOCK_ERR_INVALID_ARG;
+    if (misaligned(logits, 16) || misaligned(ids, 4) || misaligned(grad_probs, 4) || misaligned(grad_logits, 16) ||
+        misaligned(valid_tokens, 4))
+        return BLOCK_ERR_ALIGNMENT;
+    const int64_t all = tokens * experts * size_of(logits_dtype), pairs = tokens * top_k * 4;
+    if (any_overlap<1, 4>({{grad_logits, all}}, {{logits, all}, {ids, pairs}, {grad_probs, pairs}, {valid_tokens, 4}}))
+        return BLOCK_ERR_INVALID_ARG;
+    const GateGradArgs a = {logits, ids, grad_probs, grad_logits, valid_tokens, (int)tokens, experts, top_k,
+                            (int)scores, renormalize, scale};
+    if (logits_dtype == BLOCK_FP32)
+        return run_gate_grad<DT_F32>(a, stream);
+    return logits_dtype == BLOCK_BF16 ? run_gate_grad<DT_BF16>(a, stream) : run_gate_grad<DT_F16>(a, stream);
+}
+
+}  // extern "C"

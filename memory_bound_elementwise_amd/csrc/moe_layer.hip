@@ -16,22 +16,13 @@
 #include <cmath>
 
 #include "block_host.h"
+#include "gate.h"
+#include "route_device.h"
 #include "weight_stream.h"
 
 namespace {
 
 using namespace block;
-
-constexpr int kMaxPairs = 1024;    // tokens * top_k
-constexpr int kMaxExperts = 1024;
-
-__device__ __forceinline__ int live_tokens(const int *valid, int tokens)
-{
-    if (!valid)
-        return tokens;
-    const int v = *valid;
-    return v < 0 ? 0 : (v < tokens ? v : tokens);
-}
 
 // ---------------------------------------------------------------------------
 // Router
@@ -182,63 +173,6 @@ __global__ __launch_bounds__(kRouteWaves * 64) void route_logits_few_kernel(cons
         partial[((int64_t)blockIdx.z * tokens + t) * experts + e0 + i] = sum;
 }
 
-// A double as an unsigned integer in the same order; +0 and -0 alike, NaN above all.
-__device__ __forceinline__ uint64_t order_key(double v)
-{
-    if (v != v)
-        return ~(uint64_t)0;
-    const uint64_t b = __builtin_bit_cast(uint64_t, v + 0.0);
-    return b >> 63 ? ~b : b | (uint64_t)1 << 63;
-}
-
-template <int kCtrl, int kRowMask = 0xf>
-__device__ __forceinline__ double dpp64(double v)
-{
-    const uint64_t b = __builtin_bit_cast(uint64_t, v);
-    const int lo = __builtin_amdgcn_update_dpp(0, (int)(unsigned)b, kCtrl, kRowMask, 0xf, false);
-    const int hi = __builtin_amdgcn_update_dpp(0, (int)(unsigned)(b >> 32), kCtrl, kRowMask, 0xf, false);
-    return __builtin_bit_cast(double, (uint64_t)(unsigned)hi << 32 | (unsigned)lo);
-}
-
-// The value that lane `from` (the same in all lanes) holds.
-__device__ __forceinline__ double of_lane(double v, int from)
-{
-    const uint64_t b = __builtin_bit_cast(uint64_t, v);
-    const unsigned lo = __builtin_amdgcn_readlane((int)(unsigned)b, from);
-    const unsigned hi = __builtin_amdgcn_readlane((int)(unsigned)(b >> 32), from);
-    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
-}
-
-// wave_sum in fp64. The softmax stays in fp64 until its weights are rounded: with the difference
-// of two logits rounded to fp32 a weight e^-d was off by d steps.
-__device__ __forceinline__ double wave_sum64(double v)
-{
-    v += dpp64<0xB1>(v);
-    v += dpp64<0x4E>(v);
-    v += dpp64<0x141>(v);
-    v += dpp64<0x140>(v);
-    v += dpp64<0x142, 0xa>(v);
-    v += dpp64<0x143, 0xc>(v);
-    return of_lane(v, 63);
-}
-
-// The sum of a logit's parts in order, eight loads at a time (a loop of single loads waits
-// for each: 3 us for seven).
-__device__ __forceinline__ double sum_parts(const double *mine, int64_t part, int parts)
-{
-    double v = 0.0;
-    for (int s = 0; s < parts; s += 8) {
-        double p[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            p[i] = mine[(s + i < parts ? s + i : 0) * part];
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            v += s + i < parts ? p[i] : 0.0;
-    }
-    return v;
-}
-
 // One workgroup a token, a thread an expert: its logit is the sum of its parts in order, its
 // rank the number of experts before it (a larger logit, or an equal one and a lower index).
 // Counting against all others costs less than top_k reductions over the wave one after the
@@ -326,22 +260,6 @@ __device__ __forceinline__ void choose_in_wave(const double *partial, int t, int
 // ---------------------------------------------------------------------------
 // Experts
 // ---------------------------------------------------------------------------
-// The pairs (token * top_k + slot) below `pairs` whose id is e, in increasing order, into
-// list; returns their number. One wave, all lanes.
-__device__ __forceinline__ int list_pairs(const int *ids, int pairs, int e, uint16_t *list)
-{
-    const int lane = lane_id();
-    int n = 0;
-    for (int p0 = 0; p0 < pairs; p0 += 64) {
-        const bool is = p0 + lane < pairs && ids[p0 + lane] == e;
-        const uint64_t m = __ballot(is);
-        if (is)
-            list[n + __popcll(m & (((uint64_t)1 << lane) - 1))] = (uint16_t)(p0 + lane);
-        n += __popcll(m);
-    }
-    return n;
-}
-
 struct UpArgs {
     const uint16_t *x, *w;
     const int *ids;
@@ -1046,6 +964,38 @@ block_status_t block_moe_route(const uint16_t *x, const void *router_weight, blo
                           {{x, tokens * hidden * 2}, {router_weight, n_experts * hidden * wsize}, {valid_tokens, 4}}))
         return BLOCK_ERR_INVALID_ARG;
     return route(x, router_weight, router_dtype, ids, probs, s, top_k, renormalize, valid_tokens, workspace, stream);
+}
+
+block_status_t block_moe_route_gated(const uint16_t *x, const void *router_weight, block_dtype_t router_dtype,
+                                     const float *bias, int32_t *ids, float *probs, int64_t tokens, int64_t hidden,
+                                     int n_experts, int top_k, block_scores_t scores, int groups, int top_groups,
+                                     int group_top, int renormalize, float scale, const int32_t *valid_tokens,
+                                     void *workspace, int64_t workspace_bytes, hipStream_t stream)
+{
+    const RouteSizes s = {tokens, hidden, n_experts};
+    const GateRule rule = {top_k, (int)scores, groups, top_groups, group_top, renormalize, scale};
+    if (!good_route(s) || !good_gate(rule, n_experts) || (router_dtype != BLOCK_BF16 && router_dtype != BLOCK_FP32))
+        return BLOCK_ERR_INVALID_ARG;
+    if (hidden % 8)
+        return BLOCK_ERR_ALIGNMENT;
+    if (tokens == 0)
+        return BLOCK_OK;
+    const int64_t need = route_bytes(s), wsize = router_dtype == BLOCK_FP32 ? 4 : 2;
+    if (!x || !router_weight || !ids || !probs || !workspace || workspace_bytes < need)
+        return BLOCK_ERR_INVALID_ARG;
+    if (misaligned(x, 16) || misaligned(router_weight, 16) || misaligned(bias, 4) || misaligned(ids, 4) ||
+        misaligned(probs, 4) || misaligned(valid_tokens, 4) || misaligned(workspace, 16))
+        return BLOCK_ERR_ALIGNMENT;
+    if (any_overlap<3, 4>({{ids, tokens * top_k * 4}, {probs, tokens * top_k * 4}, {workspace, need}},
+                          {{x, tokens * hidden * 2},
+                           {router_weight, n_experts * hidden * wsize},
+                           {bias, n_experts * (int64_t)4},
+                           {valid_tokens, 4}}))
+        return BLOCK_ERR_INVALID_ARG;
+    if (const block_status_t r = route_logits(x, router_weight, router_dtype, s, valid_tokens, workspace, stream))
+        return r;
+    const GateArgs a = {workspace, bias, ids, probs, valid_tokens, (int)tokens, n_experts, (int)route_parts(s), rule};
+    return gate_of_parts(a, stream);
 }
 
 int64_t block_moe_experts_workspace(int64_t tokens, int64_t hidden, int64_t inter, int n_experts, int top_k)

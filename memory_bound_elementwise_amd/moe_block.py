@@ -29,6 +29,7 @@ BLOCK_BF16, BLOCK_FP16, BLOCK_FP32 = 0, 1, 2
 _TORCH = {torch.bfloat16: BLOCK_BF16, torch.float16: BLOCK_FP16, torch.float32: BLOCK_FP32}
 ACTIVATIONS = {None: 0, "none": 0, "silu": 1, "gelu": 2, "squared_relu": 3}
 EXPERT_ACTIVATIONS = {"squared_relu": 3, "swiglu": 4}
+SCORES = {"softmax": 0, "sigmoid": 1}
 
 _lock = threading.Lock()
 _lib = None
@@ -47,6 +48,20 @@ _SIGS = {
     "block_moe_layer_workspace": [_i64, _i64, _i64, _int, _int],
     "block_moe_layer": [_vp, _vp, _int, _vp, _vp, _vp, _vp, _int, _vp, _vp, _i64, _i64, _i64, _int, _int, _int,
                         _int, _f32, _vp, _vp, _i64, _vp],
+    "block_moe_gate_fwd": [_vp, _int, _vp, _vp, _vp, _i64, _int, _int, _int, _int, _int, _int, _int, _f32, _vp, _vp],
+    "block_moe_gate_bwd": [_vp, _int, _vp, _vp, _vp, _i64, _int, _int, _int, _int, _f32, _vp, _vp],
+    "block_moe_route_gated": [_vp, _vp, _int, _vp, _vp, _vp, _i64, _i64, _int, _int, _int, _int, _int, _int, _int,
+                              _f32, _vp, _vp, _i64, _vp],
+    "block_fp4_codes_bytes": [_i64, _i64],
+    "block_fp4_scales_bytes": [_i64, _i64],
+    "block_fp4_quantize": [_vp, _int, _vp, _vp, _i64, _i64, _i64, _vp],
+    "block_fp4_pack": [_vp, _vp, _vp, _vp, _i64, _i64, _i64, _vp],
+    "block_fp4_dequantize": [_vp, _vp, _vp, _i64, _i64, _i64, _vp],
+    "block_linear_act_fp4_workspace": [_i64, _i64, _i64],
+    "block_linear_act_fp4": [_vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _int, _vp, _i64, _vp],
+    "block_moe_experts_fp4_workspace": [_i64, _i64, _i64, _int, _int],
+    "block_moe_experts_fp4": [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _int, _i64, _i64, _i64, _int, _int, _int,
+                              _f32, _vp, _vp, _i64, _vp],
     "moe_block_status_string": [_int],
     "moe_block_last_hip_error": [],
     "moe_block_abi_version": [],
@@ -77,7 +92,7 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
             f = getattr(lib, name)
             f.argtypes = args
             f.restype = (ctypes.c_char_p if name == "moe_block_status_string" else
-                         _i64 if name.endswith("_workspace") else _int)
+                         _i64 if name.endswith(("_workspace", "_bytes")) else _int)
         if lib.moe_block_abi_version() != 1:
             raise RuntimeError("libmoe_block.so ABI version mismatch")
         if path is None:
@@ -317,22 +332,44 @@ def _scalar(valid_tokens, dev):
     return None if valid_tokens is None else _tensor(valid_tokens.reshape(-1), "valid_tokens", _I32, (1,), dev)
 
 
-def moe_route(x, router_weight, ids, probs, *, renormalize=False, valid_tokens=None, workspace=None, stream=None):
-    """The top experts of each token of x (bf16 [tokens, hidden]) and their softmax weights:
-    logits = x @ router_weight.T (bf16 or fp32 [experts, hidden]) in fp64, the ids.shape[1]
-    largest in descending order with ties to the lower expert into ``ids`` (int32 [tokens,
-    top_k]) and their weights, of all experts' or (``renormalize``) of the chosen ones', into
-    ``probs`` (fp32). Rows at or past ``valid_tokens`` (device int32) are left as they were."""
+def _scores(scores):
+    if scores not in SCORES:
+        raise ValueError(f"unknown scores {scores!r}")
+    return SCORES[scores]
+
+
+def _gate_rule(scores, groups, top_groups, group_top, renormalize, scale):
+    """The gate's arguments as the C functions take them in a row."""
+    return (_scores(scores), groups, groups if top_groups is None else top_groups, group_top, bool(renormalize), scale)
+
+
+def moe_route(x, router_weight, ids, probs, *, renormalize=False, scores="softmax", bias=None, groups=1,
+              top_groups=None, group_top=1, scale=1.0, valid_tokens=None, workspace=None, stream=None):
+    """The top experts of each token of x (bf16 [tokens, hidden]) and their weights: logits = x @
+    router_weight.T (bf16 or fp32 [experts, hidden]) in fp64, the ids.shape[1] largest scores in
+    descending order with ties to the lower expert into ``ids`` (int32 [tokens, top_k]) and their
+    weights, of all experts' or (``renormalize``) of the chosen ones', into ``probs`` (fp32).
+    ``scores``, ``bias``, ``groups``, ``top_groups``, ``group_top`` and ``scale``: the gate's, as
+    for ``moe_gate_fwd``. Rows at or past ``valid_tokens`` (device int32) are left as they were."""
     tokens, hidden = _rows(x, "x")
     experts = _rows(router_weight, "router_weight")[0]
     top_k = _rows(ids, "ids")[1]
     _forward_only("moe_route", x, router_weight)
     dev, rkind = x.get_device(), _kind(router_weight, "router_weight", (_BF16, _F32))
-    args = (_tensor(x, "x", _BF16, (tokens, hidden), dev),
-            _tensor(router_weight, "router_weight", rkind, (experts, hidden), dev), _TORCH[rkind],
-            _tensor(ids, "ids", _I32, (tokens, top_k), dev), _tensor(probs, "probs", _F32, (tokens, top_k), dev),
-            tokens, hidden, experts, top_k, bool(renormalize), _scalar(valid_tokens, dev))
-    _call("block_moe_route", x, stream, args, workspace, moe_route_workspace(tokens, hidden, experts))
+    px, pr = (_tensor(x, "x", _BF16, (tokens, hidden), dev),
+              _tensor(router_weight, "router_weight", rkind, (experts, hidden), dev))
+    to = (_tensor(ids, "ids", _I32, (tokens, top_k), dev), _tensor(probs, "probs", _F32, (tokens, top_k), dev), tokens,
+          hidden, experts, top_k)
+    need = moe_route_workspace(tokens, hidden, experts)
+    if (scores == "softmax" and bias is None and scale == 1.0 and groups == 1 and top_groups in (None, 1) and
+            group_top == 1):  # the logits' own order
+        _call("block_moe_route", x, stream, (px, pr, _TORCH[rkind], *to, bool(renormalize), _scalar(valid_tokens, dev)),
+              workspace, need)
+    else:
+        _call("block_moe_route_gated", x, stream,
+              (px, pr, _TORCH[rkind], _tensor(bias, "bias", _F32, (experts,), dev), *to,
+               *_gate_rule(scores, groups, top_groups, group_top, renormalize, scale), _scalar(valid_tokens, dev)),
+              workspace, need)
     return ids, probs
 
 
