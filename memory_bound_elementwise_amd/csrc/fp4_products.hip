@@ -89,6 +89,110 @@ __device__ __forceinline__ void stream_products(f32x4 (&acc)[RT][G], const Tiles
     }
 }
 
+// A wave's next tiles of RT row blocks, in flight.
+template <int RT>
+struct Ahead {
+    u32x4 codes[RT];
+    uint32_t scales[RT];
+    __device__ __forceinline__ void load(const Tiles (&w)[RT], int t)
+    {
+        const int lane = lane_id();
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {  // a tile past the last reads zeros
+            codes[i] = __builtin_amdgcn_raw_buffer_load_b128(w[i].codes, lane * 16, t * kFp4Codes, kLoadAux);
+            scales[i] = __builtin_amdgcn_raw_buffer_load_b32(w[i].scales, lane % 16 * 4, t * kFp4Scales, 0);
+        }
+    }
+};
+
+// A barrier that waits for the wave's accesses to shared memory, but not for its loads from memory.
+// Nothing is moved across.
+__device__ __forceinline__ void sync_shared()
+{
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0)
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_sched_barrier(0);
+}
+
+// The same over all k with the columns shared: W waves, each with rows of its own, walk k together. A
+// wave loads its part of the columns' next 128 k (load i of wave w takes columns 4 (w + i W) ..+4 of
+// them: col[i], the start of column lane / 16 of these plus 16 (lane % 16) bytes), and they meet in
+// shared memory: xs, two sets of G * 256 chunks of 16 bytes, used in turn, so that one barrier a step
+// is enough. Chunk c of column i lies at c ^ (i % 8), so that lanes that read one chunk of eight
+// columns fall into different banks. even, odd: the first two steps' tiles, loaded by the caller.
+// groups: those of the G that have columns.
+template <int G, int W>
+constexpr int kOwnLoads = (4 * G + W - 1) / W;
+
+template <int RT, int G, int W>
+__device__ __forceinline__ void walk_products(f32x4 (&acc)[RT][G], const Tiles (&w)[RT], Ahead<RT> &even, Ahead<RT> &odd,
+                                              rsrc_t x, const uint32_t (&col)[kOwnLoads<G, W>], int K, int groups, u32x4 *xs)
+{
+    constexpr int kLoads = kOwnLoads<G, W>;
+    struct Columns {
+        u32x4 v[kLoads];
+    };
+    const int lane = lane_id(), wave = wave_in_block(), k_tiles = (K + kFp4K - 1) / kFp4K;
+    const int i16 = lane % 16, q = lane / 16;
+    auto fetch = [&](Columns &c, int t) {
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i)
+            c.v[i] = __builtin_amdgcn_raw_buffer_load_b128(x, t * kFp4K + i16 * 8 < K ? col[i] : kNowhere, t * kFp4K * 2, 0);
+    };
+    static_assert(W % 2 == 0, "the columns of a wave's loads have one c % 8");
+    const int put = (4 * wave + q) * 16 + (i16 ^ (4 * wave + q) % 8);  // load i: 64 W i further
+    const int get = i16 * 16 + (q ^ i16 % 8), get_odd = get ^ 4;       // word j: 8 (j / 2) further
+    auto multiply = [&](const Ahead<RT> &tiles, const Columns &c, u32x4 *set) {
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i)
+            if (wave + i * W < 4 * groups)
+                set[put + i * W * 64] = c.v[i];
+        // Everyone's columns of this step are there after the barrier. Those of the next go into the
+        // other set, and into this one again only after the next barrier, which a wave reaches when
+        // its reads below have come.
+        sync_shared();
+        u32x4 b[2][G];  // the next word's columns are read beside a word's products
+        auto read = [&](int j) __attribute__((always_inline)) {
+#pragma unroll
+            for (int g = 0; g < G; ++g)
+                if (g == 0 || g < groups)
+                    b[j % 2][g] = set[(j % 2 ? get_odd : get) + j / 2 * 8 + g * 256];
+        };
+        read(0);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (j < 3)
+                read(j + 1);
+            u32x4 a[RT];
+#pragma unroll
+            for (int i = 0; i < RT; ++i)
+                a[i] = fp4_widen(tiles.codes[i][j], fp4_scale(tiles.scales[i], j));
+#pragma unroll
+            for (int g = 0; g < G; ++g)
+                if (g == 0 || g < groups)
+#pragma unroll
+                    for (int i = 0; i < RT; ++i)
+                        acc[i][g] = mfma16<DT_BF16>(a[i], b[j % 2][g], acc[i][g]);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    };
+    Columns c_even, c_odd;
+    fetch(c_even, 0);
+    fetch(c_odd, 1);
+    for (int t = 0; t < k_tiles; t += 2) {  // whole turns of two, so calls use the sets in turn too
+        multiply(even, c_even, xs);
+        even.load(w, t + 2);
+        fetch(c_even, t + 2);
+        multiply(odd, c_odd, xs + G * 256);
+        odd.load(w, t + 3);
+        fetch(c_odd, t + 3);
+    }
+}
+
 template <int RT, int G>
 __device__ __forceinline__ void clear(f32x4 (&acc)[RT][G])
 {
@@ -197,26 +301,64 @@ __device__ __forceinline__ void three_terms(float h, uint16_t (&term)[3])
     term[2] = finite ? (uint16_t)(__float_as_uint(third) >> 16) : 0;
 }
 
-// The workgroup's expert (blockIdx.y: a pair, which stands for its expert if no earlier one has
-// the same, or an expert, whichever is fewer) and its pairs; returns their number.
-__device__ __forceinline__ int expert_pairs(const ExpertArgs &a, int pairs, int &e, uint16_t *list, int &count)
+// Four neighbours' terms, one plane after the other.
+__device__ __forceinline__ void store_terms(const f32x4 &h, uint16_t *to, int64_t plane)
 {
-    e = blockIdx.y;
+    uint16_t t[4][3];
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+        three_terms(h[r], t[r]);
+#pragma unroll
+    for (int q = 0; q < 3; ++q)
+        *reinterpret_cast<u32x2 *>(to + q * plane) =
+            u32x2{t[0][q] | (uint32_t)t[1][q] << 16, t[2][q] | (uint32_t)t[3][q] << 16};
+}
+
+// The workgroup's expert: blockIdx.y is a pair, which stands for its expert if no earlier one has the
+// same, or an expert, whichever is fewer. -1: none.
+__device__ __forceinline__ int own_expert(const ExpertArgs &a, int pairs)
+{
+    int e = blockIdx.y;
     if (a.by_pair) {
-        if (e >= pairs)
-            return 0;
-        e = a.ids[e];
-        if (e < 0 || e >= a.experts)
-            return 0;
+        e = e < pairs ? a.ids[e] : -1;
+        if (e >= a.experts)
+            e = -1;
     }
-    if (wave_in_block() == 0) {
-        const int n = list_pairs(a.ids, pairs, e, list);
-        if (lane_id() == 0)
-            count = n;
+    return __builtin_amdgcn_readfirstlane(e);
+}
+
+// The pairs (token * top_k + slot) below `pairs` whose id is e, in increasing order, into list;
+// returns their number, or 0 where an earlier workgroup has them. W waves look through ids
+// together, 64 pairs a chunk. counts: of the chunks.
+template <int W>
+__device__ __forceinline__ int expert_pairs(const ExpertArgs &a, int pairs, int e, uint16_t *list, int (&counts)[kMaxPairs / 64])
+{
+    constexpr int kOwn = kMaxPairs / 64 / W;
+    const int lane = lane_id(), wave = wave_in_block(), chunks = (pairs + 63) / 64;
+    uint64_t found[kOwn];
+    int id[kOwn];
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i) {
+        const int p = (wave + i * W) * 64 + lane;
+        id[i] = p < pairs ? a.ids[p] : -1;
     }
-    __syncthreads();
-    const int n = count;
-    return n == 0 || (a.by_pair && list[0] != (int)blockIdx.y) ? 0 : n;
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i) {
+        found[i] = __ballot(id[i] == e);
+        if (lane == 0)
+            counts[wave + i * W] = __popcll(found[i]);
+    }
+    sync_shared();
+    int n = 0;
+    for (int c = 0; c < chunks; ++c) {
+#pragma unroll
+        for (int i = 0; i < kOwn; ++i)
+            if (c == wave + i * W && id[i] == e)
+                list[n + __popcll(found[i] & (((uint64_t)1 << lane) - 1))] = (uint16_t)(c * 64 + lane);
+        n += counts[c];
+    }
+    sync_shared();
+    return n == 0 || (a.by_pair && list[0] != (int)blockIdx.y) ? 0 : __builtin_amdgcn_readfirstlane(n);
 }
 
 template <int ACT, int G>
@@ -265,10 +407,11 @@ __global__ __launch_bounds__(kWaves * 64) void fp4_up_kernel(ExpertArgs a)
 {
     __shared__ f32x4 joined[kWaves * 2 * G * 64];
     __shared__ uint16_t list[kMaxPairs];
-    __shared__ int count;
-    const int pairs = live_tokens(a.valid, a.tokens) * a.top_k;
-    int e;
-    const int n = expert_pairs(a, pairs, e, list, count);
+    __shared__ int counts[kMaxPairs / 64];
+    const int pairs = live_tokens(a.valid, a.tokens) * a.top_k, e = own_expert(a, pairs);
+    if (e < 0)
+        return;
+    const int n = expert_pairs<kWaves>(a, pairs, e, list, counts);
     for (int p = 0; p < n; p += G * 16) {
         const int m = n - p < G * 16 ? n - p : G * 16;
         if (G == 1 || m <= 16)
@@ -277,6 +420,90 @@ __global__ __launch_bounds__(kWaves * 64) void fp4_up_kernel(ExpertArgs a)
             up_pass<ACT, G < 2 ? 1 : 2>(a, e, list + p, m, joined);
         else
             up_pass<ACT, G>(a, e, list + p, m, joined);
+    }
+}
+
+// Up products where experts have many tokens: a workgroup takes one expert and kManyWaves times two
+// row tiles, which walk k together (walk_products), so that x is read once for all of them. A
+// wave has gate and up of 16 columns of the activation, or 32 columns of one product.
+constexpr int kManyWaves = 8;
+
+template <int ACT, int G>
+__device__ __forceinline__ void up_many_pass(const ExpertArgs &a, const Tiles (&w)[2], Ahead<2> &even, Ahead<2> &odd,
+                                             int c0, const uint16_t *list, int n, u32x4 *xs)
+{
+    constexpr int W = kManyWaves, kLoads = kOwnLoads<G, W>;
+    const int lane = lane_id(), wave = wave_in_block();
+    const rsrc_t x = make_rsrc(a.x, (uint32_t)a.tokens * (uint32_t)a.hidden * 2u);
+    uint32_t col[kLoads];
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+        const int s = 4 * (wave + i * W) + lane / 16;
+        col[i] = s < n ? (uint32_t)(list[s] / a.top_k) * (uint32_t)a.hidden * 2u + lane % 16 * 16 : kNowhere;
+    }
+    f32x4 acc[2][G];
+    clear(acc);
+    walk_products<2, G, W>(acc, w, even, odd, x, col, a.hidden, (n + 15) / 16, xs);
+    if (c0 >= a.inter)
+        return;
+    const int64_t plane = (int64_t)a.tokens * a.top_k * a.inter;
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+        const int s = g * 16 + lane % 16;
+        if (s >= n)
+            continue;
+        const int pair = list[s];
+        const float p = a.probs[pair];
+        uint16_t *to = a.h + (int64_t)pair * a.inter + c0 + lane / 16 * 4;
+        if constexpr (ACT == ACT_SWIGLU) {
+            f32x4 h;
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                h[r] = swiglu(acc[0][g][r], acc[1][g][r], a.limit) * p;
+            store_terms(h, to, plane);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                f32x4 h;
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    h[r] = squared_relu(acc[i][g][r]) * p;
+                store_terms(h, to + 16 * i, plane);
+            }
+        }
+    }
+}
+
+template <int ACT, int G>
+__global__ __launch_bounds__(kManyWaves * 64, G == 1 ? 8 : 4) void fp4_up_many_kernel(ExpertArgs a)
+{
+    __shared__ u32x4 xs[2 * G * 256];
+    __shared__ uint16_t list[kMaxPairs];
+    __shared__ int counts[kMaxPairs / 64];
+    const int pairs = live_tokens(a.valid, a.tokens) * a.top_k, e = own_expert(a, pairs);
+    if (e < 0)
+        return;
+    constexpr int kCols = ACT == ACT_SWIGLU ? 16 : 32;
+    const int c0 = (blockIdx.x * kManyWaves + wave_in_block()) * kCols, blocks = a.inter / 16;
+    const int k_tiles = c0 < a.inter ? (a.hidden + kFp4K - 1) / kFp4K : 0;  // past the end: none, but its part of x
+    Tiles w[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        w[i] = tiles_of(a.up_codes, a.up_scales,
+                        k_tiles == 0 ? 0 : (ACT == ACT_SWIGLU ? ((int64_t)e * 2 + i) * blocks : (int64_t)e * blocks + i) + c0 / 16,
+                        k_tiles);
+    Ahead<2> even, odd;  // on their way while the pairs are looked for
+    even.load(w, 0);
+    odd.load(w, 1);
+    const int n = expert_pairs<kManyWaves>(a, pairs, e, list, counts);
+    for (int p = 0; p < n; p += G * 16) {
+        const int m = n - p < G * 16 ? n - p : G * 16;
+        if (p > 0) {
+            sync_shared();  // the columns lie elsewhere in xs now
+            even.load(w, 0);
+            odd.load(w, 1);
+        }
+        up_many_pass<ACT, G>(a, w, even, odd, c0, list + p, m, xs);
     }
 }
 
@@ -317,10 +544,11 @@ __global__ __launch_bounds__(kWaves * 64) void fp4_down_kernel(ExpertArgs a)
 {
     __shared__ f32x4 joined[kWaves * G * 64];
     __shared__ uint16_t list[kMaxPairs];
-    __shared__ int count;
-    const int pairs = live_tokens(a.valid, a.tokens) * a.top_k;
-    int e;
-    const int n = expert_pairs(a, pairs, e, list, count);
+    __shared__ int counts[kMaxPairs / 64];
+    const int pairs = live_tokens(a.valid, a.tokens) * a.top_k, e = own_expert(a, pairs);
+    if (e < 0)
+        return;
+    const int n = expert_pairs<kWaves>(a, pairs, e, list, counts);
     for (int p = 0; p < n; p += G * kPairs) {
         const int m = n - p < G * kPairs ? n - p : G * kPairs;
         if (G == 1 || m <= kPairs)
@@ -329,6 +557,72 @@ __global__ __launch_bounds__(kWaves * 64) void fp4_down_kernel(ExpertArgs a)
             down_pass<G < 2 ? 1 : 2>(a, e, list + p, m, joined);
         else
             down_pass<G>(a, e, list + p, m, joined);
+    }
+}
+
+// Down products where experts have many tokens, as up: four waves of four row tiles (64 columns of the
+// output) each.
+constexpr int kDownWaves = 4, kDownTiles = 4;
+
+template <int G>
+__device__ __forceinline__ void down_many_pass(const ExpertArgs &a, const Tiles (&w)[kDownTiles], Ahead<kDownTiles> &even,
+                                               Ahead<kDownTiles> &odd, int c0, const uint16_t *list, int n, u32x4 *xs)
+{
+    constexpr int RT = kDownTiles, W = kDownWaves, kLoads = kOwnLoads<G, W>;
+    const int lane = lane_id(), wave = wave_in_block();
+    const uint32_t pairs = (uint32_t)(a.tokens * a.top_k), row_bytes = (uint32_t)a.inter * 2u;
+    const rsrc_t h = make_rsrc(a.h, 3u * pairs * row_bytes);
+    uint32_t col[kLoads];
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+        const int at = 4 * (wave + i * W) + lane / 16, c = at % 16, s = at / 16 * kPairs + c / 3;
+        col[i] = c < 15 && s < n ? ((uint32_t)(c % 3) * pairs + list[s]) * row_bytes + lane % 16 * 16 : kNowhere;
+    }
+    f32x4 acc[RT][G];
+    clear(acc);
+    walk_products<RT, G, W>(acc, w, even, odd, h, col, a.inter, (n + kPairs - 1) / kPairs, xs);
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+        const int c = lane % 16, s = g * kPairs + c / 3;
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+            f32x4 z = acc[i][g];
+#pragma unroll
+            for (int r = 0; r < 4; ++r)  // row_shl: the second and the third term's lane
+                z[r] = z[r] + dpp<0x101>(acc[i][g][r]) + dpp<0x102>(acc[i][g][r]);
+            if (c < 15 && c % 3 == 0 && s < n && c0 + 16 * i < a.hidden)
+                *reinterpret_cast<f32x4 *>(a.z + (int64_t)list[s] * a.hidden + c0 + 16 * i + lane / 16 * 4) = z;
+        }
+    }
+}
+
+template <int G>
+__global__ __launch_bounds__(kDownWaves * 64, G == 4 ? 2 : 3) void fp4_down_many_kernel(ExpertArgs a)
+{
+    __shared__ u32x4 xs[2 * G * 256];
+    __shared__ uint16_t list[kMaxPairs];
+    __shared__ int counts[kMaxPairs / 64];
+    const int pairs = live_tokens(a.valid, a.tokens) * a.top_k, e = own_expert(a, pairs);
+    if (e < 0)
+        return;
+    const int blocks = a.hidden / 16, b0 = (blockIdx.x * kDownWaves + wave_in_block()) * kDownTiles;
+    Tiles w[kDownTiles];
+#pragma unroll
+    for (int i = 0; i < kDownTiles; ++i)  // past the last: no rows of W, but its part of h
+        w[i] = tiles_of(a.down_codes, a.down_scales, b0 + i < blocks ? (int64_t)e * blocks + b0 + i : 0,
+                        b0 + i < blocks ? (a.inter + kFp4K - 1) / kFp4K : 0);
+    Ahead<kDownTiles> even, odd;
+    even.load(w, 0);
+    odd.load(w, 1);
+    const int n = expert_pairs<kDownWaves>(a, pairs, e, list, counts);
+    for (int p = 0; p < n; p += G * kPairs) {
+        const int m = n - p < G * kPairs ? n - p : G * kPairs;
+        if (p > 0) {
+            sync_shared();
+            even.load(w, 0);
+            odd.load(w, 1);
+        }
+        down_many_pass<G>(a, w, even, odd, b0 * 16, list + p, m, xs);
     }
 }
 
@@ -396,13 +690,29 @@ int pair_groups(const ExpertSizes &s, int group)
 {
     const int64_t some = ceil_div(3 * s.tokens * s.top_k, 2 * s.experts);
     const int64_t each = s.tokens < some ? s.tokens : some;
-    return each <= group ? 1 : (each <= 2 * group ? 2 : 4);
+    return each <= group ? 1 : (each <= 2 * group ? 2 : (each <= 3 * group ? 3 : 4));
+}
+
+// Whether the waves of a workgroup take rows of their own and share the columns: where that
+// still leaves a workgroup for every CU.
+bool shares_columns(int64_t rows_of_w, unsigned experts)
+{
+    return ceil_div(rows_of_w, kManyWaves * 32) * experts >= 256;
 }
 
 template <int ACT>
-block_status_t launch_up(const ExpertArgs &a, int groups, dim3 grid, hipStream_t st)
+block_status_t launch_up(const ExpertArgs &a, int groups, unsigned each, hipStream_t st)
 {
-    const dim3 threads(kWaves * 64);
+    constexpr int kCols = ACT == ACT_SWIGLU ? 16 : 32;
+    if (shares_columns((int64_t)a.inter * 32 / kCols, each) && a.tokens > 1) {
+        const dim3 grid((unsigned)ceil_div(a.inter, kManyWaves * kCols), each), threads(kManyWaves * 64);
+        if (groups == 1)
+            return launch(fp4_up_many_kernel<ACT, 1>, grid, threads, 0, st, a);
+        if (groups == 2)
+            return launch(fp4_up_many_kernel<ACT, 2>, grid, threads, 0, st, a);
+        return launch(fp4_up_many_kernel<ACT, 4>, grid, threads, 0, st, a);
+    }
+    const dim3 grid((unsigned)(a.inter / 16), each), threads(kWaves * 64);
     if (groups == 1)
         return launch(fp4_up_kernel<ACT, 1>, grid, threads, 0, st, a);
     if (groups == 2)
@@ -410,9 +720,19 @@ block_status_t launch_up(const ExpertArgs &a, int groups, dim3 grid, hipStream_t
     return launch(fp4_up_kernel<ACT, 4>, grid, threads, 0, st, a);
 }
 
-block_status_t launch_down(const ExpertArgs &a, int groups, dim3 grid, hipStream_t st)
+block_status_t launch_down(const ExpertArgs &a, int groups, unsigned each, hipStream_t st)
 {
-    const dim3 threads(kWaves * 64);
+    if (shares_columns(a.hidden, each) && a.tokens > 1) {
+        const dim3 grid((unsigned)ceil_div(a.hidden, kDownWaves * kDownTiles * 16), each), threads(kDownWaves * 64);
+        if (groups == 1)
+            return launch(fp4_down_many_kernel<1>, grid, threads, 0, st, a);
+        if (groups == 2)
+            return launch(fp4_down_many_kernel<2>, grid, threads, 0, st, a);
+        if (groups == 3)
+            return launch(fp4_down_many_kernel<3>, grid, threads, 0, st, a);
+        return launch(fp4_down_many_kernel<4>, grid, threads, 0, st, a);
+    }
+    const dim3 grid((unsigned)(a.hidden / 16), each), threads(kWaves * 64);
     if (groups == 1)
         return launch(fp4_down_kernel<1>, grid, threads, 0, st, a);
     if (groups == 2)
@@ -519,12 +839,11 @@ block_status_t block_moe_experts_fp4(const uint16_t *x, const uint8_t *up_codes,
     const int64_t pairs = tokens * top_k;
     a.by_pair = pairs < n_experts;
     const unsigned each = (unsigned)(a.by_pair ? pairs : n_experts);
-    const dim3 up_grid((unsigned)(inter / 16), each), down_grid((unsigned)(hidden / 16), each);
     const int groups = pair_groups(s, 16);
-    if (const block_status_t r = act == BLOCK_ACT_SWIGLU ? launch_up<ACT_SWIGLU>(a, groups, up_grid, stream)
-                                                         : launch_up<ACT_SQUARED_RELU>(a, groups, up_grid, stream))
+    if (const block_status_t r = act == BLOCK_ACT_SWIGLU ? launch_up<ACT_SWIGLU>(a, groups, each, stream)
+                                                         : launch_up<ACT_SQUARED_RELU>(a, groups, each, stream))
         return r;
-    if (const block_status_t r = launch_down(a, pair_groups(s, kPairs), down_grid, stream))
+    if (const block_status_t r = launch_down(a, pair_groups(s, kPairs), each, stream))
         return r;
     const dim3 all((unsigned)ceil_div(n, 1024));
     return y_dtype == BLOCK_FP32 ? launch(fp4_combine_kernel<DT_F32>, all, dim3(256), 0, stream, a)
