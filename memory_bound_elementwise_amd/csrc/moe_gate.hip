@@ -27,65 +27,74 @@ __device__ __forceinline__ double of_key(uint64_t k)
     return __builtin_bit_cast(double, k >> 63 ? k & ~((uint64_t)1 << 63) : ~k);
 }
 
-template <int kCtrl, int kRowMask = 0xf>
-__device__ __forceinline__ uint64_t dpp_u64(uint64_t v)
-{
-    return __builtin_bit_cast(uint64_t, dpp64<kCtrl, kRowMask>(__builtin_bit_cast(double, v)));
-}
-
-template <int kCtrl, int kRowMask = 0xf>
-__device__ __forceinline__ unsigned dpp_u32(unsigned v)
-{
-    return (unsigned)__builtin_amdgcn_update_dpp(0, (int)v, kCtrl, kRowMask, 0xf, false);
-}
-
 template <typename T>
 __device__ __forceinline__ T larger(T a, T b)
 {
     return a > b ? a : b;
 }
 
-// Over the L = 16 or 64 lanes of a token, the same in each of them. (A lane that a masked step
-// leaves out compares with 0, the least of both.)
-template <int L>
-__device__ __forceinline__ uint64_t lanes_max(uint64_t v)
+template <int kCtrl>
+__device__ __forceinline__ unsigned dpp32(unsigned v)
 {
-    v = larger(v, dpp_u64<0xB1>(v));
-    v = larger(v, dpp_u64<0x4E>(v));
-    v = larger(v, dpp_u64<0x141>(v));
-    v = larger(v, dpp_u64<0x140>(v));
+    return (unsigned)__builtin_amdgcn_update_dpp(0, (int)v, kCtrl, 0xf, 0xf, false);
+}
+
+// What the lane in the other row of 16 of each pair of rows holds, or in the other half of the wave.
+// (One instruction swaps the odd rows of one register with the even rows of another.)
+template <int kLanes>
+__device__ __forceinline__ unsigned other_row(unsigned v)
+{
+    const auto s = kLanes == 16 ? __builtin_amdgcn_permlane16_swap(v, v, false, false)
+                                : __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    return (lane_id() & kLanes) ? s[0] : s[1];
+}
+
+// Over the L = 16, 32 or 64 lanes of a token, the same in each of them.
+template <int L>
+__device__ __forceinline__ unsigned lanes_max(unsigned v)
+{
+    v = larger(v, dpp32<0xB1>(v));
+    v = larger(v, dpp32<0x4E>(v));
+    v = larger(v, dpp32<0x141>(v));
+    v = larger(v, dpp32<0x140>(v));
+    if constexpr (L >= 32) {
+        const auto s = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+        v = larger(s[0], s[1]);
+    }
     if constexpr (L == 64) {
-        v = larger(v, dpp_u64<0x142, 0xa>(v));
-        v = larger(v, dpp_u64<0x143, 0xc>(v));
-        v = __builtin_bit_cast(uint64_t, of_lane(__builtin_bit_cast(double, v), 63));
+        const auto s = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+        v = larger(s[0], s[1]);
     }
     return v;
 }
 
+// The largest key: its upper half, then the lower halves of those that share it.
 template <int L>
-__device__ __forceinline__ unsigned lanes_max(unsigned v)
+__device__ __forceinline__ uint64_t lanes_max(uint64_t v)
 {
-    v = larger(v, dpp_u32<0xB1>(v));
-    v = larger(v, dpp_u32<0x4E>(v));
-    v = larger(v, dpp_u32<0x141>(v));
-    v = larger(v, dpp_u32<0x140>(v));
-    if constexpr (L == 64) {
-        v = larger(v, dpp_u32<0x142, 0xa>(v));
-        v = larger(v, dpp_u32<0x143, 0xc>(v));
-        v = (unsigned)__builtin_amdgcn_readlane((int)v, 63);
-    }
-    return v;
+    const unsigned hi = lanes_max<L>((unsigned)(v >> 32));
+    return (uint64_t)hi << 32 | lanes_max<L>((unsigned)(v >> 32) == hi ? (unsigned)v : 0u);
+}
+
+template <int kLanes>
+__device__ __forceinline__ double other_row(double v)
+{
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const uint64_t hi = other_row<kLanes>((unsigned)(b >> 32)), lo = other_row<kLanes>((unsigned)b);
+    return __builtin_bit_cast(double, hi << 32 | lo);
 }
 
 template <int L>
 __device__ __forceinline__ double lanes_sum(double v)
 {
-    if constexpr (L == 64)
-        return wave_sum64(v);
     v += dpp64<0xB1>(v);
     v += dpp64<0x4E>(v);
     v += dpp64<0x141>(v);
     v += dpp64<0x140>(v);
+    if constexpr (L >= 32)
+        v += other_row<16>(v);
+    if constexpr (L == 64)
+        v += other_row<32>(v);
     return v;
 }
 
@@ -93,7 +102,36 @@ __device__ __forceinline__ double lanes_sum(double v)
 // them across.
 __device__ __forceinline__ void wave_fence() { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront"); }
 
-__device__ __forceinline__ double sigmoid(double v) { return 1.0 / (1.0 + exp(-v)); }
+// e^v for v <= 0, within about a step of fp64: v = n ln 2 + r with |r| <= ln 2 / 2, and the series of
+// e^r to its 13th power (what follows is below 2^-57). Half of the library function's
+// instructions, which has to deal with larger v.
+__device__ __forceinline__ double exp_below(double v)
+{
+    v = v < -800.0 ? -800.0 : v;  // 0 from there on; keeps NaN
+    const double n = __builtin_rint(v * 1.4426950408889634);
+    const double r = __builtin_fma(n, -1.9082149292705877e-10, __builtin_fma(n, -0.6931471803691238, v));
+    constexpr double c[] = {1.0 / 6227020800, 1.0 / 479001600, 1.0 / 39916800, 1.0 / 3628800, 1.0 / 362880, 1.0 / 40320,
+                            1.0 / 5040, 1.0 / 720, 1.0 / 120, 1.0 / 24, 1.0 / 6, 0.5, 1.0, 1.0};
+    double e = c[0];
+#pragma unroll
+    for (int i = 1; i < 14; ++i)
+        e = __builtin_fma(e, r, c[i]);
+    return __builtin_amdgcn_ldexp(e, (int)n);
+}
+
+// 1 / d to a step or so, for d that neither overflows nor underflows.
+__device__ __forceinline__ double reciprocal(double d)
+{
+    double y = __builtin_amdgcn_rcp(d);
+    y = __builtin_fma(y, __builtin_fma(-d, y, 1.0), y);
+    return __builtin_fma(y, __builtin_fma(-d, y, 1.0), y);
+}
+
+__device__ __forceinline__ double sigmoid(double v)
+{
+    const double e = exp_below(-__builtin_fabs(v)), q = reciprocal(1.0 + e);
+    return v < 0.0 ? e * q : q;
+}
 
 template <int SRC>
 __device__ __forceinline__ double logit(const void *logits, int64_t at, int64_t part, int parts)
@@ -116,13 +154,14 @@ __device__ __forceinline__ void softmax(const double (&v)[V], double (&s)[V])
     double sum = 0.0;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        s[i] = m == -INFINITY ? 0.0 : exp(v[i] - m);
+        s[i] = m == -INFINITY ? 0.0 : exp_below(v[i] - m);
         sum += s[i];
     }
     sum = lanes_sum<L>(sum);
+    const double q = sum == 0.0 ? 0.0 : reciprocal(sum);  // a sum is 0, or at least 1
 #pragma unroll
     for (int i = 0; i < V; ++i)
-        s[i] = sum == 0.0 ? 0.0 : s[i] / sum;
+        s[i] *= q;
 }
 
 template <int SRC, int L, int V>
@@ -131,7 +170,7 @@ __global__ __launch_bounds__(kWavesHere * 64) void gate_kernel(GateArgs a)
     constexpr int T = 64 / L;
     __shared__ uint64_t tables[kWavesHere][T][L * V];
     __shared__ uint64_t worths[kWavesHere][T][kGateGroups];
-    __shared__ int slots[kWavesHere][T][kGateSlots];
+    __shared__ int kept_groups[kWavesHere][T][kGateGroups];
     const GateRule r = a.rule;
     const int lane = lane_id(), wave = wave_in_block(), l = lane % L, tl = lane / L;
     const int first = ((int)blockIdx.x * kWavesHere + wave) * T, live = live_tokens(a.valid, a.tokens);
@@ -140,13 +179,15 @@ __global__ __launch_bounds__(kWavesHere * 64) void gate_kernel(GateArgs a)
     const bool mine = first + tl < live;
     const int t = mine ? first + tl : first;  // past the last token: the first one again, not stored
     uint64_t *table = tables[wave][tl], *worth = worths[wave][tl];
-    int *slot = slots[wave][tl];
+    int *kept = kept_groups[wave][tl];
     const int64_t row = (int64_t)t * a.experts, part = (int64_t)a.tokens * a.experts;
 
     double v[V], s[V];
+    float bias[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int e = i * L + l;
+        bias[i] = a.bias && e < a.experts ? a.bias[e] : 0.0f;
         v[i] = e < a.experts ? logit<SRC>(a.logits, row + e, part, a.parts) : -INFINITY;
     }
     if (r.scores == BLOCK_SCORES_SIGMOID) {
@@ -160,59 +201,105 @@ __global__ __launch_bounds__(kWavesHere * 64) void gate_kernel(GateArgs a)
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int e = i * L + l;
-        const double b = a.bias && e < a.experts ? (double)a.bias[e] : 0.0;
-        key[i] = e < a.experts ? order_key(v[i] == -INFINITY ? v[i] : s[i] + b) : 0;
+        key[i] = e < a.experts ? order_key(v[i] == -INFINITY ? v[i] : s[i] + (double)bias[i]) : 0;
     }
     if (r.groups > 1) {
         const int size = a.experts / r.groups;
+        const unsigned inverse = ((1u << 20) + size - 1) / size;  // e / size = e inverse / 2^20 for e, size <= 1024
 #pragma unroll
         for (int i = 0; i < V; ++i)
             table[i * L + l] = key[i];
         wave_fence();
-        for (int g = l; g < r.groups; g += L) {
+        // the lanes of a token share its groups: `each` lanes, a power of two, look through one
+        const int each = r.groups >= L ? 1 : L >> (32 - __builtin_clz(r.groups - 1));
+        for (int g0 = 0; g0 < r.groups; g0 += L / each) {
+            const int g = g0 + l / each;
             uint64_t first_key = 0, second_key = 0;
-            for (int m = 0; m < size; ++m) {
-                const uint64_t k = table[g * size + m];
-                second_key = larger(second_key, k < first_key ? k : first_key);
-                first_key = larger(first_key, k);
+            const int from = g < r.groups ? g * size : 0;
+            constexpr int kTogether = 4;  // loads that go out together
+            for (int m0 = l % each; m0 < size; m0 += kTogether * each) {
+                uint64_t k[kTogether];
+#pragma unroll
+                for (int i = 0; i < kTogether; ++i) {
+                    const int m = m0 + i * each;
+                    k[i] = table[from + (m < size ? m : 0)];
+                    k[i] = m < size ? k[i] : 0;
+                }
+#pragma unroll
+                for (int i = 0; i < kTogether; ++i) {
+                    second_key = larger(second_key, k[i] < first_key ? k[i] : first_key);
+                    first_key = larger(first_key, k[i]);
+                }
+            }
+            for (int d = 1; d < each; d *= 2) {
+                const uint64_t f = __shfl_xor(first_key, d), q = __shfl_xor(second_key, d);
+                second_key = larger(larger(second_key, q), f < first_key ? f : first_key);
+                first_key = larger(first_key, f);
             }
             const double w = of_key(first_key);
-            worth[g] = order_key(r.group_top == 2 ? w + of_key(second_key) : w);
+            if (g < r.groups && l % each == 0)
+                worth[g] = order_key(r.group_top == 2 ? w + of_key(second_key) : w);
         }
         wave_fence();
         for (int g = l; g < r.groups; g += L) {
             const uint64_t own = worth[g];
             int before = 0;
+#pragma unroll 8
             for (int o = 0; o < r.groups; ++o)
                 before += worth[o] > own || (worth[o] == own && o < g);
-            slot[g] = before < r.top_groups;
+            kept[g] = before < r.top_groups;
         }
         wave_fence();
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const int e = i * L + l;
-            if (e < a.experts && !slot[e / size])
+            const unsigned e = i * L + l;
+            if ((int)e < a.experts && !kept[e * inverse >> 20])
                 key[i] = 0;
         }
         wave_fence();
     }
+    // The upper halves of the keys decide where the largest is there once for each token of the wave;
+    // otherwise the lower halves of those that share it, then the index.
+    unsigned hi[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        hi[i] = (unsigned)(key[i] >> 32);
+    constexpr int Q = kGateSlots / L;
+    int id[Q];  // lane l has slots l, L + l, ...
+#pragma unroll
+    for (int q = 0; q < Q; ++q)
+        id[q] = 0;
     for (int j = 0; j < r.top_k; ++j) {
-        uint64_t best = 0;
+        unsigned best = 0;
 #pragma unroll
         for (int i = 0; i < V; ++i)
-            best = larger(best, key[i]);
+            best = larger(best, hi[i]);
         best = lanes_max<L>(best);
         unsigned from_end = 0;  // the lowest expert of the best, counted from the end
+        int count = 0;
 #pragma unroll
-        for (int i = 0; i < V; ++i)
-            from_end = larger(from_end, key[i] == best ? (unsigned)(kGateExperts - (i * L + l)) : 0u);
+        for (int i = V - 1; i >= 0; --i) {
+            from_end = hi[i] == best ? (unsigned)(kGateExperts - (i * L + l)) : from_end;
+            count += hi[i] == best;
+        }
+        if (__popcll(__ballot(count > 0)) != T || __ballot(count > 1)) {
+            unsigned low = 0;
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                low = larger(low, hi[i] == best ? (unsigned)key[i] : 0u);
+            low = lanes_max<L>(low);
+            from_end = 0;
+#pragma unroll
+            for (int i = V - 1; i >= 0; --i)
+                from_end = hi[i] == best && (unsigned)key[i] == low ? (unsigned)(kGateExperts - (i * L + l)) : from_end;
+        }
         const int e = kGateExperts - (int)lanes_max<L>(from_end);
 #pragma unroll
         for (int i = 0; i < V; ++i)
-            if (i * L + l == e)
-                key[i] = 0;
-        if (l == 0)
-            slot[j] = e;
+            hi[i] = i * L + l == e ? 0u : hi[i];
+#pragma unroll
+        for (int q = 0; q < Q; ++q)
+            id[q] = q * L + l == j ? e : id[q];
     }
     wave_fence();
     double *score = reinterpret_cast<double *>(table);
@@ -220,17 +307,24 @@ __global__ __launch_bounds__(kWavesHere * 64) void gate_kernel(GateArgs a)
     for (int i = 0; i < V; ++i)
         score[i * L + l] = s[i];
     wave_fence();
-    double sum = 0.0;
-    if (r.renormalize)
-        for (int j = 0; j < r.top_k; ++j)
-            sum += score[slot[j]];
-    for (int j = l; j < r.top_k; j += L) {
-        double p = score[slot[j]];
-        if (r.renormalize)
-            p = sum == 0.0 ? 0.0 : p / sum;
-        if (mine) {
-            a.ids[(int64_t)t * r.top_k + j] = slot[j];
-            a.probs[(int64_t)t * r.top_k + j] = (float)(p * (double)r.scale);
+    double p[Q], sum = 0.0;
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+        p[q] = q * L + l < r.top_k ? score[id[q]] : 0.0;
+        sum += p[q];
+    }
+    if (r.renormalize) {
+        sum = lanes_sum<L>(sum);
+#pragma unroll
+        for (int q = 0; q < Q; ++q)
+            p[q] = sum == 0.0 ? 0.0 : p[q] / sum;
+    }
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+        const int j = q * L + l;
+        if (mine && j < r.top_k) {
+            a.ids[(int64_t)t * r.top_k + j] = id[q];
+            a.probs[(int64_t)t * r.top_k + j] = (float)(p[q] * (double)r.scale);
         }
     }
 }
@@ -372,13 +466,15 @@ template <int SRC>
 block_status_t run_gate(const GateArgs &a, hipStream_t st)
 {
     const dim3 threads(kWavesHere * 64);
-    const unsigned few = groups_of(a.tokens, 64), many = groups_of(a.tokens, 16);
+    const unsigned few = groups_of(a.tokens, 64);
     if (a.experts <= 64)
-        return a.tokens <= kFewTokens ? launch(gate_kernel<SRC, 64, 1>, dim3(few), threads, 0, st, a)
-                                      : launch(gate_kernel<SRC, 16, 4>, dim3(many), threads, 0, st, a);
+        return a.tokens <= kFewTokens
+                   ? launch(gate_kernel<SRC, 64, 1>, dim3(few), threads, 0, st, a)
+                   : launch(gate_kernel<SRC, 16, 4>, dim3(groups_of(a.tokens, 16)), threads, 0, st, a);
     if (a.experts <= 256)
-        return a.tokens <= kFewTokens ? launch(gate_kernel<SRC, 64, 4>, dim3(few), threads, 0, st, a)
-                                      : launch(gate_kernel<SRC, 16, 16>, dim3(many), threads, 0, st, a);
+        return a.tokens <= kFewTokens
+                   ? launch(gate_kernel<SRC, 64, 4>, dim3(few), threads, 0, st, a)
+                   : launch(gate_kernel<SRC, 32, 8>, dim3(groups_of(a.tokens, 32)), threads, 0, st, a);
     return launch(gate_kernel<SRC, 64, 16>, dim3(few), threads, 0, st, a);
 }
 
