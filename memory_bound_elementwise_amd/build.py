@@ -36,7 +36,7 @@ LIBS = {
     "moe_elementwise": ["moe_elementwise.hip"],
     "hbm_probe": ["hbm_probe.hip"],
     "moe_block": ["block_common.hip", "layer_norm.hip", "linear_act.hip", "moe_layer.hip", "moe_gate.hip",
-                  "fp4_weights.hip", "fp4_products.hip"],
+                  "fp4_weights.hip", "fp4_linear.hip", "fp4_experts.hip"],
 }
 
 

@@ -1,0 +1,699 @@
+// The expert layer of a few tokens with weights in 4 bits (layout in fp4.h), for AMD Instinct MI355X
+// (gfx950). C ABI declared in block/moe_block.h.
+//
+// For a few tokens the cost is reading each chosen expert's weights once.
+//   up       one workgroup a (chosen expert, block of columns of the activation); the activation
+//            times the probability goes to the workspace as three bf16 terms, which keep its 24 bits
+//   down     the terms are columns of their own. For up to 64 pairs one workgroup 16 columns of
+//            the output, all experts: their sums meet in shared memory. Otherwise one a (chosen
+//            expert, block of columns of the output), and a pair's fp32 products go to the workspace
+//   combine  adds a token's pairs in slot order, so no atomics are needed and the bits never change
+// Workgroups of few columns split k among their waves; where that leaves enough workgroups, the
+// waves have rows of W of their own and share the columns instead.
+#include <hip/hip_runtime.h>
+
+#include <stdint.h>
+
+#include <cmath>
+
+#include "fp4_host.h"
+#include "fp4_stream.h"
+#include "route_device.h"
+
+namespace {
+
+using namespace block;
+
+constexpr int kWaves = 4;
+
+template <int RT, int G>
+__device__ __forceinline__ void clear(f32x4 (&acc)[RT][G])
+{
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int g = 0; g < G; ++g)
+            acc[i][g] = f32x4{0, 0, 0, 0};
+}
+
+struct ExpertArgs {
+    const uint16_t *x;
+    const uint8_t *up_codes, *up_scales, *down_codes, *down_scales;
+    const int *ids;
+    const float *probs;
+    const uint16_t *residual;
+    char *y;
+    const int *valid;
+    uint16_t *h;  // [3][pairs][inter]
+    float *z;     // [pairs][hidden]
+    int tokens, hidden, inter, experts, top_k, by_pair;
+    float limit;
+};
+
+// An fp32 value as the sum of three bf16: its first 8 bits, the next 8 and the rest (nothing is
+// lost, but below 2^-109, where the last term runs out of exponents). Of an infinity or a NaN the
+// first term is one and the others zero.
+__device__ __forceinline__ void three_terms(float h, uint16_t (&term)[3])
+{
+    const uint32_t bits = __float_as_uint(h);
+    const bool finite = (bits & 0x7f800000u) != 0x7f800000u;
+    const float first = __uint_as_float(bits & 0xffff0000u), rest = h - first;
+    const float second = __uint_as_float(__float_as_uint(rest) & 0xffff0000u), third = rest - second;
+    term[0] = (uint16_t)(bits >> 16) | (h != h ? 0x40 : 0);
+    term[1] = finite ? (uint16_t)(__float_as_uint(second) >> 16) : 0;
+    term[2] = finite ? (uint16_t)(__float_as_uint(third) >> 16) : 0;
+}
+
+// Four neighbours' terms, one plane after the other.
+__device__ __forceinline__ void store_terms(const f32x4 &h, uint16_t *to, int64_t plane)
+{
+    uint16_t t[4][3];
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+        three_terms(h[r], t[r]);
+#pragma unroll
+    for (int q = 0; q < 3; ++q)
+        *reinterpret_cast<u32x2 *>(to + q * plane) =
+            u32x2{t[0][q] | (uint32_t)t[1][q] << 16, t[2][q] | (uint32_t)t[3][q] << 16};
+}
+
+// The workgroup's expert: blockIdx.y is a pair, which stands for its expert if no earlier one has the
+// same, or an expert, whichever is fewer. -1: none.
+__device__ __forceinline__ int own_expert(const ExpertArgs &a, int pairs)
+{
+    int e = blockIdx.y;
+    if (a.by_pair) {
+        e = e < pairs ? a.ids[e] : -1;
+        if (e >= a.experts)
+            e = -1;
+    }
+    return __builtin_amdgcn_readfirstlane(e);
+}
+
+// The pairs (token * top_k + slot) below `pairs` whose id is e, in increasing order, into list;
+// returns their number, or 0 where an earlier workgroup has them. W waves look through ids
+// together, 64 pairs a chunk. counts: of the chunks.
+template <int W>
+__device__ __forceinline__ int expert_pairs(const ExpertArgs &a, int pairs, int e, uint16_t *list, int (&counts)[kMaxPairs / 64])
+{
+    constexpr int kOwn = kMaxPairs / 64 / W;
+    const int lane = lane_id(), wave = wave_in_block(), chunks = (pairs + 63) / 64;
+    uint64_t found[kOwn];
+    int id[kOwn];
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i) {
+        const int p = (wave + i * W) * 64 + lane;
+        id[i] = p < pairs ? a.ids[p] : -1;
+    }
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i) {
+        found[i] = __ballot(id[i] == e);
+        if (lane == 0)
+            counts[wave + i * W] = __popcll(found[i]);
+    }
+    sync_shared();
+    int n = 0;
+    for (int c = 0; c < chunks; ++c) {
+#pragma unroll
+        for (int i = 0; i < kOwn; ++i)
+            if (c == wave + i * W && id[i] == e)
+                list[n + __popcll(found[i] & (((uint64_t)1 << lane) - 1))] = (uint16_t)(c * 64 + lane);
+        n += counts[c];
+    }
+    sync_shared();
+    return n == 0 || (a.by_pair && list[0] != (int)blockIdx.y) ? 0 : __builtin_amdgcn_readfirstlane(n);
+}
+
+// The same by one wave for up to 64 pairs: id holds the lane's pair's. The list is the wave's own.
+__device__ __forceinline__ int list_few(int id, int e, uint16_t *list)
+{
+    const uint64_t found = __ballot(id == e);
+    const int lane = lane_id();
+    if (id == e)
+        list[__popcll(found & (((uint64_t)1 << lane) - 1))] = (uint16_t)lane;
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    return __popcll(found);
+}
+
+// The lane's pair's id, -1 for none or one outside the experts (up to 64 pairs).
+__device__ __forceinline__ int few_ids(const ExpertArgs &a, int pairs)
+{
+    const int lane = lane_id(), id = lane < pairs ? a.ids[lane] : -1;
+    return id >= 0 && id < a.experts ? id : -1;
+}
+
+// FEW: up to 64 pairs. Up to 4 NX tokens of an expert share one read of its weights; an expert with
+// more reads them again.
+template <int ACT, int NX, bool FEW>
+__global__ __launch_bounds__(kWaves * 64) void fp4_up_kernel(ExpertArgs a)
+{
+    constexpr int RT = ACT == ACT_SWIGLU ? 2 : 1;  // gate and up, or the one product
+    constexpr int kStages = kWaves * NX * 64, kSums = kWaves * RT * 64;
+    __shared__ u32x4 shared[kStages > kSums ? kStages : kSums];  // the waves' stages, then their sums
+    __shared__ uint16_t lists[FEW ? kWaves * 64 : kMaxPairs];
+    __shared__ int counts[kMaxPairs / 64];
+    const int lane = lane_id(), wave = wave_in_block();
+    const int pairs = live_tokens(a.valid, a.tokens) * a.top_k;
+    int id = -1, e;
+    if constexpr (FEW) {
+        id = few_ids(a, pairs);
+        e = a.by_pair ? ((int)blockIdx.y < pairs ? __builtin_amdgcn_readlane(id, blockIdx.y) : -1) : (int)blockIdx.y;
+    } else {
+        e = own_expert(a, pairs);
+    }
+    if (e < 0)
+        return;
+    const int k_tiles = (a.hidden + kFp4K - 1) / kFp4K, blocks = a.inter / 16;
+    Tiles w[RT];
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+        w[i] = tiles_of(a.up_codes, a.up_scales, ((int64_t)e * RT + i) * blocks + blockIdx.x, k_tiles);
+    Stream<RT, NX, 2> stream;
+    stream.start(w, wave, kWaves);
+    uint16_t *list = lists;
+    int n;
+    if constexpr (FEW) {
+        list += wave * 64;
+        n = list_few(id, e, list);
+        if (n == 0 || (a.by_pair && list[0] != (int)blockIdx.y))
+            return;  // all of the workgroup: no barrier is behind or ahead of it
+    } else {
+        n = expert_pairs<kWaves>(a, pairs, e, list, counts);
+    }
+    const rsrc_t x = make_rsrc(a.x, (uint32_t)a.tokens * (uint32_t)a.hidden * 2u);
+    const int64_t plane = (int64_t)a.tokens * a.top_k * a.inter;
+    for (int p = 0; p < n; p += 4 * NX) {
+        uint32_t col[NX];
+#pragma unroll
+        for (int i = 0; i < NX; ++i) {
+            const int s = p + 4 * i + lane / 16;
+            col[i] = s < n ? (uint32_t)(list[s] / a.top_k) * (uint32_t)a.hidden * 2u + lane % 16 * 16 : kNowhere;
+        }
+        f32x4 acc[RT] = {};
+        if (p > 0) {
+            __syncthreads();  // the sums have been read
+            stream.start(w, wave, kWaves);
+        }
+        stream.run(acc, w, x, col, a.hidden, wave, kWaves, shared + wave * NX * 64);
+        __syncthreads();
+        f32x4 *joined = reinterpret_cast<f32x4 *>(shared);
+#pragma unroll
+        for (int i = 0; i < RT; ++i)
+            joined[(wave * RT + i) * 64 + lane] = acc[i];
+        __syncthreads();
+        const int row = threadIdx.x % 16, s = p + threadIdx.x / 16;
+        if (s >= n || (int)threadIdx.x / 16 >= 4 * NX)
+            continue;
+        float z[RT];
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+            z[i] = 0.0f;
+#pragma unroll
+            for (int q = 0; q < kWaves; ++q)
+                z[i] += joined[(q * RT + i) * 64 + row / 4 * 16 + (s - p)][row % 4];
+        }
+        const int pair = list[s];
+        uint16_t term[3];
+        three_terms((ACT == ACT_SWIGLU ? swiglu(z[0], z[RT - 1], a.limit) : squared_relu(z[0])) * a.probs[pair], term);
+        uint16_t *to = a.h + (int64_t)pair * a.inter + blockIdx.x * 16 + row;
+#pragma unroll
+        for (int q = 0; q < 3; ++q)
+            to[q * plane] = term[q];
+    }
+}
+
+// Up products where experts have many tokens: a workgroup takes one expert and kManyWaves times two
+// row tiles, which walk k together (walk_products), so that x is read once for all of them. A
+// wave has gate and up of 16 columns of the activation, or 32 columns of one product.
+constexpr int kManyWaves = 8;
+
+template <int ACT, int G>
+__device__ __forceinline__ void up_many_pass(const ExpertArgs &a, const Tiles (&w)[2], Ahead<2> &even, Ahead<2> &odd,
+                                             int c0, const uint16_t *list, int n, u32x4 *xs)
+{
+    constexpr int W = kManyWaves, kLoads = kOwnLoads<G, W>;
+    const int lane = lane_id(), wave = wave_in_block();
+    const rsrc_t x = make_rsrc(a.x, (uint32_t)a.tokens * (uint32_t)a.hidden * 2u);
+    uint32_t col[kLoads];
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+        const int s = 4 * (wave + i * W) + lane / 16;
+        col[i] = s < n ? (uint32_t)(list[s] / a.top_k) * (uint32_t)a.hidden * 2u + lane % 16 * 16 : kNowhere;
+    }
+    f32x4 acc[2][G];
+    clear(acc);
+    walk_products<2, G, W>(acc, w, even, odd, x, col, a.hidden, (n + 15) / 16, xs);
+    if (c0 >= a.inter)
+        return;
+    const int64_t plane = (int64_t)a.tokens * a.top_k * a.inter;
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+        const int s = g * 16 + lane % 16;
+        if (s >= n)
+            continue;
+        const int pair = list[s];
+        const float p = a.probs[pair];
+        uint16_t *to = a.h + (int64_t)pair * a.inter + c0 + lane / 16 * 4;
+        if constexpr (ACT == ACT_SWIGLU) {
+            f32x4 h;
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                h[r] = swiglu(acc[0][g][r], acc[1][g][r], a.limit) * p;
+            store_terms(h, to, plane);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                f32x4 h;
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    h[r] = squared_relu(acc[i][g][r]) * p;
+                store_terms(h, to + 16 * i, plane);
+            }
+        }
+    }
+}
+
+template <int ACT, int G>
+__global__ __launch_bounds__(kManyWaves * 64, G == 1 ? 8 : 4) void fp4_up_many_kernel(ExpertArgs a)
+{
+    __shared__ u32x4 xs[2 * G * 256];
+    __shared__ uint16_t list[kMaxPairs];
+    __shared__ int counts[kMaxPairs / 64];
+    const int pairs = live_tokens(a.valid, a.tokens) * a.top_k, e = own_expert(a, pairs);
+    if (e < 0)
+        return;
+    constexpr int kCols = ACT == ACT_SWIGLU ? 16 : 32;
+    const int c0 = (blockIdx.x * kManyWaves + wave_in_block()) * kCols, blocks = a.inter / 16;
+    const int k_tiles = c0 < a.inter ? (a.hidden + kFp4K - 1) / kFp4K : 0;  // past the end: none, but its part of x
+    Tiles w[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        w[i] = tiles_of(a.up_codes, a.up_scales,
+                        k_tiles == 0 ? 0 : (ACT == ACT_SWIGLU ? ((int64_t)e * 2 + i) * blocks : (int64_t)e * blocks + i) + c0 / 16,
+                        k_tiles);
+    Ahead<2> even, odd;  // on their way while the pairs are looked for
+    even.load(w, 0);
+    odd.load(w, 1);
+    const int n = expert_pairs<kManyWaves>(a, pairs, e, list, counts);
+    for (int p = 0; p < n; p += G * 16) {
+        const int m = n - p < G * 16 ? n - p : G * 16;
+        if (p > 0) {
+            sync_shared();  // the columns lie elsewhere in xs now
+            even.load(w, 0);
+            odd.load(w, 1);
+        }
+        up_many_pass<ACT, G>(a, w, even, odd, c0, list + p, m, xs);
+    }
+}
+
+// A group of 16 columns holds the three terms of five pairs, columns 3 p + 0 .. 2. The sum of a
+// pair's three is then in the lane of the first.
+constexpr int kPairs = 5;
+
+__device__ __forceinline__ f32x4 join_terms(const f32x4 &v)
+{
+    f32x4 z;
+#pragma unroll
+    for (int r = 0; r < 4; ++r)  // row_shl: what the next lane and the one behind it hold
+        z[r] = v[r] + dpp<0x101>(v[r]) + dpp<0x102>(v[r]);
+    return z;
+}
+
+// Where column c of the group that starts at pair s0 of the list starts in h, or kNowhere.
+__device__ __forceinline__ uint32_t term_column(const ExpertArgs &a, const uint16_t *list, int n, int s0, int c)
+{
+    const int s = s0 + c / 3;
+    const uint32_t pairs = (uint32_t)(a.tokens * a.top_k);
+    return c < 3 * kPairs && s < n ? ((uint32_t)(c % 3) * pairs + list[s]) * (uint32_t)a.inter * 2u : kNowhere;
+}
+
+__device__ __forceinline__ rsrc_t terms_of(const ExpertArgs &a)
+{
+    return make_rsrc(a.h, 3u * (uint32_t)(a.tokens * a.top_k) * (uint32_t)a.inter * 2u);
+}
+
+// Down product of up to 64 pairs: a workgroup takes 16 columns of the output, its waves the chosen
+// experts in turn, each in `parts` parts of k so that all have work; the pairs' sums meet in
+// shared memory and are added in slot order. NX 1: a pair at a time, 4: five.
+constexpr int kFewWaves = 8, kFewPairs = 64;
+
+template <int YDT>
+__device__ __forceinline__ void finish(const ExpertArgs &a, int64_t at, float v)
+{
+    if (a.residual)
+        v += load1<DT_BF16>(a.residual, at);
+    store1<YDT>(a.y, at, v);
+}
+
+template <int YDT, int NX>
+__global__ __launch_bounds__(kFewWaves * 64) void fp4_down_few_kernel(ExpertArgs a, int parts)
+{
+    constexpr int kTogether = NX == 1 ? 1 : kPairs;
+    __shared__ u32x4 stages[kFewWaves * NX * 64];
+    __shared__ f32x4 sums[kFewPairs * 4];  // [pair][part][16], pairs * parts up to kFewPairs
+    __shared__ uint16_t lists[kFewWaves * 64];
+    __shared__ int ids[kFewPairs];
+    const int lane = lane_id(), wave = wave_in_block();
+    const int live = live_tokens(a.valid, a.tokens), pairs = live * a.top_k;
+    const int id = few_ids(a, pairs), k_tiles = (a.inter + kFp4K - 1) / kFp4K;
+    const rsrc_t h = terms_of(a);
+    uint16_t *list = lists + wave * 64;
+    if (wave == 0)
+        ids[lane] = id;
+    for (int u = wave; u < pairs * parts; u += kFewWaves) {
+        const int p = u / parts, part = u % parts, e = __builtin_amdgcn_readlane(id, p);
+        if (e < 0 || (int)__builtin_ctzll(__ballot(id == e)) != p)
+            continue;  // none, or an earlier pair stands for its expert
+        const Tiles w[1] = {tiles_of(a.down_codes, a.down_scales, (int64_t)e * (a.hidden / 16) + blockIdx.x, k_tiles)};
+        Stream<1, NX, NX == 1 ? 4 : 2> stream;
+        stream.start(w, part, parts);
+        const int n = list_few(id, e, list);
+        for (int s0 = 0; s0 < n; s0 += kTogether) {
+            uint32_t col[NX];
+#pragma unroll
+            for (int i = 0; i < NX; ++i)
+                col[i] = NX == 1 && lane / 16 == 3 ? kNowhere
+                                                   : term_column(a, list, n, s0, 4 * i + lane / 16) + lane % 16 * 16;
+            if (s0 > 0)
+                stream.start(w, part, parts);
+            f32x4 acc[1] = {};
+            stream.run(acc, w, h, col, a.inter, part, parts, stages + wave * NX * 64);
+            const f32x4 z = join_terms(acc[0]);
+            const int c = lane % 16, s = s0 + c / 3;
+            if (c % 3 == 0 && c < 3 * kTogether && s < n)
+                sums[(list[s] * parts + part) * 4 + lane / 16] = z;
+        }
+    }
+    __syncthreads();
+    const int c = threadIdx.x % 16;
+    for (int t = threadIdx.x / 16; t < live; t += kFewWaves * 4) {
+        float v = 0.0f;
+        for (int j = 0; j < a.top_k; ++j) {
+            const int p = t * a.top_k + j;
+            if (ids[p] < 0)
+                continue;
+            for (int i = 0; i < parts; ++i)
+                v += sums[(p * parts + i) * 4 + c / 4][c % 4];
+        }
+        finish<YDT>(a, (int64_t)t * a.hidden + blockIdx.x * 16 + c, v);
+    }
+}
+
+// More pairs than that, and too few blocks for waves that share columns: up to five pairs of an
+// expert share one read of its weights.
+__global__ __launch_bounds__(kWaves * 64) void fp4_down_kernel(ExpertArgs a)
+{
+    constexpr int NX = 4;
+    __shared__ u32x4 shared[kWaves * NX * 64];  // the waves' stages, then their sums
+    __shared__ uint16_t list[kMaxPairs];
+    __shared__ int counts[kMaxPairs / 64];
+    const int lane = lane_id(), wave = wave_in_block(), k_tiles = (a.inter + kFp4K - 1) / kFp4K;
+    const int pairs = live_tokens(a.valid, a.tokens) * a.top_k, e = own_expert(a, pairs);
+    if (e < 0)
+        return;
+    const Tiles w[1] = {tiles_of(a.down_codes, a.down_scales, (int64_t)e * (a.hidden / 16) + blockIdx.x, k_tiles)};
+    Stream<1, NX, 2> stream;
+    stream.start(w, wave, kWaves);
+    const int n = expert_pairs<kWaves>(a, pairs, e, list, counts);
+    const rsrc_t h = terms_of(a);
+    for (int s0 = 0; s0 < n; s0 += kPairs) {
+        uint32_t col[NX];
+#pragma unroll
+        for (int i = 0; i < NX; ++i)
+            col[i] = term_column(a, list, n, s0, 4 * i + lane / 16) + lane % 16 * 16;
+        if (s0 > 0) {
+            __syncthreads();  // the sums have been read
+            stream.start(w, wave, kWaves);
+        }
+        f32x4 acc[1] = {};
+        stream.run(acc, w, h, col, a.inter, wave, kWaves, shared + wave * NX * 64);
+        __syncthreads();
+        f32x4 *joined = reinterpret_cast<f32x4 *>(shared);
+        joined[wave * 64 + lane] = join_terms(acc[0]);
+        __syncthreads();
+        const int row = threadIdx.x % 16, s = s0 + threadIdx.x / 16;
+        if (s >= n || (int)threadIdx.x / 16 >= kPairs)
+            continue;
+        float z = 0.0f;
+#pragma unroll
+        for (int q = 0; q < kWaves; ++q)
+            z += joined[q * 64 + row / 4 * 16 + (s - s0) * 3][row % 4];
+        a.z[(int64_t)list[s] * a.hidden + blockIdx.x * 16 + row] = z;
+    }
+}
+
+// Down products where experts have many tokens, as up: four waves of four row tiles (64 columns of the
+// output) each.
+constexpr int kDownWaves = 4, kDownTiles = 4;
+
+template <int G>
+__device__ __forceinline__ void down_many_pass(const ExpertArgs &a, const Tiles (&w)[kDownTiles], Ahead<kDownTiles> &even,
+                                               Ahead<kDownTiles> &odd, int c0, const uint16_t *list, int n, u32x4 *xs)
+{
+    constexpr int RT = kDownTiles, W = kDownWaves, kLoads = kOwnLoads<G, W>;
+    const int lane = lane_id(), wave = wave_in_block();
+    const rsrc_t h = terms_of(a);
+    uint32_t col[kLoads];
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+        const int at = 4 * (wave + i * W) + lane / 16;
+        col[i] = term_column(a, list, n, at / 16 * kPairs, at % 16) + lane % 16 * 16;
+    }
+    f32x4 acc[RT][G];
+    clear(acc);
+    walk_products<RT, G, W>(acc, w, even, odd, h, col, a.inter, (n + kPairs - 1) / kPairs, xs);
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+        const int c = lane % 16, s = g * kPairs + c / 3;
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+            const f32x4 z = join_terms(acc[i][g]);
+            if (c < 15 && c % 3 == 0 && s < n && c0 + 16 * i < a.hidden)
+                *reinterpret_cast<f32x4 *>(a.z + (int64_t)list[s] * a.hidden + c0 + 16 * i + lane / 16 * 4) = z;
+        }
+    }
+}
+
+template <int G>
+__global__ __launch_bounds__(kDownWaves * 64, G == 4 ? 2 : 3) void fp4_down_many_kernel(ExpertArgs a)
+{
+    __shared__ u32x4 xs[2 * G * 256];
+    __shared__ uint16_t list[kMaxPairs];
+    __shared__ int counts[kMaxPairs / 64];
+    const int pairs = live_tokens(a.valid, a.tokens) * a.top_k, e = own_expert(a, pairs);
+    if (e < 0)
+        return;
+    const int blocks = a.hidden / 16, b0 = (blockIdx.x * kDownWaves + wave_in_block()) * kDownTiles;
+    Tiles w[kDownTiles];
+#pragma unroll
+    for (int i = 0; i < kDownTiles; ++i)  // past the last: no rows of W, but its part of h
+        w[i] = tiles_of(a.down_codes, a.down_scales, b0 + i < blocks ? (int64_t)e * blocks + b0 + i : 0,
+                        b0 + i < blocks ? (a.inter + kFp4K - 1) / kFp4K : 0);
+    Ahead<kDownTiles> even, odd;
+    even.load(w, 0);
+    odd.load(w, 1);
+    const int n = expert_pairs<kDownWaves>(a, pairs, e, list, counts);
+    for (int p = 0; p < n; p += G * kPairs) {
+        const int m = n - p < G * kPairs ? n - p : G * kPairs;
+        if (p > 0) {
+            sync_shared();
+            even.load(w, 0);
+            odd.load(w, 1);
+        }
+        down_many_pass<G>(a, w, even, odd, b0 * 16, list + p, m, xs);
+    }
+}
+
+// y = residual + a token's products in slot order. A lane takes four neighbouring columns.
+template <int YDT>
+__global__ __launch_bounds__(256) void fp4_combine_kernel(ExpertArgs a)
+{
+    const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+    if (i >= (int64_t)live_tokens(a.valid, a.tokens) * a.hidden)
+        return;
+    const int t = (int)(i / a.hidden), c = (int)(i % a.hidden);
+    f32x4 v = {0, 0, 0, 0};
+    constexpr int kTogether = 8;  // loads that go out together
+    for (int j0 = 0; j0 < a.top_k; j0 += kTogether) {
+        f32x4 z[kTogether];
+        bool in[kTogether];
+#pragma unroll
+        for (int j = 0; j < kTogether; ++j) {
+            const int pair = t * a.top_k + (j0 + j < a.top_k ? j0 + j : 0), e = a.ids[pair];
+            in[j] = j0 + j < a.top_k && e >= 0 && e < a.experts;
+            z[j] = *reinterpret_cast<const f32x4 *>(a.z + (int64_t)pair * a.hidden + c);  // unwritten where the id is none
+        }
+#pragma unroll
+        for (int j = 0; j < kTogether; ++j)
+            if (in[j])
+                v += z[j];
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+        finish<YDT>(a, i + q, v[q]);
+}
+
+// ---------------------------------------------------------------------------
+// Host
+// ---------------------------------------------------------------------------
+struct ExpertSizes {
+    int64_t tokens, hidden, inter;
+    int experts, top_k;
+};
+
+block_status_t check_experts(const ExpertSizes &s, block_act_t act, float limit)
+{
+    if (s.tokens < 0 || s.hidden < 32 || s.inter < 32 || s.hidden > (1 << 16) || s.inter > (1 << 16) || s.experts < 1 ||
+        s.experts > kMaxExperts || s.top_k < 1 || s.top_k > kMaxPairs || s.tokens > kMaxPairs ||
+        s.tokens * s.top_k > kMaxPairs)
+        return BLOCK_ERR_INVALID_ARG;
+    if (act != BLOCK_ACT_SWIGLU && act != BLOCK_ACT_SQUARED_RELU)
+        return BLOCK_ERR_INVALID_ARG;
+    if (act == BLOCK_ACT_SWIGLU && !(limit > 0.0f))
+        return BLOCK_ERR_INVALID_ARG;
+    if (s.hidden % 32 || s.inter % 32)
+        return BLOCK_ERR_ALIGNMENT;
+    return BLOCK_OK;
+}
+
+// Workspace: the activations' terms, then the pairs' products.
+int64_t h_bytes(const ExpertSizes &s) { return round_up(s.tokens * s.top_k * s.inter * 6, 16); }
+int64_t expert_bytes(const ExpertSizes &s) { return h_bytes(s) + s.tokens * s.top_k * s.hidden * 4; }
+
+// Groups of pairs that share a read of an expert's weights: enough for one and a half times the
+// pairs an expert has on average.
+int pair_groups(const ExpertSizes &s, int group)
+{
+    const int64_t some = ceil_div(3 * s.tokens * s.top_k, 2 * s.experts);
+    const int64_t each = s.tokens < some ? s.tokens : some;
+    return each <= group ? 1 : (each <= 2 * group ? 2 : (each <= 3 * group ? 3 : 4));
+}
+
+// Whether the waves of a workgroup take rows of their own and share the columns: where that
+// still leaves a workgroup for every CU, and for more tokens than a few. (7168 x 2048, 8 of 64
+// experts, shared and split k: up, 2 tokens 43.9 and 39.7 us, 4 tokens 67.8 and 66.5, 8 tokens
+// 123.6 and 127.0; down, 2 tokens 25.2 and 6.4 for its combine against 38.2.)
+bool shares_columns(int64_t rows_of_w, unsigned experts)
+{
+    return ceil_div(rows_of_w, kManyWaves * 32) * experts >= 256;
+}
+
+template <int ACT>
+block_status_t launch_up(const ExpertArgs &a, int groups, unsigned each, hipStream_t st)
+{
+    constexpr int kCols = ACT == ACT_SWIGLU ? 16 : 32;
+    if (shares_columns((int64_t)a.inter * 32 / kCols, each) && a.tokens > 2) {
+        const dim3 grid((unsigned)ceil_div(a.inter, kManyWaves * kCols), each), threads(kManyWaves * 64);
+        if (groups == 1)
+            return launch(fp4_up_many_kernel<ACT, 1>, grid, threads, 0, st, a);
+        if (groups == 2)
+            return launch(fp4_up_many_kernel<ACT, 2>, grid, threads, 0, st, a);
+        return launch(fp4_up_many_kernel<ACT, 4>, grid, threads, 0, st, a);
+    }
+    const dim3 grid((unsigned)(a.inter / 16), each), threads(kWaves * 64);
+    if (a.tokens * a.top_k > kFewPairs)
+        return launch(fp4_up_kernel<ACT, 4, false>, grid, threads, 0, st, a);
+    return a.tokens <= 4 ? launch(fp4_up_kernel<ACT, 1, true>, grid, threads, 0, st, a)
+                         : launch(fp4_up_kernel<ACT, 4, true>, grid, threads, 0, st, a);
+}
+
+// Parts of k of the down product of few pairs: enough that all waves of a workgroup have work.
+int few_parts(const ExpertArgs &a)
+{
+    const int pairs = a.tokens * a.top_k;
+    int parts = 1;
+    while (pairs * parts * 2 <= kFewPairs && pairs * parts < kFewWaves && parts * 2 * kFp4K <= a.inter)
+        parts *= 2;
+    return parts;
+}
+
+template <int YDT>
+block_status_t launch_down(const ExpertArgs &a, int groups, unsigned each, hipStream_t st)
+{
+    const int pairs = a.tokens * a.top_k;
+    block_status_t r;
+    if (shares_columns(a.hidden, each) && a.tokens > 1) {
+        const dim3 grid((unsigned)ceil_div(a.hidden, kDownWaves * kDownTiles * 16), each), threads(kDownWaves * 64);
+        if (groups == 1)
+            r = launch(fp4_down_many_kernel<1>, grid, threads, 0, st, a);
+        else if (groups == 2)
+            r = launch(fp4_down_many_kernel<2>, grid, threads, 0, st, a);
+        else if (groups == 3)
+            r = launch(fp4_down_many_kernel<3>, grid, threads, 0, st, a);
+        else
+            r = launch(fp4_down_many_kernel<4>, grid, threads, 0, st, a);
+    } else if (pairs <= kFewPairs) {
+        const dim3 grid((unsigned)(a.hidden / 16)), threads(kFewWaves * 64);
+        return a.tokens == 1 ? launch(fp4_down_few_kernel<YDT, 1>, grid, threads, 0, st, a, few_parts(a))
+                             : launch(fp4_down_few_kernel<YDT, 4>, grid, threads, 0, st, a, few_parts(a));
+    } else {
+        r = launch(fp4_down_kernel, dim3((unsigned)(a.hidden / 16), each), dim3(kWaves * 64), 0, st, a);
+    }
+    return r ? r : launch(fp4_combine_kernel<YDT>, dim3((unsigned)ceil_div((int64_t)a.tokens * a.hidden, 1024)), dim3(256), 0, st, a);
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t block_moe_experts_fp4_workspace(int64_t tokens, int64_t hidden, int64_t inter, int n_experts, int top_k)
+{
+    const ExpertSizes s = {tokens, hidden, inter, n_experts, top_k};
+    return check_experts(s, BLOCK_ACT_SQUARED_RELU, 0.0f) == BLOCK_OK ? expert_bytes(s) : 0;
+}
+
+block_status_t block_moe_experts_fp4(const uint16_t *x, const uint8_t *up_codes, const uint8_t *up_scales,
+                                     const uint8_t *down_codes, const uint8_t *down_scales, const int32_t *ids,
+                                     const float *probs, const uint16_t *residual, void *y, block_dtype_t y_dtype,
+                                     int64_t tokens, int64_t hidden, int64_t inter, int n_experts, int top_k,
+                                     block_act_t act, float limit, const int32_t *valid_tokens, void *workspace,
+                                     int64_t workspace_bytes, hipStream_t stream)
+{
+    const ExpertSizes s = {tokens, hidden, inter, n_experts, top_k};
+    if (const block_status_t r = check_experts(s, act, limit))
+        return r;
+    if (y_dtype != BLOCK_BF16 && y_dtype != BLOCK_FP32)
+        return BLOCK_ERR_INVALID_ARG;
+    if (tokens == 0)
+        return BLOCK_OK;
+    const int64_t need = expert_bytes(s);
+    if (!x || !up_codes || !up_scales || !down_codes || !down_scales || !ids || !probs || !y || !workspace ||
+        workspace_bytes < need)
+        return BLOCK_ERR_INVALID_ARG;
+    if (misaligned(x, 16) || misaligned(up_codes, 16) || misaligned(up_scales, 16) || misaligned(down_codes, 16) ||
+        misaligned(down_scales, 16) || misaligned(residual, 16) || misaligned(y, 16) || misaligned(ids, 4) ||
+        misaligned(probs, 4) || misaligned(valid_tokens, 4) || misaligned(workspace, 16))
+        return BLOCK_ERR_ALIGNMENT;
+    const int64_t n = tokens * hidden;
+    const Fp4Shape up = {n_experts, act == BLOCK_ACT_SWIGLU ? 2 * inter : inter, hidden}, down = {n_experts, hidden, inter};
+    if (any_overlap<2, 9>({{y, n * (y_dtype == BLOCK_FP32 ? 4 : 2)}, {workspace, need}},
+                          {{x, n * 2},
+                           {up_codes, up.codes()},
+                           {up_scales, up.scales()},
+                           {down_codes, down.codes()},
+                           {down_scales, down.scales()},
+                           {ids, tokens * top_k * 4},
+                           {probs, tokens * top_k * 4},
+                           {residual, n * 2},
+                           {valid_tokens, 4}}))
+        return BLOCK_ERR_INVALID_ARG;
+    ExpertArgs a = {};
+    a.x = x, a.up_codes = up_codes, a.up_scales = up_scales, a.down_codes = down_codes, a.down_scales = down_scales;
+    a.ids = ids, a.probs = probs, a.residual = residual, a.y = static_cast<char *>(y), a.valid = valid_tokens;
+    a.h = static_cast<uint16_t *>(workspace);
+    a.z = reinterpret_cast<float *>(static_cast<char *>(workspace) + h_bytes(s));
+    a.tokens = (int)tokens, a.hidden = (int)hidden, a.inter = (int)inter, a.experts = n_experts, a.top_k = top_k;
+    a.limit = limit;
+    const int64_t pairs = tokens * top_k;
+    a.by_pair = pairs < n_experts;
+    const unsigned each = (unsigned)(a.by_pair ? pairs : n_experts);
+    const int groups = pair_groups(s, 16);
+    if (const block_status_t r = act == BLOCK_ACT_SWIGLU ? launch_up<ACT_SWIGLU>(a, groups, each, stream)
+                                                         : launch_up<ACT_SQUARED_RELU>(a, groups, each, stream))
+        return r;
+    const int pair_columns = pair_groups(s, kPairs);
+    return y_dtype == BLOCK_FP32 ? launch_down<DT_F32>(a, pair_columns, each, stream)
+                                 : launch_down<DT_BF16>(a, pair_columns, each, stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,198 @@
+// The inner loops of products with weights in 4 bits (layout in fp4.h) and a few columns: a wave reads
+// tiles of 16 rows x 128 k in whole, straight into the registers from which the matrix
+// instructions take them; the columns of x go through shared memory.
+#ifndef MBE_FP4_STREAM_H
+#define MBE_FP4_STREAM_H
+
+#include "fp4.h"
+
+namespace block {
+
+// Offset of a lane that reads nothing: past the end of every resource, so the load returns zeros
+// (tensors of these products stay below 2^31 bytes a resource).
+constexpr uint32_t kNowhere = 0x80000000u;
+
+// One matrix's row blocks for a wave: W's tiles and their scales.
+struct Tiles {
+    rsrc_t codes, scales;
+};
+
+__device__ __forceinline__ Tiles tiles_of(const uint8_t *codes, const uint8_t *scales, int64_t block, int k_tiles)
+{
+    return {make_rsrc(codes + block * k_tiles * kFp4Codes, (uint32_t)k_tiles * kFp4Codes),
+            make_rsrc(scales + block * k_tiles * kFp4Scales, (uint32_t)k_tiles * kFp4Scales)};
+}
+
+// A wave's next tiles of RT row blocks, in flight.
+template <int RT>
+struct Ahead {
+    u32x4 codes[RT];
+    uint32_t scales[RT];
+    __device__ __forceinline__ void load(const Tiles (&w)[RT], int t)
+    {
+        const int lane = lane_id();
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {  // a tile past the last reads zeros
+            codes[i] = __builtin_amdgcn_raw_buffer_load_b128(w[i].codes, lane * 16, t * kFp4Codes, kLoadAux);
+            scales[i] = __builtin_amdgcn_raw_buffer_load_b32(w[i].scales, lane % 16 * 4, t * kFp4Scales, 0);
+        }
+    }
+};
+
+// A barrier that waits for the wave's accesses to shared memory, but not for its loads from memory.
+// Nothing is moved across.
+__device__ __forceinline__ void sync_shared()
+{
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0)
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_sched_barrier(0);
+}
+
+// The columns' chunks in shared memory: chunk c (16 bytes) of a column's 128 k lies at c ^ (column %
+// 8), so that lanes that read one chunk of eight columns fall into different banks. A lane that
+// loads chunk lane % 16 of column `of` puts it at put_at.
+__device__ __forceinline__ int put_at(int of) { return of * 16 + (lane_id() % 16 ^ of % 8); }
+
+// acc[i] += 16 rows of W (w[i]) times up to 4 NX columns, over the k tiles first, first + stride, ...,
+// by one wave for itself. D steps of tiles and columns are in flight; start() sends the first
+// tiles on their way, before the columns need be known. x: resource of the columns; col[i]:
+// where column 4 i + lane / 16 starts in it, plus 16 (lane % 16) bytes, or kNowhere. stage: NX
+// * 64 chunks of shared memory of the wave's own. (Each lane loading its own operand of x instead
+// takes four loads a step, each to 16 lines.)
+template <int RT, int NX, int D>
+struct Stream {
+    Ahead<RT> tiles[D];
+
+    __device__ __forceinline__ void start(const Tiles (&w)[RT], int first, int stride)
+    {
+#pragma unroll
+        for (int d = 0; d < D; ++d)
+            tiles[d].load(w, first + d * stride);
+    }
+
+    __device__ __forceinline__ void run(f32x4 (&acc)[RT], const Tiles (&w)[RT], rsrc_t x, const uint32_t (&col)[NX],
+                                        int K, int first, int stride, u32x4 *stage)
+    {
+        const int lane = lane_id(), i16 = lane % 16, q = lane / 16, k_tiles = (K + kFp4K - 1) / kFp4K;
+        u32x4 buf[D][NX];
+        auto fetch = [&](u32x4 (&to)[NX], int t) {
+#pragma unroll
+            for (int i = 0; i < NX; ++i)
+                to[i] = __builtin_amdgcn_raw_buffer_load_b128(x, t * kFp4K + i16 * 8 < K ? col[i] : kNowhere, t * kFp4K * 2, 0);
+        };
+        const int c = i16 % (4 * NX);  // further columns repeat these and are not read
+        const int get = c * 16 + (q ^ c % 8), get_odd = get ^ 4;  // word j: 8 (j / 2) further
+        auto multiply = [&](const Ahead<RT> &now, const u32x4 (&from)[NX]) {
+#pragma unroll
+            for (int i = 0; i < NX; ++i)
+                stage[put_at(4 * i + q)] = from[i];
+            // the lanes of a wave run together and its accesses to shared memory stay in order;
+            // the fence keeps the compiler from moving them across
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            u32x4 b[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                b[j] = stage[(j % 2 ? get_odd : get) + j / 2 * 8];
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int i = 0; i < RT; ++i)
+                    acc[i] = mfma16<DT_BF16>(fp4_widen(now.codes[i][j], fp4_scale(now.scales[i], j)), b[j], acc[i]);
+        };
+#pragma unroll
+        for (int d = 0; d < D; ++d)
+            fetch(buf[d], first + d * stride);
+        for (int t = first; t < k_tiles;) {
+#pragma unroll
+            for (int d = 0; d < D; ++d) {  // past the last tile: zeros
+                multiply(tiles[d], buf[d]);
+                tiles[d].load(w, t + D * stride);
+                fetch(buf[d], t + D * stride);
+                t += stride;
+            }
+        }
+    }
+};
+
+// acc[i][g] += 16 rows of W (w[i]) times 16 columns (group g) over all k, with the columns shared: W waves, each with rows of its own, walk k together. A
+// wave loads its part of the columns' next 128 k (load i of wave w takes columns 4 (w + i W) ..+4 of
+// them: col[i], the start of column lane / 16 of these plus 16 (lane % 16) bytes), and they meet in
+// shared memory: xs, two sets of G * 256 chunks of 16 bytes, used in turn, so that one barrier a step
+// is enough. even, odd: the first two steps' tiles, loaded by the caller.
+// groups: those of the G that have columns.
+template <int G, int W>
+constexpr int kOwnLoads = (4 * G + W - 1) / W;
+
+template <int RT, int G, int W>
+__device__ __forceinline__ void walk_products(f32x4 (&acc)[RT][G], const Tiles (&w)[RT], Ahead<RT> &even, Ahead<RT> &odd,
+                                              rsrc_t x, const uint32_t (&col)[kOwnLoads<G, W>], int K, int groups, u32x4 *xs)
+{
+    constexpr int kLoads = kOwnLoads<G, W>;
+    struct Columns {
+        u32x4 v[kLoads];
+    };
+    const int lane = lane_id(), wave = wave_in_block(), k_tiles = (K + kFp4K - 1) / kFp4K;
+    const int i16 = lane % 16, q = lane / 16;
+    auto fetch = [&](Columns &c, int t) {
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i)
+            c.v[i] = __builtin_amdgcn_raw_buffer_load_b128(x, t * kFp4K + i16 * 8 < K ? col[i] : kNowhere, t * kFp4K * 2, 0);
+    };
+    static_assert(W % 2 == 0, "the columns of a wave's loads have one c % 8");
+    const int put = put_at(4 * wave + q);                             // load i: 64 W i further
+    const int get = i16 * 16 + (q ^ i16 % 8), get_odd = get ^ 4;       // word j: 8 (j / 2) further
+    auto multiply = [&](const Ahead<RT> &tiles, const Columns &c, u32x4 *set) {
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i)
+            if (wave + i * W < 4 * groups)
+                set[put + i * W * 64] = c.v[i];
+        // Everyone's columns of this step are there after the barrier. Those of the next go into the
+        // other set, and into this one again only after the next barrier, which a wave reaches when
+        // its reads below have come.
+        sync_shared();
+        u32x4 b[2][G];  // the next word's columns are read beside a word's products
+        auto read = [&](int j) __attribute__((always_inline)) {
+#pragma unroll
+            for (int g = 0; g < G; ++g)
+                if (g == 0 || g < groups)
+                    b[j % 2][g] = set[(j % 2 ? get_odd : get) + j / 2 * 8 + g * 256];
+        };
+        read(0);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (j < 3)
+                read(j + 1);
+            u32x4 a[RT];
+#pragma unroll
+            for (int i = 0; i < RT; ++i)
+                a[i] = fp4_widen(tiles.codes[i][j], fp4_scale(tiles.scales[i], j));
+#pragma unroll
+            for (int g = 0; g < G; ++g)
+                if (g == 0 || g < groups)
+#pragma unroll
+                    for (int i = 0; i < RT; ++i)
+                        acc[i][g] = mfma16<DT_BF16>(a[i], b[j % 2][g], acc[i][g]);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    };
+    Columns c_even, c_odd;
+    fetch(c_even, 0);
+    fetch(c_odd, 1);
+    for (int t = 0; t < k_tiles; t += 2) {  // whole turns of two, so calls use the sets in turn too
+        multiply(even, c_even, xs);
+        even.load(w, t + 2);
+        fetch(c_even, t + 2);
+        multiply(odd, c_odd, xs + G * 256);
+        odd.load(w, t + 3);
+        fetch(c_odd, t + 3);
+    }
+}
+
+}  // namespace block
+
+#endif  // MBE_FP4_STREAM_H
