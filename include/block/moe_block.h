@@ -248,8 +248,8 @@ block_status_t block_fp4_dequantize(const uint8_t *codes, const uint8_t *scales,
 /*
  * block_linear_act with x, bias, residual and y in bf16 and W [n, k] in 4 bits (one matrix).
  * Products are exact, sums and epilogue fp32, one rounding. n a multiple of 8 and k of 32, within
- * block_linear_act's limits. More than 64 rows multiply the weights' bf16 values, which go to the
- * workspace; fewer read W once as it is and need no workspace.
+ * block_linear_act's limits. workspace: partial products of a split sum; may be NULL where
+ * _workspace returns 0.
  */
 int64_t block_linear_act_fp4_workspace(int64_t m, int64_t n, int64_t k);
 block_status_t block_linear_act_fp4(const uint16_t *x, const uint8_t *codes, const uint8_t *scales,

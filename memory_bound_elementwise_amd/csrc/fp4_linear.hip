@@ -6,17 +6,14 @@
 
 #include "fp4_host.h"
 #include "fp4_stream.h"
+#include "linear_tiles.h"
 
 namespace {
 
 using namespace block;
 
-struct Args {
-    const uint16_t *x;
+struct Args : LinearArgs {
     const uint8_t *codes, *scales;
-    const uint16_t *bias, *residual;
-    uint16_t *y;
-    int m, n, k, act;
 };
 
 // ---------------------------------------------------------------------------
@@ -57,13 +54,171 @@ __global__ __launch_bounds__(kWaves * 64) void fp4_linear_few_kernel(Args a)
 #pragma unroll
     for (int i = 0; i < kWaves; ++i)  // row c of W's tile is element c % 4 of lane 16 (c / 4) + its column
         z += joined[i * 64 + c / 4 * 16 + row][c % 4];
-    if (a.bias)
-        z += load1<DT_BF16>(a.bias, col_n);
-    z = activate(a.act, z);
-    const int64_t at = (int64_t)row * a.n + col_n;
-    if (a.residual)
-        z += load1<DT_BF16>(a.residual, at);
-    store1<DT_BF16>(a.y, at, z);
+    finish<DT_BF16>(a, row, col_n, z);
+}
+
+// ---------------------------------------------------------------------------
+// Many rows
+// ---------------------------------------------------------------------------
+// Tiles of 16 FM rows of x by 64 FN rows of W, four waves, 128 k a step. x goes straight from memory
+// to shared memory into two buffers in turn, as chunks of 16 bytes, chunk c of row r at c ^ (r % 8)
+// (a load's lanes fill shared memory in order, so the exchange is made in the addresses they
+// read). W needs no shared memory: each wave has 16 FN rows of it for itself, loads their tiles a
+// step ahead and widens a word of each when its turn comes. What is read from shared memory is so
+// 1 / FN of an operand a matrix instruction. (Three buffers and loads two steps ahead leave room
+// for fewer workgroups: 1009 x 1408 x 7168 26.6 -> 29.5 us, 6720 x 7168 x 4096 323 -> 371. Tiles of
+// 128 x 256, a wave a SIMD: 33.8 and 340.) Weights come from cache for all tiles but the first.
+//   parts > 1: the sums over one of `parts` ranges of k, to partial [parts][m][n] in fp32.
+constexpr int kTileWaves = 4;
+
+template <int FM, int FN>
+__global__ __launch_bounds__(kTileWaves * 64, FN == 4 ? 3 : 4) void fp4_linear_tile_kernel(Args a, int tiles_m, int tiles_n,
+                                                                                              int parts, float *partial)
+{
+    constexpr int W = kTileWaves, TM = FM * 16, TN = W * FN * 16, kLoads = TM / 4 / W;
+    static_assert(kLoads % 2 == 0, "");
+    // one object each: the compiler then knows that a load into one does not touch the other
+    __shared__ u32x4 s0[TM * 16], s1[TM * 16];
+    const int lane = lane_id(), wave = wave_in_block(), i16 = lane % 16, q = lane / 16;
+
+    // Workgroups go to the eight XCDs in turn; each XCD takes a run of tiles, in bands of rows of x,
+    // so that its cache serves one band's x and W moving past it.
+    const int tiles = tiles_m * tiles_n, all = tiles * parts;
+    const int run = (all + 7) / 8, id = (int)blockIdx.x % 8 * run + (int)blockIdx.x / 8;
+    if ((int)blockIdx.x / 8 >= run || id >= all)
+        return;
+    const int part = id / tiles, tile = id % tiles;
+    constexpr int kBand = 8;
+    const int band = tile / (kBand * tiles_n) * kBand, in_band = tile % (kBand * tiles_n);
+    const int high = tiles_m - band < kBand ? tiles_m - band : kBand;
+    const int r0 = (band + in_band % high) * TM, c0 = in_band / high * TN + wave * FN * 16;
+
+    const int k_tiles = (a.k + kFp4K - 1) / kFp4K, blocks = (a.n + 15) / 16;
+    Tiles w[FN];
+#pragma unroll
+    for (int g = 0; g < FN; ++g) {
+        const bool there = c0 / 16 + g < blocks;
+        w[g] = tiles_of(a.codes, a.scales, there ? c0 / 16 + g : 0, k_tiles, there);
+    }
+    const uint32_t row_bytes = (uint32_t)a.k * 2u;
+    const int rows = a.m - r0 < TM ? a.m - r0 : TM;
+    const rsrc_t x = make_rsrc(a.x + (int64_t)r0 * a.k, (uint32_t)rows * row_bytes);  // further rows read zeros
+    const int first = (int)((int64_t)k_tiles * part / parts), last = (int)((int64_t)k_tiles * (part + 1) / parts);
+    // load i of the wave: rows 4 (wave kLoads + i) ..+4, chunk i16 ^ row % 8 of each
+    const int chunk[2] = {i16 ^ q, i16 ^ (4 + q)};
+    const uint32_t base = (uint32_t)(4 * wave * kLoads + q) * row_bytes;
+    auto load = [&](u32x4 *to, int t) {
+        const int k = t * kFp4K;
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const bool in = t < last && k + chunk[i % 2] * 8 < a.k;  // past the last step: zeros
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(x, (shared_void *)(to + (wave * kLoads + i) * 64), 16,
+                                                     in ? base + (uint32_t)(4 * i) * row_bytes + chunk[i % 2] * 16 : kNowhere,
+                                                     k * 2, 0, 0);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    f32x4 acc[FM][FN];
+#pragma unroll
+    for (int f = 0; f < FM; ++f)
+#pragma unroll
+        for (int g = 0; g < FN; ++g)
+            acc[f][g] = f32x4{0, 0, 0, 0};
+    // Units of up to four row tiles of x and one word of W; a unit's operands are read beside the
+    // products of the one before it.
+    constexpr int kUnit = FM < 4 ? FM : 4, kUnits = 4 * FM / kUnit;
+    const int get = i16 * 16 + (q ^ i16 % 8), get_odd = get ^ 4;  // word j: 8 (j / 2) further
+    auto step = [&](u32x4 *now, const Ahead<FN> &tiles_now, Ahead<FN> &tiles_next, int t) {
+        tiles_next.template load<true>(w, t + 1 < last ? t + 1 : k_tiles);
+        __builtin_amdgcn_sched_barrier(0);  // here, not where the step ends and waits for them
+        u32x4 b[2][kUnit], wide[FN];
+        auto read = [&](int u) __attribute__((always_inline)) {
+            const int j = u / (FM / kUnit), f0 = u % (FM / kUnit) * kUnit;
+#pragma unroll
+            for (int f = 0; f < kUnit; ++f)
+                b[u % 2][f] = now[(j % 2 ? get_odd : get) + j / 2 * 8 + (f0 + f) * 256];
+        };
+        read(0);
+#pragma unroll
+        for (int u = 0; u < kUnits; ++u) {
+            const int j = u / (FM / kUnit), f0 = u % (FM / kUnit) * kUnit;
+            if (u + 1 < kUnits)
+                read(u + 1);
+            if (f0 == 0) {
+#pragma unroll
+                for (int g = 0; g < FN; ++g)
+                    wide[g] = fp4_widen(tiles_now.codes[g][j], fp4_scale(tiles_now.scales[g], j));
+            }
+#pragma unroll
+            for (int f = 0; f < kUnit; ++f)
+#pragma unroll
+                for (int g = 0; g < FN; ++g)
+                    acc[f0 + f][g] = mfma16<DT_BF16>(wide[g], b[u % 2][f], acc[f0 + f][g]);
+            __builtin_amdgcn_sched_barrier(0);  // or later units' operands are read early, and spilt
+        }
+        wait_and_sync();  // everyone has read `now`, and the other buffer has come
+        load(now, t + 2);
+    };
+    Ahead<FN> even, odd;
+    load(s0, first);
+    even.template load<true>(w, first);
+    load(s1, first + 1);
+    wait_and_sync();
+    for (int t = first; t < last; ++t) {
+        step(s0, even, odd, t);
+        if (++t >= last)
+            break;
+        step(s1, odd, even, t);
+    }
+    // What a lane adds at the end, its rows of the residual all together.
+    constexpr int kLanes = FN * 2, kTogether = 64 / kLanes, kOuts = TM / kTogether;  // lanes a row of eights
+    int late = lane;
+    asm volatile("" : "+v"(late));  // computed here, not kept over the loop
+    const int my_row = late / kLanes, my_col = late % kLanes * 8, col = c0 + my_col;
+    Raw8<DT_BF16> bias, residual[kOuts];
+    if (a.bias && col < a.n)
+        bias = load8<DT_BF16>(reinterpret_cast<const char *>(a.bias), col, a.n);
+    if (a.residual && parts == 1) {
+        const rsrc_t from = make_rsrc(a.residual + (int64_t)r0 * a.n, (uint32_t)rows * (uint32_t)a.n * 2u);
+#pragma unroll
+        for (int i = 0; i < kOuts; ++i) {
+            const uint32_t row = i * kTogether + my_row;  // rows past the end read zeros
+            residual[i].v[0] = __builtin_amdgcn_raw_buffer_load_b128(
+                from, col < a.n ? (row * (uint32_t)a.n + col) * 2u : kNowhere, 0, 0);
+        }
+    }
+    wait_and_sync();  // the last loads, of nothing, also write shared memory
+    // acc[f][g][e] is row 16 f + lane % 16, column c0 + 16 g + 4 (lane / 16) + e. Through shared memory,
+    // 16 rows at a time, into rows of eight columns a lane.
+    constexpr int kChunks = FN * 4, kOwn = TM * 16 * 2 / W;
+    static_assert(16 * kChunks <= kOwn, "");
+    u32x4 *const own = wave < W / 2 ? s0 + wave * kOwn : s1 + (wave - W / 2) * kOwn;
+#pragma unroll
+    for (int f = 0; f < FM; ++f) {
+#pragma unroll
+        for (int g = 0; g < FN; ++g)
+            own[i16 * kChunks + (g * 4 + q ^ i16 % kChunks)] = __builtin_bit_cast(u32x4, acc[f][g]);
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+        for (int t = 0; t < 16 / kTogether; ++t) {
+            const int r = t * kTogether + my_row, row = r0 + f * 16 + r;
+            float z[8];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const u32x4 v = own[r * kChunks + (my_col / 4 + h ^ r % kChunks)];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    z[4 * h + e] = __uint_as_float(v[e]);
+            }
+            if (row >= a.m || col >= a.n)
+                continue;
+            if (parts > 1)
+                store8<DT_F32>(reinterpret_cast<char *>(partial + ((int64_t)part * a.m + row) * a.n), col, a.n, z);
+            else
+                finish8<DT_BF16>(a, row, col, z, bias, residual[f * 16 / kTogether + t]);
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -77,6 +232,48 @@ bool good_sizes(int64_t m, int64_t n, int64_t k)
            n * k <= ((int64_t)1 << 36) && m * n <= ((int64_t)1 << 36) && m * k <= ((int64_t)1 << 36);
 }
 
+// How a product of many rows is cut: tiles of 16 fm rows of x by 64 fn of W, and the parts of k.
+struct Plan {
+    int fm, fn;
+    int parts;
+};
+
+int64_t tile_count(int64_t m, int64_t n, const Plan &p) { return ceil_div(m, 16 * p.fm) * ceil_div(n, 64 * p.fn); }
+
+// The largest tile that leaves work for most of the 256 CUs; the smallest ones that are still too few
+// for two workgroups a CU share their k.
+Plan plan(int64_t m, int64_t n, int64_t k)
+{
+    Plan p = {4, 4, 1};
+    if (tile_count(m, n, p) < 512)
+        p = {m <= 32 ? 2 : 4, 2, 1};
+    const int64_t steps = ceil_div(k, kFp4K), tiles = tile_count(m, n, p);
+    while (p.fn == 2 && p.parts < 16 && tiles * p.parts * 2 <= 512 && p.parts * 8 <= steps)
+        p.parts *= 2;
+    return p;
+}
+
+template <int FM, int FN>
+block_status_t run_tiles(const Args &a, int parts, float *partial, hipStream_t st)
+{
+    const int tm = (int)ceil_div(a.m, FM * 16), tn = (int)ceil_div(a.n, kTileWaves * FN * 16);
+    const int64_t blocks = ceil_div((int64_t)tm * tn * parts, 8) * 8;
+    return launch(fp4_linear_tile_kernel<FM, FN>, dim3((unsigned)blocks), dim3(kTileWaves * 64), 0, st, a, tm, tn, parts, partial);
+}
+
+block_status_t run_many(const Args &a, float *partial, hipStream_t st)
+{
+    const Plan p = plan(a.m, a.n, a.k);
+    const block_status_t r = p.fn == 4   ? run_tiles<4, 4>(a, p.parts, partial, st)
+                             : p.fm == 4 ? run_tiles<4, 2>(a, p.parts, partial, st)
+                                         : run_tiles<2, 2>(a, p.parts, partial, st);
+    if (r || p.parts == 1)
+        return r;
+    const int64_t blocks = ceil_div((int64_t)a.m * a.n, 2048);
+    return launch(linear_join_kernel<DT_BF16>, dim3((unsigned)(blocks < 4096 ? blocks : 4096)), dim3(256), 0, st, a, p.parts,
+                  partial);
+}
+
 }  // namespace
 
 extern "C" {
@@ -85,7 +282,8 @@ int64_t block_linear_act_fp4_workspace(int64_t m, int64_t n, int64_t k)
 {
     if (!good_sizes(m, n, k) || k % 32 || n % 8 || m <= kFewRows)
         return 0;
-    return round_up(n * k * 2, 16) + block_linear_act_workspace(m, n, k);
+    const Plan p = plan(m, n, k);
+    return p.parts > 1 ? p.parts * m * n * 4 : 0;
 }
 
 block_status_t block_linear_act_fp4(const uint16_t *x, const uint8_t *codes, const uint8_t *scales, const uint16_t *bias,
@@ -108,15 +306,9 @@ block_status_t block_linear_act_fp4(const uint16_t *x, const uint8_t *codes, con
     if (any_overlap<2, 5>({{y, m * n * 2}, {workspace, need}},
                           {{x, m * k * 2}, {codes, s.codes()}, {scales, s.scales()}, {bias, n * 2}, {residual, m * n * 2}}))
         return BLOCK_ERR_INVALID_ARG;
-    if (m > kFewRows) {  // the weights' bf16 values, then the product with those
-        const int64_t wide = round_up(n * k * 2, 16);
-        uint16_t *weight = static_cast<uint16_t *>(workspace);
-        if (const block_status_t r = block_fp4_dequantize(codes, scales, weight, 1, n, k, stream))
-            return r;
-        return block_linear_act(x, weight, bias, residual, y, m, n, k, act, BLOCK_BF16,
-                                static_cast<char *>(workspace) + wide, need - wide, stream);
-    }
-    const Args a = {x, codes, scales, bias, residual, y, (int)m, (int)n, (int)k, act};
+    const Args a = {{x, nullptr, bias, residual, y, (int)m, (int)n, (int)k, act}, codes, scales};
+    if (m > kFewRows)
+        return run_many(a, static_cast<float *>(workspace), stream);
     const dim3 grid((unsigned)s.row_tiles()), threads(kWaves * 64);
     return m <= 4 ? launch(fp4_linear_few_kernel<1, 4>, grid, threads, 0, stream, a)
                   : launch(fp4_linear_few_kernel<4, 2>, grid, threads, 0, stream, a);

@@ -17,10 +17,12 @@ struct Tiles {
     rsrc_t codes, scales;
 };
 
-__device__ __forceinline__ Tiles tiles_of(const uint8_t *codes, const uint8_t *scales, int64_t block, int k_tiles)
+// there: whether the matrix has such a block (its tiles read zeros otherwise).
+__device__ __forceinline__ Tiles tiles_of(const uint8_t *codes, const uint8_t *scales, int64_t block, int k_tiles,
+                                          bool there = true)
 {
-    return {make_rsrc(codes + block * k_tiles * kFp4Codes, (uint32_t)k_tiles * kFp4Codes),
-            make_rsrc(scales + block * k_tiles * kFp4Scales, (uint32_t)k_tiles * kFp4Scales)};
+    return {make_rsrc(codes + block * k_tiles * kFp4Codes, there ? (uint32_t)k_tiles * kFp4Codes : 0u),
+            make_rsrc(scales + block * k_tiles * kFp4Scales, there ? (uint32_t)k_tiles * kFp4Scales : 0u)};
 }
 
 // A wave's next tiles of RT row blocks, in flight.
@@ -28,12 +30,14 @@ template <int RT>
 struct Ahead {
     u32x4 codes[RT];
     uint32_t scales[RT];
+    // kCached: of weights that other workgroups read too; past the caches otherwise.
+    template <bool kCached = false>
     __device__ __forceinline__ void load(const Tiles (&w)[RT], int t)
     {
         const int lane = lane_id();
 #pragma unroll
         for (int i = 0; i < RT; ++i) {  // a tile past the last reads zeros
-            codes[i] = __builtin_amdgcn_raw_buffer_load_b128(w[i].codes, lane * 16, t * kFp4Codes, kLoadAux);
+            codes[i] = __builtin_amdgcn_raw_buffer_load_b128(w[i].codes, lane * 16, t * kFp4Codes, kCached ? 0 : kLoadAux);
             scales[i] = __builtin_amdgcn_raw_buffer_load_b32(w[i].scales, lane % 16 * 4, t * kFp4Scales, 0);
         }
     }

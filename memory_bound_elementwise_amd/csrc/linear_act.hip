@@ -10,59 +10,18 @@
 #include <stdint.h>
 
 #include "block_host.h"
+#include "linear_tiles.h"
 #include "weight_stream.h"
 
 namespace {
 
 using namespace block;
 
-struct Args {
-    const uint16_t *x, *w, *bias, *residual;
-    uint16_t *y;
-    int m, n, k, act;
-};
-
-template <int DT>
-__device__ __forceinline__ void finish(const Args &a, int row, int col, float z)
-{
-    if (a.bias)
-        z += load1<DT>(a.bias, col);
-    z = activate(a.act, z);
-    const int64_t at = (int64_t)row * a.n + col;
-    if (a.residual)
-        z += load1<DT>(a.residual, at);
-    store1<DT>(a.y, at, z);
-}
-
-// Eight neighbouring columns at once (col and n multiples of 8), with the bias and the residual
-// there.
-template <int DT>
-__device__ __forceinline__ void finish8(const Args &a, int row, int col, float (&z)[8], const Raw8<DT> &bias,
-                                        const Raw8<DT> &residual)
-{
-    float f[8];
-    if (a.bias) {
-        widen8<DT>(bias, f);
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            z[i] += f[i];
-    }
-    activate8(a.act, z);
-    if (a.residual) {
-        widen8<DT>(residual, f);
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            z[i] += f[i];
-    }
-    // past the caches, which the operands need (6720 x 7168 x 4096: 357 us against 377)
-    __builtin_nontemporal_store(narrow8<DT>(z).v[0], reinterpret_cast<u32x4 *>(a.y + (int64_t)row * a.n + col));
-}
-
 // ---------------------------------------------------------------------------
 // Few rows
 // ---------------------------------------------------------------------------
 template <int DT, int G, int WAVES>
-__global__ __launch_bounds__(WAVES * 64) void linear_few_kernel(Args a)
+__global__ __launch_bounds__(WAVES * 64) void linear_few_kernel(LinearArgs a)
 {
     __shared__ u32x4 shared[WAVES * kStage<1, G, false>];
     const int lane = lane_id(), wave = wave_in_block();
@@ -104,8 +63,6 @@ __global__ __launch_bounds__(WAVES * 64) void linear_few_kernel(Args a)
 // ---------------------------------------------------------------------------
 // Many rows
 // ---------------------------------------------------------------------------
-typedef __attribute__((address_space(3))) void shared_void;
-
 // The largest divisor of n up to most.
 constexpr int most_dividing(int n, int most)
 {
@@ -113,19 +70,6 @@ constexpr int most_dividing(int n, int most)
     while (n % d)
         --d;
     return d;
-}
-
-// Waits for the wave's loads into shared memory and its reads of it, then for the workgroup.
-// (Loads into shared memory count as loads from memory: a fence need not wait for them.)
-// Nothing is moved across.
-__device__ __forceinline__ void wait_and_sync()
-{
-    __builtin_amdgcn_sched_barrier(0);
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0)
-    __builtin_amdgcn_s_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_sched_barrier(0);
 }
 
 // Tiles of TM rows of x by TN rows of W, WM x WN waves, 64 k a step. Both operands go straight
@@ -144,7 +88,7 @@ __device__ __forceinline__ void wait_and_sync()
 // barrier a step and no product waiting for a read.
 //   parts > 1: the sums over one of `parts` ranges of k, to partial [parts][m][n] in fp32.
 template <int DT, int TM, int TN, int WM, int WN>
-__global__ __launch_bounds__(WM * WN * 64) void linear_tile_kernel(Args a, int tiles_m, int tiles_n, int parts,
+__global__ __launch_bounds__(WM * WN * 64) void linear_tile_kernel(LinearArgs a, int tiles_m, int tiles_n, int parts,
                                                                    float *partial)
 {
     constexpr int W = WM * WN, FM = TM / WM / 16, FN = TN / WN / 16;
@@ -300,31 +244,6 @@ __global__ __launch_bounds__(WM * WN * 64) void linear_tile_kernel(Args a, int t
     }
 }
 
-// The parts' sums in order, then the epilogue. A lane takes eight neighbouring columns.
-template <int DT>
-__global__ __launch_bounds__(256) void linear_join_kernel(Args a, int parts, const float *partial)
-{
-    const int64_t all = (int64_t)a.m * a.n;
-    for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8; i < all; i += (int64_t)gridDim.x * 2048) {
-        float z[8] = {};
-        for (int p = 0; p < parts; p += 2) {  // a power of two, at least 2; two loads at a time
-            float f0[8], f1[8];
-            widen8<DT_F32>(load8<DT_F32>(reinterpret_cast<const char *>(partial + p * all + i), 0, 8), f0);
-            widen8<DT_F32>(load8<DT_F32>(reinterpret_cast<const char *>(partial + (p + 1) * all + i), 0, 8), f1);
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                z[e] = z[e] + f0[e] + f1[e];
-        }
-        const int row = (int)(i / a.n), col = (int)(i % a.n);
-        Raw8<DT> bias, residual;
-        if (a.bias)
-            bias = load8<DT>(reinterpret_cast<const char *>(a.bias), col, a.n);
-        if (a.residual)
-            residual = load8<DT>(reinterpret_cast<const char *>(a.residual + i), 0, 8);
-        finish8<DT>(a, row, col, z, bias, residual);
-    }
-}
-
 // ---------------------------------------------------------------------------
 // Host
 // ---------------------------------------------------------------------------
@@ -367,7 +286,7 @@ Plan plan(int64_t m, int64_t n, int64_t k)
 }
 
 template <int DT, int TM, int TN, int WM, int WN>
-block_status_t run_tiles(const Args &a, int parts, float *partial, hipStream_t st)
+block_status_t run_tiles(const LinearArgs &a, int parts, float *partial, hipStream_t st)
 {
     const int tm = (int)ceil_div(a.m, TM), tn = (int)ceil_div(a.n, TN);
     const int64_t blocks = ceil_div((int64_t)tm * tn * parts, 8) * 8;
@@ -376,7 +295,7 @@ block_status_t run_tiles(const Args &a, int parts, float *partial, hipStream_t s
 }
 
 template <int DT>
-block_status_t run(const Args &a, float *partial, hipStream_t st)
+block_status_t run(const LinearArgs &a, float *partial, hipStream_t st)
 {
     if (a.m <= kFewRows) {
         const dim3 grid((unsigned)ceil_div(a.n, 16));
@@ -435,7 +354,7 @@ block_status_t block_linear_act(const void *x, const void *weight, const void *b
     if (any_overlap<2, 4>({{y, m * n * 2}, {workspace, need}},
                           {{x, m * k * 2}, {weight, n * k * 2}, {bias, n * 2}, {residual, m * n * 2}}))
         return BLOCK_ERR_INVALID_ARG;
-    Args a = {};
+    LinearArgs a = {};
     a.x = static_cast<const uint16_t *>(x), a.w = static_cast<const uint16_t *>(weight);
     a.bias = static_cast<const uint16_t *>(bias), a.residual = static_cast<const uint16_t *>(residual);
     a.y = static_cast<uint16_t *>(y), a.m = (int)m, a.n = (int)n, a.k = (int)k, a.act = act;

@@ -86,8 +86,7 @@ def linear_act_fp4_workspace(m: int, n: int, k: int) -> int:
 def linear_act_fp4(x, codes, scales, y, *, bias=None, activation=None, residual=None, workspace=None, stream=None):
     """``linear_act`` with the weight [n, k] in 4 bits: y = act(x @ weight.T + bias) + residual; x
     [m, k], bias [n], residual and y [m, n] bf16, products exact, sums and epilogue fp32, one
-    rounding. n a multiple of 8, k of 32. Up to 64 rows read the weight once; more go through
-    its bf16 values in the workspace. Forward only."""
+    rounding. n a multiple of 8, k of 32. Forward only."""
     m, k = _rows(x, "x")
     n = _rows(y, "y")[1]
     if activation not in ACTIVATIONS:

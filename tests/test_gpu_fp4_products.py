@@ -79,6 +79,19 @@ def test_linear_long_and_wide(m, n, k):
     _check_linear(m, n, k, "silu")
 
 
+@pytest.mark.parametrize("m,n,k", [(2050, 4088, 160), (2100, 4104, 32), (1030, 8200, 288), (4100, 2056, 1056)])
+def test_linear_many_tiles(m, n, k):
+    """Enough tiles for the widest ones, ragged on every side; the 64-bit product runs on the GPU
+    (float64 matmul)."""
+    say(f"[linear_fp4] m {m} n {n} k {k}")
+    g = torch.Generator().manual_seed(m)
+    x, b, r = _normal(g, m, k), _normal(g, n), _normal(g, m, n)
+    v, w = _weights(g, n, k, std=k ** -0.5)
+    y = _linear(x, w, b, r, "silu", n)
+    want, bound, _ = ref.linear_act(x.to(DEV).double(), v.to(DEV), b.to(DEV).double(), "silu", r.to(DEV).double(), BF)
+    ref.check(y, want.cpu(), bound.cpu(), f"linear {m}x{n}x{k}")
+
+
 def test_linear_scales():
     """Each group by its own scale, exactly: the smallest powers too; a NaN group reaches its own
     column alone."""
