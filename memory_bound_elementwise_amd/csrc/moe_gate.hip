@@ -164,32 +164,28 @@ __device__ __forceinline__ void softmax(const double (&v)[V], double (&s)[V])
         s[i] *= q;
 }
 
-template <int SRC, int L, int V>
-__global__ __launch_bounds__(kWavesHere * 64) void gate_kernel(GateArgs a)
+// A token's room in its wave's shared memory.
+struct Room {
+    uint64_t *table;  // an entry an expert
+    uint64_t *worth;  // an entry a group
+    int *kept;        // which groups are kept
+};
+
+// Lanes of a token that look through one group together: a power of two.
+template <int L>
+__device__ __forceinline__ int lanes_a_group(int groups)
+{
+    return groups >= L ? 1 : L >> (32 - __builtin_clz(groups - 1));
+}
+
+// The choice, in fp64: lane l gets the experts of slots l, L + l, ... and their scores. v: the
+// logits, -inf past the last expert.
+template <int L, int V, int Q>
+__device__ __forceinline__ void choose(const GateRule &r, int experts, int l, const double (&v)[V], const float (&bias)[V],
+                                       const Room &room, int (&id)[Q], double (&p)[Q])
 {
     constexpr int T = 64 / L;
-    __shared__ uint64_t tables[kWavesHere][T][L * V];
-    __shared__ uint64_t worths[kWavesHere][T][kGateGroups];
-    __shared__ int kept_groups[kWavesHere][T][kGateGroups];
-    const GateRule r = a.rule;
-    const int lane = lane_id(), wave = wave_in_block(), l = lane % L, tl = lane / L;
-    const int first = ((int)blockIdx.x * kWavesHere + wave) * T, live = live_tokens(a.valid, a.tokens);
-    if (first >= live)
-        return;
-    const bool mine = first + tl < live;
-    const int t = mine ? first + tl : first;  // past the last token: the first one again, not stored
-    uint64_t *table = tables[wave][tl], *worth = worths[wave][tl];
-    int *kept = kept_groups[wave][tl];
-    const int64_t row = (int64_t)t * a.experts, part = (int64_t)a.tokens * a.experts;
-
-    double v[V], s[V];
-    float bias[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const int e = i * L + l;
-        bias[i] = a.bias && e < a.experts ? a.bias[e] : 0.0f;
-        v[i] = e < a.experts ? logit<SRC>(a.logits, row + e, part, a.parts) : -INFINITY;
-    }
+    double s[V];
     if (r.scores == BLOCK_SCORES_SIGMOID) {
 #pragma unroll
         for (int i = 0; i < V; ++i)
@@ -201,17 +197,16 @@ __global__ __launch_bounds__(kWavesHere * 64) void gate_kernel(GateArgs a)
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int e = i * L + l;
-        key[i] = e < a.experts ? order_key(v[i] == -INFINITY ? v[i] : s[i] + (double)bias[i]) : 0;
+        key[i] = e < experts ? order_key(v[i] == -INFINITY ? v[i] : s[i] + (double)bias[i]) : 0;
     }
     if (r.groups > 1) {
-        const int size = a.experts / r.groups;
+        const int size = experts / r.groups;
         const unsigned inverse = ((1u << 20) + size - 1) / size;  // e / size = e inverse / 2^20 for e, size <= 1024
 #pragma unroll
         for (int i = 0; i < V; ++i)
-            table[i * L + l] = key[i];
+            room.table[i * L + l] = key[i];
         wave_fence();
-        // the lanes of a token share its groups: `each` lanes, a power of two, look through one
-        const int each = r.groups >= L ? 1 : L >> (32 - __builtin_clz(r.groups - 1));
+        const int each = lanes_a_group<L>(r.groups);
         for (int g0 = 0; g0 < r.groups; g0 += L / each) {
             const int g = g0 + l / each;
             uint64_t first_key = 0, second_key = 0;
@@ -222,7 +217,7 @@ __global__ __launch_bounds__(kWavesHere * 64) void gate_kernel(GateArgs a)
 #pragma unroll
                 for (int i = 0; i < kTogether; ++i) {
                     const int m = m0 + i * each;
-                    k[i] = table[from + (m < size ? m : 0)];
+                    k[i] = room.table[from + (m < size ? m : 0)];
                     k[i] = m < size ? k[i] : 0;
                 }
 #pragma unroll
@@ -238,22 +233,22 @@ __global__ __launch_bounds__(kWavesHere * 64) void gate_kernel(GateArgs a)
             }
             const double w = of_key(first_key);
             if (g < r.groups && l % each == 0)
-                worth[g] = order_key(r.group_top == 2 ? w + of_key(second_key) : w);
+                room.worth[g] = order_key(r.group_top == 2 ? w + of_key(second_key) : w);
         }
         wave_fence();
         for (int g = l; g < r.groups; g += L) {
-            const uint64_t own = worth[g];
+            const uint64_t own = room.worth[g];
             int before = 0;
 #pragma unroll 8
             for (int o = 0; o < r.groups; ++o)
-                before += worth[o] > own || (worth[o] == own && o < g);
-            kept[g] = before < r.top_groups;
+                before += room.worth[o] > own || (room.worth[o] == own && o < g);
+            room.kept[g] = before < r.top_groups;
         }
         wave_fence();
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const unsigned e = i * L + l;
-            if ((int)e < a.experts && !kept[e * inverse >> 20])
+            if ((int)e < experts && !room.kept[e * inverse >> 20])
                 key[i] = 0;
         }
         wave_fence();
@@ -264,8 +259,6 @@ __global__ __launch_bounds__(kWavesHere * 64) void gate_kernel(GateArgs a)
 #pragma unroll
     for (int i = 0; i < V; ++i)
         hi[i] = (unsigned)(key[i] >> 32);
-    constexpr int Q = kGateSlots / L;
-    int id[Q];  // lane l has slots l, L + l, ...
 #pragma unroll
     for (int q = 0; q < Q; ++q)
         id[q] = 0;
@@ -302,17 +295,64 @@ __global__ __launch_bounds__(kWavesHere * 64) void gate_kernel(GateArgs a)
             id[q] = q * L + l == j ? e : id[q];
     }
     wave_fence();
-    double *score = reinterpret_cast<double *>(table);
+    double *score = reinterpret_cast<double *>(room.table);
 #pragma unroll
     for (int i = 0; i < V; ++i)
         score[i * L + l] = s[i];
     wave_fence();
-    double p[Q], sum = 0.0;
 #pragma unroll
-    for (int q = 0; q < Q; ++q) {
+    for (int q = 0; q < Q; ++q)
         p[q] = q * L + l < r.top_k ? score[id[q]] : 0.0;
-        sum += p[q];
+}
+
+template <int SRC, int L, int V>
+__global__ __launch_bounds__(kWavesHere * 64) void gate_kernel(GateArgs a)
+{
+    constexpr int T = 64 / L;
+    __shared__ uint64_t tables[kWavesHere][T][L * V];
+    __shared__ uint64_t worths[kWavesHere][T][kGateGroups];
+    __shared__ int kept_groups[kWavesHere][T][kGateGroups];
+    const GateRule r = a.rule;
+    const int lane = lane_id(), wave = wave_in_block(), l = lane % L, tl = lane / L;
+    const int first = ((int)blockIdx.x * kWavesHere + wave) * T, live = live_tokens(a.valid, a.tokens);
+    if (first >= live)
+        return;
+    const bool mine = first + tl < live;
+    const int t = mine ? first + tl : first;  // past the last token: the first one again, not stored
+    uint64_t *table = tables[wave][tl], *worth = worths[wave][tl];
+    int *kept = kept_groups[wave][tl];
+    const int64_t row = (int64_t)t * a.experts, part = (int64_t)a.tokens * a.experts;
+
+    // Loads without branches, past the last expert of the first one again: all of them are on their way
+    // together, and what follows is no chain of branches either. (With a condition around each
+    // load, 6720 x 256 took 14.7 us.)
+    double v[V];
+    float bias[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int e = i * L + l < a.experts ? i * L + l : 0;
+        v[i] = logit<SRC>(a.logits, row + e, part, a.parts);
     }
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        bias[i] = 0.0f;
+    if (a.bias) {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            bias[i] = a.bias[i * L + l < a.experts ? i * L + l : 0];
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        v[i] = i * L + l < a.experts ? v[i] : -INFINITY;
+    constexpr int Q = kGateSlots / L;
+    int id[Q];  // lane l has slots l, L + l, ...
+    double p[Q];
+    const Room room = {table, worth, kept};
+    choose<L, V, Q>(r, a.experts, l, v, bias, room, id, p);
+    double sum = 0.0;
+#pragma unroll
+    for (int q = 0; q < Q; ++q)
+        sum += p[q];
     if (r.renormalize) {
         sum = lanes_sum<L>(sum);
 #pragma unroll
@@ -365,10 +405,11 @@ __global__ __launch_bounds__(kWavesHere * 64) void gate_grad_kernel(GateGradArgs
     if constexpr (DENSE) {
         double v[V];
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int e = i * L + l;
-            v[i] = e < a.experts ? (double)load1<DT>(a.logits, row + e) : -INFINITY;
-        }
+        for (int i = 0; i < V; ++i)
+            v[i] = (double)load1<DT>(a.logits, row + (i * L + l < a.experts ? i * L + l : 0));
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            v[i] = i * L + l < a.experts ? v[i] : -INFINITY;
         softmax<L, V>(v, s);
 #pragma unroll
         for (int i = 0; i < V; ++i)
@@ -379,18 +420,20 @@ __global__ __launch_bounds__(kWavesHere * 64) void gate_grad_kernel(GateGradArgs
     double x[Q], g[Q];  // the slot's logit (DENSE: score), its gradient
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
-        const int j = q * L + l;
-        id[q] = -1;
-        x[q] = -INFINITY;
-        g[q] = 0.0;
-        if (j < a.top_k) {
-            const int e = a.ids[(int64_t)t * a.top_k + j];
-            if (e >= 0 && e < a.experts) {
-                id[q] = e;
-                x[q] = DENSE ? table[e] : (double)load1<DT>(a.logits, row + e);
-                g[q] = (double)a.scale * (double)a.grad_probs[(int64_t)t * a.top_k + j];
-            }
-        }
+        const int j = q * L + l, at = j < a.top_k ? j : 0;
+        const int e = a.ids[(int64_t)t * a.top_k + at];
+        g[q] = (double)a.scale * (double)a.grad_probs[(int64_t)t * a.top_k + at];
+        id[q] = j < a.top_k && e >= 0 && e < a.experts ? e : -1;
+    }
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+        const int e = id[q] < 0 ? 0 : id[q];
+        x[q] = DENSE ? table[e] : (double)load1<DT>(a.logits, row + e);
+    }
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+        x[q] = id[q] < 0 ? -INFINITY : x[q];
+        g[q] = id[q] < 0 ? 0.0 : g[q];
     }
     wave_fence();
 #pragma unroll
@@ -409,7 +452,7 @@ __global__ __launch_bounds__(kWavesHere * 64) void gate_grad_kernel(GateGradArgs
         if (a.scores == BLOCK_SCORES_SIGMOID) {
 #pragma unroll
             for (int q = 0; q < Q; ++q)
-                p[q] = sigmoid(x[q]);
+                p[q] = q * L < a.top_k ? sigmoid(x[q]) : 0.0;
         } else {
             softmax<L, Q>(x, p);
         }
@@ -429,7 +472,7 @@ __global__ __launch_bounds__(kWavesHere * 64) void gate_grad_kernel(GateGradArgs
 #pragma unroll
         for (int q = 0; q < Q; ++q) {
             out[q] = p[q] * (g[q] - dot);
-            if (a.scores == BLOCK_SCORES_SIGMOID)
+            if (a.scores == BLOCK_SCORES_SIGMOID && q * L < a.top_k)
                 out[q] *= sigmoid(-x[q]);
         }
     }
@@ -482,13 +525,15 @@ template <int DT, bool DENSE>
 block_status_t run_gate_grad(const GateGradArgs &a, hipStream_t st)
 {
     const dim3 threads(kWavesHere * 64);
-    const unsigned few = groups_of(a.tokens, 64), many = groups_of(a.tokens, 16);
+    const unsigned few = groups_of(a.tokens, 64);
     if (a.experts <= 64)
-        return a.tokens <= kFewTokens ? launch(gate_grad_kernel<DT, 64, 1, DENSE>, dim3(few), threads, 0, st, a)
-                                      : launch(gate_grad_kernel<DT, 16, 4, DENSE>, dim3(many), threads, 0, st, a);
+        return a.tokens <= kFewTokens
+                   ? launch(gate_grad_kernel<DT, 64, 1, DENSE>, dim3(few), threads, 0, st, a)
+                   : launch(gate_grad_kernel<DT, 16, 4, DENSE>, dim3(groups_of(a.tokens, 16)), threads, 0, st, a);
     if (a.experts <= 256)
-        return a.tokens <= kFewTokens ? launch(gate_grad_kernel<DT, 64, 4, DENSE>, dim3(few), threads, 0, st, a)
-                                      : launch(gate_grad_kernel<DT, 16, 16, DENSE>, dim3(many), threads, 0, st, a);
+        return a.tokens <= kFewTokens
+                   ? launch(gate_grad_kernel<DT, 64, 4, DENSE>, dim3(few), threads, 0, st, a)
+                   : launch(gate_grad_kernel<DT, 32, 8, DENSE>, dim3(groups_of(a.tokens, 32)), threads, 0, st, a);
     return launch(gate_grad_kernel<DT, 64, 16, DENSE>, dim3(few), threads, 0, st, a);
 }
 
