@@ -227,22 +227,25 @@ __global__ __launch_bounds__(kWaves * 64) void fp4_up_kernel(ExpertArgs a)
 // wave has gate and up of 16 columns of the activation, or 32 columns of one product.
 constexpr int kManyWaves = 8;
 
+template <int G>
+using UpWalk = Walk<2, G, kManyWaves, 2, false>;
+
 template <int ACT, int G>
-__device__ __forceinline__ void up_many_pass(const ExpertArgs &a, const Tiles (&w)[2], Ahead<2> &even, Ahead<2> &odd,
-                                             int c0, const uint16_t *list, int n, u32x4 *xs)
+__device__ __forceinline__ void up_many_pass(const ExpertArgs &a, UpWalk<G> &walk, typename UpWalk<G>::Ends &ends, int c0,
+                                             const uint16_t *list, int n, u32x4 *xs)
 {
-    constexpr int W = kManyWaves, kLoads = kOwnLoads<G, W>;
+    constexpr int W = kManyWaves;
     const int lane = lane_id(), wave = wave_in_block();
     const rsrc_t x = make_rsrc(a.x, (uint32_t)a.tokens * (uint32_t)a.hidden * 2u);
-    uint32_t col[kLoads];
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
+    for (int i = 0; i < UpWalk<G>::kLoads; ++i) {
         const int s = 4 * (wave + i * W) + lane / 16;
-        col[i] = s < n ? (uint32_t)(list[s] / a.top_k) * (uint32_t)a.hidden * 2u + lane % 16 * 16 : kNowhere;
+        ends.col[i] = s < n ? (uint32_t)(list[s] / a.top_k) * (uint32_t)a.hidden * 2u + lane % 16 * 16 : kNowhere;
     }
     f32x4 acc[2][G];
     clear(acc);
-    walk_products<2, G, W>(acc, w, even, odd, x, col, a.hidden, (n + 15) / 16, xs);
+    walk.start_columns(x, ends, a.hidden);
+    walk.run(acc, x, ends, ends, a.hidden, (n + 15) / 16, xs);
     if (c0 >= a.inter)
         return;
     const int64_t plane = (int64_t)a.tokens * a.top_k * a.inter;
@@ -285,24 +288,22 @@ __global__ __launch_bounds__(kManyWaves * 64, G == 1 ? 8 : 4) void fp4_up_many_k
     constexpr int kCols = ACT == ACT_SWIGLU ? 16 : 32;
     const int c0 = (blockIdx.x * kManyWaves + wave_in_block()) * kCols, blocks = a.inter / 16;
     const int k_tiles = c0 < a.inter ? (a.hidden + kFp4K - 1) / kFp4K : 0;  // past the end: none, but its part of x
-    Tiles w[2];
+    typename UpWalk<G>::Ends ends;
 #pragma unroll
     for (int i = 0; i < 2; ++i)
-        w[i] = tiles_of(a.up_codes, a.up_scales,
-                        k_tiles == 0 ? 0 : (ACT == ACT_SWIGLU ? ((int64_t)e * 2 + i) * blocks : (int64_t)e * blocks + i) + c0 / 16,
-                        k_tiles);
-    Ahead<2> even, odd;  // on their way while the pairs are looked for
-    even.load(w, 0);
-    odd.load(w, 1);
+        ends.w.block[i] = tiles_of(a.up_codes, a.up_scales,
+                             k_tiles == 0 ? 0 : (ACT == ACT_SWIGLU ? ((int64_t)e * 2 + i) * blocks : (int64_t)e * blocks + i) + c0 / 16,
+                             k_tiles);
+    UpWalk<G> walk;
+    walk.start_tiles(ends);  // on their way while the pairs are looked for
     const int n = expert_pairs<kManyWaves>(a, pairs, e, list, counts);
     for (int p = 0; p < n; p += G * 16) {
         const int m = n - p < G * 16 ? n - p : G * 16;
         if (p > 0) {
-            sync_shared();  // the columns lie elsewhere in xs now
-            even.load(w, 0);
-            odd.load(w, 1);
+            sync_shared();  // what is in xs has been read
+            walk.start_tiles(ends);
         }
-        up_many_pass<ACT, G>(a, w, even, odd, c0, list + p, m, xs);
+        up_many_pass<ACT, G>(a, walk, ends, c0, list + p, m, xs);
     }
 }
 
@@ -442,65 +443,125 @@ __global__ __launch_bounds__(kWaves * 64) void fp4_down_kernel(ExpertArgs a)
     }
 }
 
-// Down products where experts have many tokens, as up: four waves of four row tiles (64 columns of the
-// output) each.
-constexpr int kDownWaves = 4, kDownTiles = 4;
+// Down products where experts have many tokens: units of one expert, up to G * 5 of its pairs and
+// four waves of four row tiles (64 columns of the output) each. A workgroup takes every
+// gridDim.x-th unit, and its walk over one ends by sending for the next one's first steps: k is
+// short here (2048: 16 steps), and a workgroup a unit spent half of its time on its ends (7168 x
+// 2048, 64 tokens, 64 experts: 125 us).
+constexpr int kDownWaves = 8, kDownTiles = 2;
 
 template <int G>
-__device__ __forceinline__ void down_many_pass(const ExpertArgs &a, const Tiles (&w)[kDownTiles], Ahead<kDownTiles> &even,
-                                               Ahead<kDownTiles> &odd, int c0, const uint16_t *list, int n, u32x4 *xs)
+__global__ __launch_bounds__(kDownWaves * 64, 4) void fp4_down_many_kernel(ExpertArgs a)
 {
-    constexpr int RT = kDownTiles, W = kDownWaves, kLoads = kOwnLoads<G, W>;
-    const int lane = lane_id(), wave = wave_in_block();
-    const rsrc_t h = terms_of(a);
-    uint32_t col[kLoads];
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-        const int at = 4 * (wave + i * W) + lane / 16;
-        col[i] = term_column(a, list, n, at / 16 * kPairs, at % 16) + lane % 16 * 16;
-    }
-    f32x4 acc[RT][G];
-    clear(acc);
-    walk_products<RT, G, W>(acc, w, even, odd, h, col, a.inter, (n + kPairs - 1) / kPairs, xs);
-#pragma unroll
-    for (int g = 0; g < G; ++g) {
-        const int c = lane % 16, s = g * kPairs + c / 3;
-#pragma unroll
-        for (int i = 0; i < RT; ++i) {
-            const f32x4 z = join_terms(acc[i][g]);
-            if (c < 15 && c % 3 == 0 && s < n && c0 + 16 * i < a.hidden)
-                *reinterpret_cast<f32x4 *>(a.z + (int64_t)list[s] * a.hidden + c0 + 16 * i + lane / 16 * 4) = z;
-        }
-    }
-}
-
-template <int G>
-__global__ __launch_bounds__(kDownWaves * 64, G == 4 ? 2 : 3) void fp4_down_many_kernel(ExpertArgs a)
-{
+    using DownWalk = Walk<kDownTiles, G, kDownWaves, 2, true>;
+    constexpr int kThreads = kDownWaves * 64, kOnce = G * kPairs;  // pairs of a unit
     __shared__ u32x4 xs[2 * G * 256];
-    __shared__ uint16_t list[kMaxPairs];
-    __shared__ int counts[kMaxPairs / 64];
-    const int pairs = live_tokens(a.valid, a.tokens) * a.top_k, e = own_expert(a, pairs);
-    if (e < 0)
-        return;
-    const int blocks = a.hidden / 16, b0 = (blockIdx.x * kDownWaves + wave_in_block()) * kDownTiles;
-    Tiles w[kDownTiles];
+    __shared__ uint16_t loose[kMaxPairs], list[kMaxPairs];
+    __shared__ uint16_t unit_at[kMaxPairs], unit_end[kMaxPairs], unit_expert[kMaxPairs];
+    __shared__ int start[kMaxExperts];  // first counts, then where an expert's next pair goes
+    __shared__ int unit_count;
+    const int lane = lane_id(), wave = wave_in_block(), tid = threadIdx.x;
+    const int pairs = live_tokens(a.valid, a.tokens) * a.top_k;
+    for (int e = tid; e < a.experts; e += kThreads)
+        start[e] = 0;
+    __syncthreads();
+    for (int p = tid; p < pairs; p += kThreads) {
+        const int e = a.ids[p];
+        if (e >= 0 && e < a.experts)
+            atomicAdd(&start[e], 1);
+    }
+    __syncthreads();
+    if (wave == 0) {  // where each expert's pairs start, and its units
+        int at = 0, units = 0;
+        for (int e0 = 0; e0 < a.experts; e0 += 64) {
+            const int n = e0 + lane < a.experts ? start[e0 + lane] : 0, own = (n + kOnce - 1) / kOnce;
+            int sum = n, count = own;
 #pragma unroll
-    for (int i = 0; i < kDownTiles; ++i)  // past the last: no rows of W, but its part of h
-        w[i] = tiles_of(a.down_codes, a.down_scales, b0 + i < blocks ? (int64_t)e * blocks + b0 + i : 0,
-                        b0 + i < blocks ? (a.inter + kFp4K - 1) / kFp4K : 0);
-    Ahead<kDownTiles> even, odd;
-    even.load(w, 0);
-    odd.load(w, 1);
-    const int n = expert_pairs<kDownWaves>(a, pairs, e, list, counts);
-    for (int p = 0; p < n; p += G * kPairs) {
-        const int m = n - p < G * kPairs ? n - p : G * kPairs;
-        if (p > 0) {
-            sync_shared();
-            even.load(w, 0);
-            odd.load(w, 1);
+            for (int d = 1; d < 64; d *= 2) {
+                const int s = __shfl_up(sum, d), c = __shfl_up(count, d);
+                sum += lane >= d ? s : 0;
+                count += lane >= d ? c : 0;
+            }
+            const int first = at + sum - n;
+            if (e0 + lane < a.experts)
+                start[e0 + lane] = first;
+            for (int i = 0; i < own; ++i) {
+                const int u = units + count - own + i;
+                unit_expert[u] = (uint16_t)(e0 + lane);
+                unit_at[u] = (uint16_t)(first + i * kOnce);
+                unit_end[u] = (uint16_t)(first + (i + 1) * kOnce < first + n ? first + (i + 1) * kOnce : first + n);
+            }
+            at += __shfl(sum, 63);
+            units += __shfl(count, 63);
         }
-        down_many_pass<G>(a, w, even, odd, b0 * 16, list + p, m, xs);
+        if (lane == 0)
+            unit_count = units;
+    }
+    __syncthreads();
+    // The pairs by expert, each expert's in any order at first, then in increasing order: workgroups
+    // share an expert's pairs, so all of them have to cut the same list.
+    for (int p = tid; p < pairs; p += kThreads) {
+        const int e = a.ids[p];
+        if (e >= 0 && e < a.experts)
+            loose[atomicAdd(&start[e], 1)] = (uint16_t)p;
+    }
+    __syncthreads();
+    for (int p = tid; p < pairs; p += kThreads) {
+        const int e = a.ids[p];
+        if (e < 0 || e >= a.experts)
+            continue;
+        const int first = e > 0 ? start[e - 1] : 0, end = start[e];  // its end is where the next one starts
+        int before = 0;
+#pragma unroll 8
+        for (int i = first; i < end; ++i)
+            before += loose[i] < p;
+        list[first + before] = (uint16_t)p;
+    }
+    __syncthreads();
+
+    const int blocks = a.hidden / 16, row_units = (blocks + kDownWaves * kDownTiles - 1) / (kDownWaves * kDownTiles);
+    const int units = unit_count * row_units, k_tiles = (a.inter + kFp4K - 1) / kFp4K;
+    const rsrc_t h = terms_of(a);
+    auto block_of = [&](int u) { return (u % row_units * kDownWaves + wave) * kDownTiles; };
+    auto ends_of = [&](typename DownWalk::Ends &ends, int u) {
+        const bool there = u < units;  // past the last one: nothing is loaded
+        const int at = there ? u / row_units : 0;
+        const int e = __builtin_amdgcn_readfirstlane(unit_expert[at]), b0 = block_of(u);
+        const int from = __builtin_amdgcn_readfirstlane(unit_at[at]), n = __builtin_amdgcn_readfirstlane(unit_end[at]) - from;
+        const int rows = !there || b0 >= blocks ? 0 : (blocks - b0 < kDownTiles ? blocks - b0 : kDownTiles);
+        ends.w = run_of(a.down_codes, a.down_scales, rows ? (int64_t)e * blocks + b0 : 0, k_tiles, rows);
+#pragma unroll
+        for (int i = 0; i < DownWalk::kLoads; ++i) {
+            const int c = 4 * (wave + i * kDownWaves) + lane / 16;
+            ends.col[i] = there ? term_column(a, list + from, n, c / 16 * kPairs, c % 16) + lane % 16 * 16 : kNowhere;
+        }
+    };
+    int u = blockIdx.x;
+    if (u >= units)
+        return;
+    typename DownWalk::Ends ends, next;
+    DownWalk walk;
+    ends_of(ends, u);
+    walk.start_tiles(ends);
+    walk.start_columns(h, ends, a.inter);
+    for (; u < units; u += gridDim.x) {
+        const int at = u / row_units, b0 = block_of(u);
+        const int from = __builtin_amdgcn_readfirstlane(unit_at[at]), n = __builtin_amdgcn_readfirstlane(unit_end[at]) - from;
+        ends_of(next, u + gridDim.x);
+        f32x4 acc[kDownTiles][G];
+        clear(acc);
+        walk.run(acc, h, ends, next, a.inter, (n + kPairs - 1) / kPairs, xs);
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+            const int c = lane % 16, s = g * kPairs + c / 3;
+#pragma unroll
+            for (int i = 0; i < kDownTiles; ++i) {
+                const f32x4 z = join_terms(acc[i][g]);
+                if (c < 15 && c % 3 == 0 && s < n && b0 + i < blocks)
+                    *reinterpret_cast<f32x4 *>(a.z + (int64_t)list[from + s] * a.hidden + (b0 + i) * 16 + lane / 16 * 4) = z;
+            }
+        }
+        ends = next;
     }
 }
 
@@ -613,7 +674,10 @@ block_status_t launch_down(const ExpertArgs &a, int groups, unsigned each, hipSt
     const int pairs = a.tokens * a.top_k;
     block_status_t r;
     if (shares_columns(a.hidden, each) && a.tokens > 1) {
-        const dim3 grid((unsigned)ceil_div(a.hidden, kDownWaves * kDownTiles * 16), each), threads(kDownWaves * 64);
+        // as many workgroups as fit, and of these as many as have the same number of units
+        const int64_t units = ceil_div(a.hidden, kDownWaves * kDownTiles * 16) * (each + pairs / (groups * kPairs));
+        const int64_t fit = 256 * 2;
+        const dim3 grid((unsigned)ceil_div(units, ceil_div(units, fit))), threads(kDownWaves * 64);
         if (groups == 1)
             r = launch(fp4_down_many_kernel<1>, grid, threads, 0, st, a);
         else if (groups == 2)

@@ -4,6 +4,8 @@
 #ifndef MBE_FP4_STREAM_H
 #define MBE_FP4_STREAM_H
 
+#include <type_traits>
+
 #include "fp4.h"
 
 namespace block {
@@ -25,7 +27,22 @@ __device__ __forceinline__ Tiles tiles_of(const uint8_t *codes, const uint8_t *s
             make_rsrc(scales + block * k_tiles * kFp4Scales, there ? (uint32_t)k_tiles * kFp4Scales : 0u)};
 }
 
-// A wave's next tiles of RT row blocks, in flight.
+// Neighbouring row blocks of one matrix: the first one's tiles and the distance of the blocks, in k
+// tiles. (A resource a block would take four times the scalar registers.)
+struct TileRun {
+    Tiles first;
+    int k_tiles;
+};
+
+// rows: the blocks that are there, of those that are asked for.
+__device__ __forceinline__ TileRun run_of(const uint8_t *codes, const uint8_t *scales, int64_t block, int k_tiles, int there)
+{
+    return {{make_rsrc(codes + block * k_tiles * kFp4Codes, (uint32_t)(there * k_tiles) * kFp4Codes),
+             make_rsrc(scales + block * k_tiles * kFp4Scales, (uint32_t)(there * k_tiles) * kFp4Scales)},
+            k_tiles};
+}
+
+// A wave's next tiles of RT row blocks, in flight. A tile past the last reads zeros.
 template <int RT>
 struct Ahead {
     u32x4 codes[RT];
@@ -36,9 +53,20 @@ struct Ahead {
     {
         const int lane = lane_id();
 #pragma unroll
-        for (int i = 0; i < RT; ++i) {  // a tile past the last reads zeros
+        for (int i = 0; i < RT; ++i) {
             codes[i] = __builtin_amdgcn_raw_buffer_load_b128(w[i].codes, lane * 16, t * kFp4Codes, kCached ? 0 : kLoadAux);
             scales[i] = __builtin_amdgcn_raw_buffer_load_b32(w[i].scales, lane % 16 * 4, t * kFp4Scales, 0);
+        }
+    }
+    __device__ __forceinline__ void load(const TileRun &w, int t)
+    {
+        const int lane = lane_id();
+        const uint32_t at = t < w.k_tiles ? lane * 16 : kNowhere, scale_at = t < w.k_tiles ? lane % 16 * 4 : kNowhere;
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+            const int tile = i * w.k_tiles + t;
+            codes[i] = __builtin_amdgcn_raw_buffer_load_b128(w.first.codes, at, tile * kFp4Codes, kLoadAux);
+            scales[i] = __builtin_amdgcn_raw_buffer_load_b32(w.first.scales, scale_at, tile * kFp4Scales, 0);
         }
     }
 };
@@ -122,80 +150,122 @@ struct Stream {
     }
 };
 
-// acc[i][g] += 16 rows of W (w[i]) times 16 columns (group g) over all k, with the columns shared: W waves, each with rows of its own, walk k together. A
-// wave loads its part of the columns' next 128 k (load i of wave w takes columns 4 (w + i W) ..+4 of
-// them: col[i], the start of column lane / 16 of these plus 16 (lane % 16) bytes), and they meet in
-// shared memory: xs, two sets of G * 256 chunks of 16 bytes, used in turn, so that one barrier a step
-// is enough. even, odd: the first two steps' tiles, loaded by the caller.
-// groups: those of the G that have columns.
-template <int G, int W>
-constexpr int kOwnLoads = (4 * G + W - 1) / W;
+// acc[i][g] += 16 rows of W (w[i]) times 16 columns (group g) over all k, with the columns shared: W
+// waves, each with rows of its own, walk k together. A wave loads its part of the columns' next 128
+// k (load i of wave w takes columns 4 (w + i W) ..+4 of them: col[i], the start of column lane / 16
+// of these plus 16 (lane % 16) bytes), and they meet in shared memory: xs, two sets of G * 256
+// chunks of 16 bytes, used in turn, so that one barrier a step is enough. D steps of tiles and two of
+// columns, which come from cache, are in flight. W's blocks are a TileRun where CHAIN, and the walk
+// ends by sending for the first steps of the next one.
+template <int RT>
+struct TileSet {
+    Tiles block[RT];
+};
 
-template <int RT, int G, int W>
-__device__ __forceinline__ void walk_products(f32x4 (&acc)[RT][G], const Tiles (&w)[RT], Ahead<RT> &even, Ahead<RT> &odd,
-                                              rsrc_t x, const uint32_t (&col)[kOwnLoads<G, W>], int K, int groups, u32x4 *xs)
-{
-    constexpr int kLoads = kOwnLoads<G, W>;
-    struct Columns {
-        u32x4 v[kLoads];
+template <int RT>
+__device__ __forceinline__ void load_tiles(Ahead<RT> &to, const TileSet<RT> &w, int t) { to.load(w.block, t); }
+template <int RT>
+__device__ __forceinline__ void load_tiles(Ahead<RT> &to, const TileRun &w, int t) { to.load(w, t); }
+
+template <int RT, int G, int W, int D, bool CHAIN>
+struct Walk {
+    static_assert(D % 2 == 0, "the sets of columns go on in turn");
+    static constexpr int kLoads = (4 * G + W - 1) / W;  // a wave's loads of columns a step
+    struct Ends {
+        typename std::conditional<CHAIN, TileRun, TileSet<RT>>::type w;
+        uint32_t col[kLoads];
     };
-    const int lane = lane_id(), wave = wave_in_block(), k_tiles = (K + kFp4K - 1) / kFp4K;
-    const int i16 = lane % 16, q = lane / 16;
-    auto fetch = [&](Columns &c, int t) {
+    Ahead<RT> tiles[D];
+    u32x4 columns[2][kLoads];
+
+    __device__ __forceinline__ void start_tiles(const Ends &of)
+    {
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i)
-            c.v[i] = __builtin_amdgcn_raw_buffer_load_b128(x, t * kFp4K + i16 * 8 < K ? col[i] : kNowhere, t * kFp4K * 2, 0);
-    };
-    static_assert(W % 2 == 0, "the columns of a wave's loads have one c % 8");
-    const int put = put_at(4 * wave + q);                             // load i: 64 W i further
-    const int get = i16 * 16 + (q ^ i16 % 8), get_odd = get ^ 4;       // word j: 8 (j / 2) further
-    auto multiply = [&](const Ahead<RT> &tiles, const Columns &c, u32x4 *set) {
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i)
-            if (wave + i * W < 4 * groups)
-                set[put + i * W * 64] = c.v[i];
-        // Everyone's columns of this step are there after the barrier. Those of the next go into the
-        // other set, and into this one again only after the next barrier, which a wave reaches when
-        // its reads below have come.
-        sync_shared();
-        u32x4 b[2][G];  // the next word's columns are read beside a word's products
-        auto read = [&](int j) __attribute__((always_inline)) {
-#pragma unroll
-            for (int g = 0; g < G; ++g)
-                if (g == 0 || g < groups)
-                    b[j % 2][g] = set[(j % 2 ? get_odd : get) + j / 2 * 8 + g * 256];
-        };
-        read(0);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            if (j < 3)
-                read(j + 1);
-            u32x4 a[RT];
-#pragma unroll
-            for (int i = 0; i < RT; ++i)
-                a[i] = fp4_widen(tiles.codes[i][j], fp4_scale(tiles.scales[i], j));
-#pragma unroll
-            for (int g = 0; g < G; ++g)
-                if (g == 0 || g < groups)
-#pragma unroll
-                    for (int i = 0; i < RT; ++i)
-                        acc[i][g] = mfma16<DT_BF16>(a[i], b[j % 2][g], acc[i][g]);
-            __builtin_amdgcn_sched_barrier(0);
-        }
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    };
-    Columns c_even, c_odd;
-    fetch(c_even, 0);
-    fetch(c_odd, 1);
-    for (int t = 0; t < k_tiles; t += 2) {  // whole turns of two, so calls use the sets in turn too
-        multiply(even, c_even, xs);
-        even.load(w, t + 2);
-        fetch(c_even, t + 2);
-        multiply(odd, c_odd, xs + G * 256);
-        odd.load(w, t + 3);
-        fetch(c_odd, t + 3);
+        for (int d = 0; d < D; ++d)
+            load_tiles(tiles[d], of.w, d);
     }
-}
+
+    __device__ __forceinline__ void fetch(u32x4 (&to)[kLoads], rsrc_t x, const Ends &of, int K, int t)
+    {
+        const int k = t * kFp4K + lane_id() % 16 * 8;
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i)
+            to[i] = __builtin_amdgcn_raw_buffer_load_b128(x, k < K ? of.col[i] : kNowhere, t * kFp4K * 2, 0);
+    }
+
+    __device__ __forceinline__ void start_columns(rsrc_t x, const Ends &of, int K)
+    {
+        fetch(columns[0], x, of, K, 0);
+        fetch(columns[1], x, of, K, 1);
+    }
+
+    // groups: those of the G that have columns.
+    __device__ __forceinline__ void run(f32x4 (&acc)[RT][G], rsrc_t x, const Ends &of, const Ends &next, int K, int groups,
+                                        u32x4 *xs)
+    {
+        static_assert(W % 2 == 0, "the columns of a wave's loads have one c % 8");
+        const int lane = lane_id(), wave = wave_in_block(), k_tiles = (K + kFp4K - 1) / kFp4K;
+        const int i16 = lane % 16, q = lane / 16;
+        const int put = put_at(4 * wave + q);                         // load i: 64 W i further
+        const int get = i16 * 16 + (q ^ i16 % 8), get_odd = get ^ 4;  // word j: 8 (j / 2) further
+        auto multiply = [&](const Ahead<RT> &now, const u32x4 (&from)[kLoads], u32x4 *set) __attribute__((always_inline)) {
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i)
+                if (wave + i * W < 4 * groups)
+                    set[put + i * W * 64] = from[i];
+            // Everyone's columns of this step are there after the barrier. Those of the next go into the
+            // other set, and into this one again only after the next barrier, which a wave reaches when
+            // its reads below have come.
+            sync_shared();
+            // the next word's columns are read beside a word's products, where there are registers
+            constexpr int kAhead = G < 3 ? 1 : 0;
+            u32x4 b[kAhead + 1][G];
+            auto read = [&](int j) __attribute__((always_inline)) {
+#pragma unroll
+                for (int g = 0; g < G; ++g)
+                    if (g == 0 || g < groups)
+                        b[j % (kAhead + 1)][g] = set[(j % 2 ? get_odd : get) + j / 2 * 8 + g * 256];
+            };
+            if (kAhead)
+                read(0);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (j + kAhead < 4)
+                    read(j + kAhead);
+                u32x4 a[RT];
+#pragma unroll
+                for (int i = 0; i < RT; ++i)
+                    a[i] = fp4_widen(now.codes[i][j], fp4_scale(now.scales[i], j));
+#pragma unroll
+                for (int g = 0; g < G; ++g)
+                    if (g == 0 || g < groups)
+#pragma unroll
+                        for (int i = 0; i < RT; ++i)
+                            acc[i][g] = mfma16<DT_BF16>(a[i], b[j % (kAhead + 1)][g], acc[i][g]);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        };
+        const auto once = [&](int d, const Ends &tile_of, int tile, const Ends &column_of, int column)
+            __attribute__((always_inline)) {
+            multiply(tiles[d], columns[d % 2], xs + d % 2 * G * 256);
+            // loads come back in order: columns that are sent for behind later tiles would wait for those
+            fetch(columns[d % 2], x, column_of, K, column);
+            load_tiles(tiles[d], tile_of.w, tile);
+        };
+        int t = 0;
+        for (; t + (CHAIN ? D : 0) < k_tiles; t += D) {  // whole turns of D; past the last tile: zeros
+#pragma unroll
+            for (int d = 0; d < D; ++d)
+                once(d, of, t + d + D, of, t + d + 2);
+        }
+        if constexpr (CHAIN) {
+#pragma unroll
+            for (int d = 0; d < D; ++d)
+                once(d, next, d, d < D - 2 ? of : next, d < D - 2 ? t + d + 2 : d + 2 - D);
+        }
+    }
+};
 
 }  // namespace block
 
