@@ -87,15 +87,17 @@ def linear_act_fp4(x, codes, scales, y, *, bias=None, activation=None, residual=
     """``linear_act`` with the weight [n, k] in 4 bits: y = act(x @ weight.T + bias) + residual; x
     [m, k], bias [n], residual and y [m, n] bf16, products exact, sums and epilogue fp32, one
     rounding. n a multiple of 8, k of 32. Forward only."""
-    m, k = _rows(x, "x")
-    n = _rows(y, "y")[1]
+    xs, ys = _rows(x, "x"), _rows(y, "y")
+    (m, k), n = xs, ys[1]
     if activation not in ACTIVATIONS:
         raise ValueError(f"unknown activation {activation!r}")
     _forward_only("linear_act_fp4", x, bias, residual)
-    dev = x.get_device()
-    args = (_tensor(x, "x", _BF16, (m, k), dev), *_pair(codes, scales, "", (), n, k, dev),
-            _tensor(bias, "bias", _BF16, (n,), dev), _tensor(residual, "residual", _BF16, (m, n), dev),
-            _tensor(y, "y", _BF16, (m, n), dev), m, n, k, ACTIVATIONS[activation])
+    dev, out = x.get_device(), (m, n)
+    c, s = fp4_shapes(n, k)
+    args = (_tensor(x, "x", _BF16, xs, dev), _tensor(codes, "codes", _U8, c, dev), _tensor(scales, "scales", _U8, s, dev),
+            None if bias is None else _tensor(bias, "bias", _BF16, (n,), dev),
+            None if residual is None else _tensor(residual, "residual", _BF16, out, dev),
+            _tensor(y, "y", _BF16, out, dev), m, n, k, ACTIVATIONS[activation])
     _call("block_linear_act_fp4", x, stream, args, workspace, linear_act_fp4_workspace(m, n, k))
     return y
 
@@ -105,14 +107,19 @@ def moe_experts_fp4_workspace(tokens: int, hidden: int, inter: int, experts: int
     return _block.load_library().block_moe_experts_fp4_workspace(tokens, hidden, inter, experts, top_k)
 
 
+@_by_size
+def _expert_shapes(experts, ups, hidden, inter):
+    return tuple(tuple((experts, *shape) for shape in fp4_shapes(*size)) for size in ((ups, hidden), (hidden, inter)))
+
+
 def moe_experts_fp4(x, up_codes, up_scales, down_codes, down_scales, ids, probs, y, *, activation="swiglu",
                     limit=math.inf, residual=None, valid_tokens=None, workspace=None, stream=None):
     """``moe_experts`` with the experts' weights in 4 bits: up_* hold [experts, 2 inter, hidden]
     ("swiglu", gate rows first, clamped at ``limit``) or [experts, inter, hidden]
     ("squared_relu"), down_* [experts, hidden, inter]. hidden and inter are multiples of 32; inter is
     told by the rows of up_codes."""
-    tokens, hidden = _rows(x, "x")
-    top_k = _rows(ids, "ids")[1]
+    xs = tokens, hidden = _rows(x, "x")
+    chosen = (tokens, _rows(ids, "ids")[1])
     if activation not in EXPERT_ACTIVATIONS:
         raise ValueError(f"unknown expert activation {activation!r}")
     gated = activation == "swiglu"
@@ -123,14 +130,15 @@ def moe_experts_fp4(x, up_codes, up_scales, down_codes, down_scales, ids, probs,
     experts, blocks = up_codes.shape[:2]
     inter = blocks * 8 if gated else blocks * 16
     _forward_only("moe_experts_fp4", x, probs, residual)
-    dev, ykind = x.get_device(), _kind(y, "y", (_BF16, _F32))
-    args = (_tensor(x, "x", _BF16, (tokens, hidden), dev),
-            *_pair(up_codes, up_scales, "up_", (experts,), 2 * inter if gated else inter, hidden, dev),
-            *_pair(down_codes, down_scales, "down_", (experts,), hidden, inter, dev),
-            _tensor(ids, "ids", _I32, (tokens, top_k), dev), _tensor(probs, "probs", _F32, (tokens, top_k), dev),
-            _tensor(residual, "residual", _BF16, (tokens, hidden), dev), _tensor(y, "y", ykind, (tokens, hidden), dev),
+    dev, ykind, top_k = x.get_device(), _kind(y, "y", (_BF16, _F32)), chosen[1]
+    up, down = _expert_shapes(experts, 2 * inter if gated else inter, hidden, inter)
+    args = (_tensor(x, "x", _BF16, xs, dev), _tensor(up_codes, "up_codes", _U8, up[0], dev),
+            _tensor(up_scales, "up_scales", _U8, up[1], dev), _tensor(down_codes, "down_codes", _U8, down[0], dev),
+            _tensor(down_scales, "down_scales", _U8, down[1], dev), _tensor(ids, "ids", _I32, chosen, dev),
+            _tensor(probs, "probs", _F32, chosen, dev),
+            None if residual is None else _tensor(residual, "residual", _BF16, xs, dev), _tensor(y, "y", ykind, xs, dev),
             _TORCH[ykind], tokens, hidden, inter, experts, top_k, EXPERT_ACTIVATIONS[activation], limit,
-            _scalar(valid_tokens, dev))
+            None if valid_tokens is None else _scalar(valid_tokens, dev))
     _call("block_moe_experts_fp4", x, stream, args, workspace,
           moe_experts_fp4_workspace(tokens, hidden, inter, experts, top_k))
     return y

@@ -340,7 +340,7 @@ def _scores(scores):
 
 def _gate_rule(scores, groups, top_groups, group_top, renormalize, scale):
     """The gate's arguments as the C functions take them in a row."""
-    return (_scores(scores), groups, groups if top_groups is None else top_groups, group_top, bool(renormalize), scale)
+    return (SCORES[scores] if scores in SCORES else _scores(scores), groups, groups if top_groups is None else top_groups, group_top, bool(renormalize), scale)
 
 
 def moe_route(x, router_weight, ids, probs, *, renormalize=False, scores="softmax", bias=None, groups=1,
@@ -367,9 +367,9 @@ def moe_route(x, router_weight, ids, probs, *, renormalize=False, scores="softma
               workspace, need)
     else:
         _call("block_moe_route_gated", x, stream,
-              (px, pr, _TORCH[rkind], _tensor(bias, "bias", _F32, (experts,), dev), *to,
-               *_gate_rule(scores, groups, top_groups, group_top, renormalize, scale), _scalar(valid_tokens, dev)),
-              workspace, need)
+              (px, pr, _TORCH[rkind], None if bias is None else _tensor(bias, "bias", _F32, (experts,), dev), *to,
+               *_gate_rule(scores, groups, top_groups, group_top, renormalize, scale),
+               None if valid_tokens is None else _scalar(valid_tokens, dev)), workspace, need)
     return ids, probs
 
 

@@ -10,7 +10,18 @@ from __future__ import annotations
 import torch
 from torch.autograd.function import once_differentiable
 
-from .moe_block import (_ANY, _F32, _I32, _TORCH, _aligned, _call, _gate_rule, _kind, _rows, _scalar, _scores, _tensor)
+from .moe_block import (_ANY, _F32, _I32, _TORCH, SCORES, _aligned, _call, _gate_rule, _kind, _rows, _scalar, _scores,
+                        _tensor)
+
+
+def _logits(logits, ids):
+    """What both directions take from the logits, and the slots a token."""
+    shape, code, chosen = logits.shape, _TORCH.get(logits.dtype), ids.shape
+    if len(shape) != 2 or code is None or len(chosen) != 2 or not logits.is_contiguous():
+        _rows(logits, "logits")
+        _rows(ids, "ids")
+        _tensor(logits, "logits", _kind(logits, "logits", _ANY), shape, logits.get_device())
+    return logits.data_ptr(), code, *shape, chosen[1], logits.get_device()
 
 
 def moe_gate_fwd(logits, ids, probs, *, scores="softmax", bias=None, groups=1, top_groups=None, group_top=1,
@@ -26,14 +37,13 @@ def moe_gate_fwd(logits, ids, probs, *, scores="softmax", bias=None, groups=1, t
     to the lower expert. Rows at or past ``valid_tokens`` (device int32) are left as they were.
     Nothing is recorded for autograd: the gradient comes from ``moe_gate_bwd``, or from
     ``MoeGate``, which calls both."""
-    shape = tokens, experts = _rows(logits, "logits")
-    top_k = _rows(ids, "ids")[1]
-    dev, kind = logits.get_device(), _kind(logits, "logits", _ANY)
-    rule = _gate_rule(scores, groups, top_groups, group_top, renormalize, scale)
+    pl, code, tokens, experts, top_k, dev = _logits(logits, ids)
+    chosen = (tokens, top_k)
     _call("block_moe_gate_fwd", logits, stream,
-          (_tensor(logits, "logits", kind, shape, dev), _TORCH[kind], _tensor(bias, "bias", _F32, (experts,), dev),
-           _tensor(ids, "ids", _I32, (tokens, top_k), dev), _tensor(probs, "probs", _F32, (tokens, top_k), dev),
-           tokens, experts, top_k, *rule, _scalar(valid_tokens, dev)))
+          (pl, code, None if bias is None else _tensor(bias, "bias", _F32, (experts,), dev),
+           _tensor(ids, "ids", _I32, chosen, dev), _tensor(probs, "probs", _F32, chosen, dev), tokens, experts, top_k,
+           *_gate_rule(scores, groups, top_groups, group_top, renormalize, scale),
+           None if valid_tokens is None else _scalar(valid_tokens, dev)))
     return ids, probs
 
 
@@ -42,14 +52,13 @@ def moe_gate_bwd(logits, ids, grad_probs, grad_logits, *, scores="softmax", reno
     """``grad_logits`` (logits' dtype and shape, every element written) from ``grad_probs`` (fp32
     [tokens, top_k]) and the forward's ``logits`` and ``ids``; the choice itself and the bias
     have no gradient. Rows at or past ``valid_tokens`` are left as they were."""
-    shape = tokens, experts = _rows(logits, "logits")
-    top_k = _rows(ids, "ids")[1]
-    dev, kind = logits.get_device(), _kind(logits, "logits", _ANY)
+    pl, code, tokens, experts, top_k, dev = _logits(logits, ids)
+    chosen = (tokens, top_k)
     _call("block_moe_gate_bwd", logits, stream,
-          (_tensor(logits, "logits", kind, shape, dev), _TORCH[kind], _tensor(ids, "ids", _I32, (tokens, top_k), dev),
-           _tensor(grad_probs, "grad_probs", _F32, (tokens, top_k), dev),
-           _tensor(grad_logits, "grad_logits", kind, shape, dev), tokens, experts, top_k, _scores(scores),
-           bool(renormalize), scale, _scalar(valid_tokens, dev)))
+          (pl, code, _tensor(ids, "ids", _I32, chosen, dev), _tensor(grad_probs, "grad_probs", _F32, chosen, dev),
+           _tensor(grad_logits, "grad_logits", logits.dtype, logits.shape, dev), tokens, experts, top_k,
+           SCORES[scores] if scores in SCORES else _scores(scores), bool(renormalize), scale,
+           None if valid_tokens is None else _scalar(valid_tokens, dev)))
     return grad_logits
 
 
