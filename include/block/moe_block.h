@@ -175,7 +175,8 @@ block_status_t block_moe_layer(const uint16_t *x, const void *router_weight, blo
  * Scores, ranks and sums are formed in fp64, each weight is rounded once to fp32. Equal ranks go in
  * increasing index, NaN before any number. An expert whose logit is -inf is masked: its score is 0
  * and its rank -inf whatever its bias, so that it is chosen (with weight 0) only where too few
- * others are left; where the chosen scores are all 0, so are the weights.
+ * others are left; where the chosen scores are all 0, so are the weights. (Renormalised softmax
+ * weights are the softmax of the chosen logits, also far below the row's largest.)
  *   logits: [tokens, experts] of logits_dtype, any of block_dtype_t; bias: fp32 [experts] or NULL;
  *   ids: int32 [tokens, top_k]; probs: fp32 [tokens, top_k].
  *   valid_tokens: device int32 scalar or NULL (= tokens), clamped to 0 .. tokens; rows of ids and

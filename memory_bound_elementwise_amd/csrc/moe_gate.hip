@@ -358,6 +358,20 @@ __global__ __launch_bounds__(kWavesHere * 64) void gate_kernel(GateArgs a)
 #pragma unroll
         for (int q = 0; q < Q; ++q)
             p[q] = sum == 0.0 ? 0.0 : p[q] / sum;
+        // Chosen for their bias, hundreds below the largest logit: from the chosen logits alone, as in
+        // the gradient, where the scores run out of exponents (fp32 weights reach down to 2^-149).
+        if (r.scores == BLOCK_SCORES_SOFTMAX && __any(sum < 0x1p-840)) {
+            double x[Q], own[Q];
+#pragma unroll
+            for (int q = 0; q < Q; ++q) {
+                const double chosen = logit<SRC>(a.logits, row + id[q], part, a.parts);
+                x[q] = q * L + l < r.top_k ? chosen : -INFINITY;
+            }
+            softmax<L, Q>(x, own);
+#pragma unroll
+            for (int q = 0; q < Q; ++q)
+                p[q] = sum < 0x1p-840 ? own[q] : p[q];
+        }
     }
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
@@ -501,7 +515,12 @@ __global__ __launch_bounds__(kWavesHere * 64) void gate_grad_kernel(GateGradArgs
 // ---------------------------------------------------------------------------
 // Host
 // ---------------------------------------------------------------------------
-constexpr int kFewTokens = 1024;  // a wave each
+// Up to so many tokens take a wave each, more share one by two or, with up to 64 experts, by four: a
+// wave of its own has the shorter way to the answer, shared ones spend fewer instructions a
+// token. (us, own and shared: 1024 tokens of 64 experts 3.7 and 4.5, of 256 4.7 and 5.8; 2048 tokens
+// 4.0 and 4.5, 5.5 and 6.0; 4096 tokens 5.1 and 4.6, 7.7 and 7.3. The gradient's: 3.6 and 4.2, 4.3
+// and 5.1; 3.9 and 4.2, 5.0 and 5.4; 4.8 and 4.4, 6.4 and 6.4.)
+constexpr int kFewTokens = 2048;
 
 unsigned groups_of(int64_t tokens, int lanes) { return (unsigned)ceil_div(tokens, kWavesHere * (64 / lanes)); }
 

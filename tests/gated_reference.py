@@ -48,7 +48,10 @@ def gate(logits, top_k, scores, bias=None, groups=1, top_groups=None, group_top=
         p = s[order]
         if renormalize:
             total = float(p.sum())
-            p = torch.zeros_like(p) if total == 0 else p / total
+            if scores == "softmax" and total == total:
+                p = scores_of(row[order], scores)           # the same, but where s runs out of exponents
+            else:
+                p = torch.zeros_like(p) if total == 0 else p / total
         ids.append(torch.tensor(order, dtype=torch.int32))
         probs.append(p * scale)
     ids = torch.stack(ids) if ids else torch.empty(0, top_k, dtype=torch.int32)

@@ -57,14 +57,14 @@ def test_sizes(tokens, experts, top_k):
 @pytest.mark.parametrize("experts,top_k", [(7, 7), (64, 8), (160, 6), (256, 20), (300, 3)])
 def test_many_tokens(experts, top_k):
     """More tokens than waves of a token each, and no multiple of a workgroup's."""
-    say(f"[gate] 1031 tokens, {experts} experts, top {top_k}")
-    _check(_logits(1031, experts), top_k, "sigmoid", _bias(experts), renormalize=True)
-    _check(_logits(1031, experts, "bf16"), top_k, "softmax")
+    say(f"[gate] 2055 tokens, {experts} experts, top {top_k}")
+    _check(_logits(2055, experts), top_k, "sigmoid", _bias(experts), renormalize=True)
+    _check(_logits(2055, experts, "bf16"), top_k, "softmax")
 
 
 @pytest.mark.parametrize("groups,size,top_groups", [(2, 2, 1), (8, 32, 4), (8, 20, 3), (4, 15, 4), (64, 16, 5), (64, 1, 9),
                                                    (3, 21, 2), (16, 4, 16)])
-@pytest.mark.parametrize("tokens", [1, 37, 1030])
+@pytest.mark.parametrize("tokens", [1, 37, 2054])
 def test_groups(tokens, groups, size, top_groups):
     experts = groups * size
     say(f"[gate] {tokens} tokens, {groups} groups of {size}, top {top_groups}")
@@ -80,7 +80,7 @@ def test_groups(tokens, groups, size, top_groups):
                        group_top=group_top, renormalize=scores == "sigmoid", scale=1.5)
 
 
-@pytest.mark.parametrize("tokens", [4, 1100])
+@pytest.mark.parametrize("tokens", [4, 2124])
 def test_ties(tokens):
     """Equal ranks go to the lower expert, equal groups to the lower one; a bias decides between
     equal scores."""
@@ -101,11 +101,11 @@ def test_neighbouring_scores():
     logits = torch.tensor([[18.0, 18.000002, 17.999998, 18.000004], [20.0, 20.25, 20.5, 20.125]])
     _check(logits, 4, "sigmoid")
     _check(logits, 4, "sigmoid", torch.full((4,), 4096.0))
-    _check(torch.tensor([[0.0, 1e-8, -1e-8, 2e-8]]).repeat(1030, 1), 4, "softmax")
+    _check(torch.tensor([[0.0, 1e-8, -1e-8, 2e-8]]).repeat(2054, 1), 4, "softmax")
 
 
 @pytest.mark.parametrize("scores", ["softmax", "sigmoid"])
-@pytest.mark.parametrize("tokens", [8, 1040])
+@pytest.mark.parametrize("tokens", [8, 2064])
 def test_masked_experts(tokens, scores):
     """Logits of -inf: chosen last, with weight 0, whatever their bias; a row of them has weights 0."""
     for experts in (40, 128):
@@ -128,14 +128,30 @@ def test_masked_experts(tokens, scores):
     _check(lowest, 6, scores, renormalize=True)
 
 
+@pytest.mark.parametrize("tokens,experts", [(7, 24), (7, 200), (2074, 48), (2074, 200), (9, 900)])
+def test_chosen_far_below_the_largest(tokens, experts):
+    """A bias that keeps the largest logits out: the chosen ones' softmax is far from fp64's end, also
+    where their scores among all experts are past it; the gradient is that of these weights."""
+    logits = _logits(tokens, experts)
+    logits[::2, :4] += torch.tensor([600.0, 700.0, 900.0, 1e30])
+    logits[1::3, 3] += 650.0
+    bias = _bias(experts)
+    bias[:4] = -INF
+    ids, probs = _check(logits, 6, "softmax", bias, renormalize=True, scale=2.0)
+    assert (ids > 3).all() and (probs.sum(1) - 2).abs().max() < 1e-6
+    g = torch.randn(tokens, 6)
+    want, bound = gated.gate_grads(logits, ids, g, "softmax", True, 2.0, torch.float32)
+    ref.check(_grads(logits, ids, g, scores="softmax", renormalize=True, scale=2.0), want, bound, "grad_logits")
+
+
 @pytest.mark.parametrize("scores", ["softmax", "sigmoid"])
 def test_not_finite(scores):
     """NaN comes before any number, +inf is a number for the sigmoid; a token's NaN stays its own."""
-    logits = _logits(1030, 70)
+    logits = _logits(2054, 70)
     logits[1, 9] = NAN
     logits[3, 20] = INF
     logits[4] = NAN
-    for tokens in (6, 1030):
+    for tokens in (6, 2054):
         part = logits[:tokens]
         for how in (dict(), dict(renormalize=True), dict(groups=7, top_groups=2, group_top=2)):
             ids, probs = _check(part, 5, scores, **how)
@@ -152,7 +168,7 @@ def test_valid_tokens(valid):
     v = torch.tensor([valid], dtype=torch.int32, device=DEV)
     n = min(max(valid, 0), 20)
     logits = _logits(20, 48)
-    for reps in (1, 60):                                    # 1200 tokens: several a wave
+    for reps in (1, 110):                                   # 2200 tokens: several a wave
         part = logits.repeat(reps, 1)
         whole = _gate(part, 4, scores="sigmoid")
         ids, probs = _gate(part, 4, scores="sigmoid", valid_tokens=v)
@@ -225,7 +241,7 @@ def _grads(logits, ids, g, **how):
     return out
 
 
-@pytest.mark.parametrize("tokens", [1, 2, 5, 130, 1031])
+@pytest.mark.parametrize("tokens", [1, 2, 5, 130, 2055])
 @pytest.mark.parametrize("experts,top_k", [(1, 1), (5, 5), (60, 6), (64, 8), (65, 3), (256, 8), (257, 9), (1000, 64)])
 def test_gradient(tokens, experts, top_k):
     say(f"[gate_bwd] {tokens} tokens, {experts} experts, top {top_k}")
@@ -245,17 +261,17 @@ def test_gradient(tokens, experts, top_k):
 def test_gradient_of_odd_choices():
     """Ids outside the experts contribute nothing, a repeated one twice; masked experts and rows of
     them have zeros; far logits keep their digits."""
-    logits = _logits(1030, 40)
+    logits = _logits(2054, 40)
     logits[3] = -INF
     logits[4, 1:] = -INF
     logits[5] *= 200
     logits[6] -= 500
-    ids = torch.randint(-2, 43, (1030, 7), generator=torch.Generator().manual_seed(2), dtype=torch.int32)
+    ids = torch.randint(-2, 43, (2054, 7), generator=torch.Generator().manual_seed(2), dtype=torch.int32)
     ids[0], ids[1] = 11, -1
     ids[2, 3] = 2 ** 31 - 1
     ids[4] = torch.arange(7)
-    g = torch.randn(1030, 7, generator=torch.Generator().manual_seed(3))
-    for tokens in (8, 1030):
+    g = torch.randn(2054, 7, generator=torch.Generator().manual_seed(3))
+    for tokens in (8, 2054):
         for scores in ("softmax", "sigmoid"):
             for renorm in (False, True):
                 got = _grads(logits[:tokens], ids[:tokens], g[:tokens], scores=scores, renormalize=renorm)
@@ -318,6 +334,16 @@ def test_autograd():
     half = logits.to(torch.bfloat16).requires_grad_()
     MoeGate.apply(half, 2)[0].sum().backward()
     assert half.grad.dtype == torch.bfloat16
+    none = torch.empty(3, 0, 96, device=DEV, requires_grad=True)
+    probs, ids = MoeGate.apply(none, 2)
+    probs.sum().backward()
+    assert probs.shape == ids.shape == (3, 0, 2) and none.grad.shape == none.shape
+    one = logits[0].clone().requires_grad_()
+    probs, ids = MoeGate.apply(one, 2)
+    probs.backward(up[0].to(DEV))
+    assert probs.shape == ids.shape == (2,)
+    ref.check(one.grad[None], *gated.gate_grads(logits[:1].cpu(), ids[None].cpu(), up[:1], "softmax", False, 1.0,
+                                                torch.float32), "grad_logits")
 
 
 def test_captured_autograd_is_refused():
@@ -342,7 +368,7 @@ def test_captured_autograd_is_refused():
 # ---------------------------------------------------------------------------
 def test_same_bits_streams_and_capture():
     """Every replay of a captured run gives the eager bits, also while another stream runs the same."""
-    for tokens in (3, 1500):
+    for tokens in (3, 2500):
         logits, bias = _logits(tokens, 96).to(DEV), _bias(96).to(DEV)
         x = torch.randn(tokens, 256, device=DEV).to(torch.bfloat16)
         router = (torch.randn(96, 256, device=DEV) * 0.1).to(torch.bfloat16)
