@@ -643,7 +643,7 @@ template <int ACT>
 block_status_t launch_up(const ExpertArgs &a, int groups, unsigned each, hipStream_t st)
 {
     constexpr int kCols = ACT == ACT_SWIGLU ? 16 : 32;
-    if (shares_columns((int64_t)a.inter * 32 / kCols, each) && a.tokens > 2) {
+    if (shares_columns((int64_t)a.inter * 32 / kCols, each) && (a.tokens > 4 || a.tokens * a.top_k > kFewPairs)) {
         const dim3 grid((unsigned)ceil_div(a.inter, kManyWaves * kCols), each), threads(kManyWaves * 64);
         if (groups == 1)
             return launch(fp4_up_many_kernel<ACT, 1>, grid, threads, 0, st, a);
