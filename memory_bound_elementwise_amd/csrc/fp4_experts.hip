@@ -338,20 +338,12 @@ __device__ __forceinline__ rsrc_t terms_of(const ExpertArgs &a)
 // shared memory and are added in slot order. NX 1: a pair at a time, 4: five.
 constexpr int kFewWaves = 8, kFewPairs = 64;
 
-template <int YDT>
-__device__ __forceinline__ void finish(const ExpertArgs &a, int64_t at, float v)
-{
-    if (a.residual)
-        v += load1<DT_BF16>(a.residual, at);
-    store1<YDT>(a.y, at, v);
-}
-
 template <int YDT, int NX>
 __global__ __launch_bounds__(kFewWaves * 64) void fp4_down_few_kernel(ExpertArgs a, int parts)
 {
     constexpr int kTogether = NX == 1 ? 1 : kPairs;
     __shared__ u32x4 stages[kFewWaves * NX * 64];
-    __shared__ f32x4 sums[kFewPairs * 4];  // [pair][part][16], pairs * parts up to kFewPairs
+    __shared__ f32x4 sums[kFewPairs * 4];  // [pair][part][16]
     __shared__ uint16_t lists[kFewWaves * 64];
     __shared__ int ids[kFewPairs];
     const int lane = lane_id(), wave = wave_in_block();
@@ -361,6 +353,17 @@ __global__ __launch_bounds__(kFewWaves * 64) void fp4_down_few_kernel(ExpertArgs
     uint16_t *list = lists + wave * 64;
     if (wave == 0)
         ids[lane] = id;
+    // The token that the thread adds up at the end and the next one, with their part of the residual
+    const int c = threadIdx.x % 16, first = threadIdx.x / 16;
+    constexpr int kTokensHere = kFewWaves * 4, kTurns = kFewPairs / kTokensHere;
+    float residual[kTurns] = {};
+    if (a.residual) {
+#pragma unroll
+        for (int i = 0; i < kTurns; ++i) {
+            const int t = first + i * kTokensHere;
+            residual[i] = load1<DT_BF16>(a.residual, (int64_t)(t < a.tokens ? t : 0) * a.hidden + blockIdx.x * 16 + c);
+        }
+    }
     for (int u = wave; u < pairs * parts; u += kFewWaves) {
         const int p = u / parts, part = u % parts, e = __builtin_amdgcn_readlane(id, p);
         if (e < 0 || (int)__builtin_ctzll(__ballot(id == e)) != p)
@@ -386,8 +389,11 @@ __global__ __launch_bounds__(kFewWaves * 64) void fp4_down_few_kernel(ExpertArgs
         }
     }
     __syncthreads();
-    const int c = threadIdx.x % 16;
-    for (int t = threadIdx.x / 16; t < live; t += kFewWaves * 4) {
+#pragma unroll
+    for (int turn = 0; turn < kTurns; ++turn) {
+        const int t = first + turn * kTokensHere;
+        if (t >= live)
+            return;
         float v = 0.0f;
         for (int j = 0; j < a.top_k; ++j) {
             const int p = t * a.top_k + j;
@@ -396,7 +402,7 @@ __global__ __launch_bounds__(kFewWaves * 64) void fp4_down_few_kernel(ExpertArgs
             for (int i = 0; i < parts; ++i)
                 v += sums[(p * parts + i) * 4 + c / 4][c % 4];
         }
-        finish<YDT>(a, (int64_t)t * a.hidden + blockIdx.x * 16 + c, v);
+        store1<YDT>(a.y, (int64_t)t * a.hidden + blockIdx.x * 16 + c, v + residual[turn]);
     }
 }
 
@@ -569,10 +575,11 @@ __global__ __launch_bounds__(kDownWaves * 64, 4) void fp4_down_many_kernel(Exper
 template <int YDT>
 __global__ __launch_bounds__(256) void fp4_combine_kernel(ExpertArgs a)
 {
-    const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
-    if (i >= (int64_t)live_tokens(a.valid, a.tokens) * a.hidden)
+    const int i = (blockIdx.x * 256 + threadIdx.x) * 4;  // up to 2^26
+    if (i >= live_tokens(a.valid, a.tokens) * a.hidden)
         return;
-    const int t = (int)(i / a.hidden), c = (int)(i % a.hidden);
+    const int t = i / a.hidden, c = i % a.hidden;
+    const u32x2 residual = a.residual ? *reinterpret_cast<const u32x2 *>(a.residual + i) : u32x2{0, 0};
     f32x4 v = {0, 0, 0, 0};
     constexpr int kTogether = 8;  // loads that go out together
     for (int j0 = 0; j0 < a.top_k; j0 += kTogether) {
@@ -589,9 +596,12 @@ __global__ __launch_bounds__(256) void fp4_combine_kernel(ExpertArgs a)
             if (in[j])
                 v += z[j];
     }
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-        finish<YDT>(a, i + q, v[q]);
+    if (a.residual)
+        v += f32x4{bf16_lo(residual[0]), bf16_hi(residual[0]), bf16_lo(residual[1]), bf16_hi(residual[1])};
+    if constexpr (YDT == DT_F32)
+        *reinterpret_cast<f32x4 *>(reinterpret_cast<float *>(a.y) + i) = v;
+    else
+        *reinterpret_cast<u32x2 *>(reinterpret_cast<uint16_t *>(a.y) + i) = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
 }
 
 // ---------------------------------------------------------------------------
@@ -658,12 +668,12 @@ block_status_t launch_up(const ExpertArgs &a, int groups, unsigned each, hipStre
                          : launch(fp4_up_kernel<ACT, 4, true>, grid, threads, 0, st, a);
 }
 
-// Parts of k of the down product of few pairs: enough that all waves of a workgroup have work.
+// Parts of k of the down product of few pairs: as many as still leave a wave one turn.
 int few_parts(const ExpertArgs &a)
 {
     const int pairs = a.tokens * a.top_k;
     int parts = 1;
-    while (pairs * parts * 2 <= kFewPairs && pairs * parts < kFewWaves && parts * 2 * kFp4K <= a.inter)
+    while (pairs * parts * 2 <= kFewWaves && parts * 2 * kFp4K <= a.inter)
         parts *= 2;
     return parts;
 }
