@@ -21,7 +21,10 @@ struct Args : LinearArgs {
 // ---------------------------------------------------------------------------
 // Up to 16 rows of x: the cost is reading W once. A workgroup takes 16 rows of W, its waves split k,
 // and their sums meet in shared memory. 16 waves, so that 7168 x 4096, a workgroup a CU, has all
-// its loads in flight at once.
+// its loads in flight at once: one row 5.5 us for 15.6 MB, which is mostly the start and the end of
+// that one round. (us, this and tiles with their joining kernel, 7168 x 4096: 8 rows 7.5 and 7.8 + 3.7,
+// 16 rows 8.6 and 9.1 + 3.8.) Up to four rows are one load a step and leave room for four steps in
+// flight, more are four (4 rows 6.9 and 8.2 us, 2 rows 6.2 and 10.2).
 constexpr int kWaves = 16;
 
 template <int NX, int D>
@@ -66,8 +69,10 @@ __global__ __launch_bounds__(kWaves * 64) void fp4_linear_few_kernel(Args a)
 // read). W needs no shared memory: each wave has 16 FN rows of it for itself, loads their tiles a
 // step ahead and widens a word of each when its turn comes. What is read from shared memory is so
 // 1 / FN of an operand a matrix instruction. (Three buffers and loads two steps ahead leave room
-// for fewer workgroups: 1009 x 1408 x 7168 26.6 -> 29.5 us, 6720 x 7168 x 4096 323 -> 371. Tiles of
-// 128 x 256, a wave a SIMD: 33.8 and 340.) Weights come from cache for all tiles but the first.
+// for fewer workgroups: 1009 x 1408 x 7168 26.6 -> 29.5 us, 6720 x 4096 x 7168 323 -> 371. Tiles of
+// 128 x 256, a wave a SIMD: 33.8 and 340. Two waves a workgroup: 27.4 and 470.) Weights come from cache
+// for all tiles but the first. 6720 x 4096 x 7168 takes 298 us, 1.32 PFLOP/s; the 896 tiles of 1009 x
+// 1408 x 7168 23.5, 0.87, of 11 steps each and no whole number a CU.
 //   parts > 1: the sums over one of `parts` ranges of k, to partial [parts][m][n] in fp32.
 constexpr int kTileWaves = 4;
 
@@ -240,13 +245,21 @@ struct Plan {
 
 int64_t tile_count(int64_t m, int64_t n, const Plan &p) { return ceil_div(m, 16 * p.fm) * ceil_div(n, 64 * p.fn); }
 
-// The largest tile that leaves work for most of the 256 CUs; the smallest ones that are still too few
-// for two workgroups a CU share their k.
+// The largest tile that leaves work for all of the 256 CUs. (us, with the time of the joining kernel, of
+// 64 x 256 and 64 x 128: 1009 x 4096 x 7168, 448 of the larger tiles, 55.9 and 56.1; 1536 rows, 672
+// tiles, 77 and 85; 6720 rows 298 and 321. Of 64 x 128 and 32 x 128: 128 x 7168 x 4096, 64 of the
+// larger tiles, 19.0 + 4.0 and 16.4 + 4.0; 256 x 1408 x 7168, 224 tiles, 16.0 + 4.1 and 11.0; 512 x 1408 x
+// 7168, 448 tiles, 15.2 and 15.8; 1009 x 7168 x 4096, 512 tiles, 56.4 and 61.5; 17 rows fill half of
+// a tile of 64: 10.3 and 9.0.) The smaller ones share their k where they are too few for two
+// workgroups a CU (64 x 7168 x 4096 in one part 42.7, in eight 13.4 + 4.0).
 Plan plan(int64_t m, int64_t n, int64_t k)
 {
     Plan p = {4, 4, 1};
-    if (tile_count(m, n, p) < 512)
-        p = {m <= 32 ? 2 : 4, 2, 1};
+    if (tile_count(m, n, p) < 512) {
+        p = {4, 2, 1};
+        if (m <= 32 || tile_count(m, n, p) < 256)
+            p.fm = 2;
+    }
     const int64_t steps = ceil_div(k, kFp4K), tiles = tile_count(m, n, p);
     while (p.fn == 2 && p.parts < 16 && tiles * p.parts * 2 <= 512 && p.parts * 8 <= steps)
         p.parts *= 2;
