@@ -1,7 +1,10 @@
 // The expert layer of a few tokens with weights in 4 bits (layout in fp4.h), for AMD Instinct MI355X
 // (gfx950). C ABI declared in block/moe_block.h.
 //
-// For a few tokens the cost is reading each chosen expert's weights once.
+// y = residual + sum over a token's slots of down (act(up x) p), sums fp32. For a few tokens the cost is
+// reading each chosen expert's weights once: 187 MB for one token of 8 of 64 experts, hidden 7168, inter
+// 2048 (up 21.3 us, 5.9 TB/s; down 15.9, 3.9 TB/s), 1.5 GB for 64 tokens (160, 6.2 TB/s; 107, 4.7;
+// combine 5.4).
 //   up       one workgroup a (chosen expert, block of columns of the activation); the activation
 //            times the probability goes to the workspace as three bf16 terms, which keep its 24 bits
 //   down     the terms are columns of their own. For up to 64 pairs one workgroup 16 columns of
@@ -143,7 +146,9 @@ __device__ __forceinline__ int few_ids(const ExpertArgs &a, int pairs)
 }
 
 // FEW: up to 64 pairs. Up to 4 NX tokens of an expert share one read of its weights; an expert with
-// more reads them again.
+// more reads them again. What one token costs beyond its weights is one chain of loads: ids, then
+// (tiles are sent for before the pairs are looked through) tiles and x. (Eight waves a workgroup 24.2
+// us, four steps in flight 22.2, seven 22.7, for 21.4.)
 template <int ACT, int NX, bool FEW>
 __global__ __launch_bounds__(kWaves * 64) void fp4_up_kernel(ExpertArgs a)
 {
@@ -223,8 +228,10 @@ __global__ __launch_bounds__(kWaves * 64) void fp4_up_kernel(ExpertArgs a)
 }
 
 // Up products where experts have many tokens: a workgroup takes one expert and kManyWaves times two
-// row tiles, which walk k together (walk_products), so that x is read once for all of them. A
-// wave has gate and up of 16 columns of the activation, or 32 columns of one product.
+// row tiles, which walk k together (Walk), so that x is read once for all of them. A wave has gate
+// and up of 16 columns of the activation, or 32 columns of one product. Bound by the stream of weights:
+// 64 tokens, 7168 x 2048, 64 experts 160 us. (Four steps in flight 164; weights kept in the caches
+// 180; without the scales' loads 150.)
 constexpr int kManyWaves = 8;
 
 template <int G>
@@ -335,7 +342,9 @@ __device__ __forceinline__ rsrc_t terms_of(const ExpertArgs &a)
 
 // Down product of up to 64 pairs: a workgroup takes 16 columns of the output, its waves the chosen
 // experts in turn, each in `parts` parts of k so that all have work; the pairs' sums meet in
-// shared memory and are added in slot order. NX 1: a pair at a time, 4: five.
+// shared memory and are added in slot order. NX 1: a pair at a time, 4: five. One token's eight
+// experts are one round of 3.5 waves a SIMD, whose start and end are half of its 15.9 us. (Six or
+// eight steps in flight 17.3, sixteen waves a workgroup 18.2.)
 constexpr int kFewWaves = 8, kFewPairs = 64;
 
 template <int YDT, int NX>
@@ -407,7 +416,7 @@ __global__ __launch_bounds__(kFewWaves * 64) void fp4_down_few_kernel(ExpertArgs
 }
 
 // More pairs than that, and too few blocks for waves that share columns: up to five pairs of an
-// expert share one read of its weights.
+// expert share one read of its weights. (16 tokens, 512 x 256, 64 experts, top 8: 8.0 us.)
 __global__ __launch_bounds__(kWaves * 64) void fp4_down_kernel(ExpertArgs a)
 {
     constexpr int NX = 4;
@@ -450,10 +459,12 @@ __global__ __launch_bounds__(kWaves * 64) void fp4_down_kernel(ExpertArgs a)
 }
 
 // Down products where experts have many tokens: units of one expert, up to G * 5 of its pairs and
-// four waves of four row tiles (64 columns of the output) each. A workgroup takes every
-// gridDim.x-th unit, and its walk over one ends by sending for the next one's first steps: k is
-// short here (2048: 16 steps), and a workgroup a unit spent half of its time on its ends (7168 x
-// 2048, 64 tokens, 64 experts: 125 us).
+// eight waves of two row tiles (256 columns of the output). A workgroup takes every gridDim.x-th unit,
+// and its walk over one ends by sending for the next one's first steps: k is short here (2048: 16
+// steps). Its pairs' terms come from cache, 12 KB a pair and unit beside the unit's 278 KB of weights.
+// 64 tokens, 7168 x 2048, 64 experts: 107 us; a workgroup a unit 126; the weights' stream and the
+// stores of z alone 93. (Four waves of four tiles 115, four of two 158, sixteen of one 141, four steps
+// in flight 118.)
 constexpr int kDownWaves = 8, kDownTiles = 2;
 
 template <int G>
@@ -632,7 +643,8 @@ int64_t h_bytes(const ExpertSizes &s) { return round_up(s.tokens * s.top_k * s.i
 int64_t expert_bytes(const ExpertSizes &s) { return h_bytes(s) + s.tokens * s.top_k * s.hidden * 4; }
 
 // Groups of pairs that share a read of an expert's weights: enough for one and a half times the
-// pairs an expert has on average.
+// pairs an expert has on average. (Enough for the average, and for twice it: up, 128 tokens, 7168 x
+// 2048, 64 experts, top 8, 264 and 185 us for 185; down, 32 tokens, 113 and 99 for 101.)
 int pair_groups(const ExpertSizes &s, int group)
 {
     const int64_t some = ceil_div(3 * s.tokens * s.top_k, 2 * s.experts);
@@ -642,8 +654,9 @@ int pair_groups(const ExpertSizes &s, int group)
 
 // Whether the waves of a workgroup take rows of their own and share the columns: where that
 // still leaves a workgroup for every CU, and for more tokens than a few. (7168 x 2048, 8 of 64
-// experts, shared and split k: up, 2 tokens 43.9 and 39.7 us, 4 tokens 67.8 and 66.5, 8 tokens
-// 123.6 and 127.0; down, 2 tokens 25.2 and 6.4 for its combine against 38.2.)
+// experts, us, shared and split k: up, 2 tokens 43.9 and 39.7, 4 tokens 67.8 and 66.5, 8 tokens 123.6
+// and 127.0, 64 tokens 160 and 211; down, 2 tokens 29.1 + 4.6 for its combine and 38.2, 16 tokens 82
+// and 150, 64 tokens 107 and 331.)
 bool shares_columns(int64_t rows_of_w, unsigned experts)
 {
     return ceil_div(rows_of_w, kManyWaves * 32) * experts >= 256;
@@ -668,7 +681,8 @@ block_status_t launch_up(const ExpertArgs &a, int groups, unsigned each, hipStre
                          : launch(fp4_up_kernel<ACT, 4, true>, grid, threads, 0, st, a);
 }
 
-// Parts of k of the down product of few pairs: as many as still leave a wave one turn.
+// Parts of k of the down product of few pairs: as many as still leave a wave one turn. (One token, two
+// experts, 4096 x 8192: 17.3 us in one part, 9.2 in four.)
 int few_parts(const ExpertArgs &a)
 {
     const int pairs = a.tokens * a.top_k;

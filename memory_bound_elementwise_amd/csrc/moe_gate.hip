@@ -5,6 +5,13 @@
 // wave holds 64 / L tokens. Scores are formed in fp64, as the choice is made between neighbouring
 // values; what has to be seen by other lanes goes through the wave's own shared memory, and no
 // kernel here has a barrier.
+//
+// Few tokens take 2.7 to 7 us, a launch and a chain of exchanges. Many are bound by vector
+// instructions, not by memory: with 256 experts in 8 groups of which 4 are kept, top 8, a wave of two
+// tokens issues 1400 of them, and 6720 tokens (13.8 us for 6.9 MB) leave some of the 1024 SIMDs four
+// waves and others three. (Sixteen lanes a token 13.9 us, a wave each 14.6; the same choice in fp32
+// where its gaps certify it 1196 instructions and 13.8; the winner's index found in the scalar unit
+// 14.0.)
 #include <hip/hip_runtime.h>
 
 #include <stdint.h>
@@ -397,7 +404,8 @@ struct GateGradArgs {
 //     renormalised: p_j = s_j / sum s, v_j = p_j (g_j - sum g p), otherwise v_j = g_j s_j;
 //     sigmoid: v_j (1 - s_j) goes to expert ids_j. softmax: v_j does, and without
 //     renormalisation (DENSE) every expert loses s sum v.
-// Only DENSE reads logits that were not chosen.
+// Only DENSE reads logits that were not chosen. The gradient is a stream of stores: 6720 x 256 fp32
+// 6.2 us for 6.9 MB, of which a launch and the chain ids, logits, stores take most.
 template <int DT, int L, int V, bool DENSE>
 __global__ __launch_bounds__(kWavesHere * 64) void gate_grad_kernel(GateGradArgs a)
 {
