@@ -6,12 +6,12 @@
 // values; what has to be seen by other lanes goes through the wave's own shared memory, and no
 // kernel here has a barrier.
 //
-// Few tokens take 2.7 to 7 us, a launch and a chain of exchanges. Many are bound by vector
-// instructions, not by memory: with 256 experts in 8 groups of which 4 are kept, top 8, a wave of two
-// tokens issues 1400 of them, and 6720 tokens (13.8 us for 6.9 MB) leave some of the 1024 SIMDs four
-// waves and others three. (Sixteen lanes a token 13.9 us, a wave each 14.6; the same choice in fp32
-// where its gaps certify it 1196 instructions and 13.8; the winner's index found in the scalar unit
-// 14.0.)
+// Few tokens take 2.7 to 6 us: a launch, a chain of exchanges for groups (1.3) and one for each slot
+// (0.15). Many are bound by vector instructions, not by memory: with 256 experts in 8 groups of which 4
+// are kept, top 8, a wave of two tokens issues 1400 of them, and 6720 tokens (13.8 us for 6.9 MB) leave
+// some of the 1024 SIMDs four waves and others three. (Sixteen lanes a token 13.9 us, a wave each
+// 14.6; the same choice in fp32 where its gaps certify it 1196 instructions and 13.8; the winner's
+// index found in the scalar unit 14.0.)
 #include <hip/hip_runtime.h>
 
 #include <stdint.h>
@@ -140,13 +140,37 @@ __device__ __forceinline__ double sigmoid(double v)
     return v < 0.0 ? e * q : q;
 }
 
-template <int SRC>
-__device__ __forceinline__ double logit(const void *logits, int64_t at, int64_t part, int parts)
+// The logits at row + at[i]. Loads go out together, of partial sums those of several parts (a
+// logit after the other, one token's 256 of seven parts took 1.4 us more); the parts are added in
+// order.
+template <int SRC, int N>
+__device__ __forceinline__ void logits_at(const GateArgs &a, int64_t row, const int (&at)[N], double (&v)[N])
 {
-    if constexpr (SRC == SRC_PARTS)
-        return sum_parts(static_cast<const double *>(logits) + at, part, parts);
-    else
-        return (double)load1<SRC>(logits, at);
+    if constexpr (SRC == SRC_PARTS) {
+        constexpr int kTogether = N > 8 ? 2 : (N > 4 ? 4 : 8);
+        const double *from = static_cast<const double *>(a.logits) + row;
+        const int64_t part = (int64_t)a.tokens * a.experts;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            v[i] = 0.0;
+        for (int s = 0; s < a.parts; s += kTogether) {
+            double p[kTogether][N];
+#pragma unroll
+            for (int j = 0; j < kTogether; ++j)
+#pragma unroll
+                for (int i = 0; i < N; ++i)
+                    p[j][i] = from[(s + j < a.parts ? s + j : 0) * part + at[i]];
+#pragma unroll
+            for (int j = 0; j < kTogether; ++j)
+#pragma unroll
+                for (int i = 0; i < N; ++i)
+                    v[i] += s + j < a.parts ? p[j][i] : 0.0;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            v[i] = (double)load1<SRC>(a.logits, row + at[i]);
+    }
 }
 
 // s = softmax(v) over a token's lanes; all zeros where every logit is -inf.
@@ -175,7 +199,6 @@ __device__ __forceinline__ void softmax(const double (&v)[V], double (&s)[V])
 struct Room {
     uint64_t *table;  // an entry an expert
     uint64_t *worth;  // an entry a group
-    int *kept;        // which groups are kept
 };
 
 // Lanes of a token that look through one group together: a power of two.
@@ -243,20 +266,22 @@ __device__ __forceinline__ void choose(const GateRule &r, int experts, int l, co
                 room.worth[g] = order_key(r.group_top == 2 ? w + of_key(second_key) : w);
         }
         wave_fence();
-        for (int g = l; g < r.groups; g += L) {
+        uint64_t kept = 0;  // a bit a group
+        for (int g0 = 0; g0 < r.groups; g0 += L) {
+            const int g = g0 + l < r.groups ? g0 + l : 0;
             const uint64_t own = room.worth[g];
             int before = 0;
 #pragma unroll 8
             for (int o = 0; o < r.groups; ++o)
                 before += room.worth[o] > own || (room.worth[o] == own && o < g);
-            room.kept[g] = before < r.top_groups;
+            const uint64_t lanes = __ballot(g0 + l < r.groups && before < r.top_groups) >> (lane_id() & (64 - L));
+            kept |= (L == 64 ? lanes : lanes & (((uint64_t)1 << (L & 63)) - 1)) << g0;
         }
-        wave_fence();
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const unsigned e = i * L + l;
-            if ((int)e < experts && !room.kept[e * inverse >> 20])
-                key[i] = 0;
+            const unsigned e = i * L + l, g = e * inverse >> 20;
+            const unsigned word = g < 32 ? (unsigned)kept : (unsigned)(kept >> 32);
+            key[i] = word >> g % 32 & 1 ? key[i] : 0;  // experts past the last one have 0 already
         }
         wave_fence();
     }
@@ -318,7 +343,6 @@ __global__ __launch_bounds__(kWavesHere * 64) void gate_kernel(GateArgs a)
     constexpr int T = 64 / L;
     __shared__ uint64_t tables[kWavesHere][T][L * V];
     __shared__ uint64_t worths[kWavesHere][T][kGateGroups];
-    __shared__ int kept_groups[kWavesHere][T][kGateGroups];
     const GateRule r = a.rule;
     const int lane = lane_id(), wave = wave_in_block(), l = lane % L, tl = lane / L;
     const int first = ((int)blockIdx.x * kWavesHere + wave) * T, live = live_tokens(a.valid, a.tokens);
@@ -327,34 +351,33 @@ __global__ __launch_bounds__(kWavesHere * 64) void gate_kernel(GateArgs a)
     const bool mine = first + tl < live;
     const int t = mine ? first + tl : first;  // past the last token: the first one again, not stored
     uint64_t *table = tables[wave][tl], *worth = worths[wave][tl];
-    int *kept = kept_groups[wave][tl];
-    const int64_t row = (int64_t)t * a.experts, part = (int64_t)a.tokens * a.experts;
+    const int64_t row = (int64_t)t * a.experts;
 
     // Loads without branches, past the last expert of the first one again: all of them are on their way
     // together, and what follows is no chain of branches either. (With a condition around each
     // load, 6720 x 256 took 14.7 us.)
-    double v[V];
-    float bias[V];
+    int at[V];
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const int e = i * L + l < a.experts ? i * L + l : 0;
-        v[i] = logit<SRC>(a.logits, row + e, part, a.parts);
-    }
+    for (int i = 0; i < V; ++i)
+        at[i] = i * L + l < a.experts ? i * L + l : 0;
+    float bias[V];
 #pragma unroll
     for (int i = 0; i < V; ++i)
         bias[i] = 0.0f;
     if (a.bias) {
 #pragma unroll
         for (int i = 0; i < V; ++i)
-            bias[i] = a.bias[i * L + l < a.experts ? i * L + l : 0];
+            bias[i] = a.bias[at[i]];
     }
+    double v[V];
+    logits_at<SRC, V>(a, row, at, v);
 #pragma unroll
     for (int i = 0; i < V; ++i)
         v[i] = i * L + l < a.experts ? v[i] : -INFINITY;
     constexpr int Q = kGateSlots / L;
     int id[Q];  // lane l has slots l, L + l, ...
     double p[Q];
-    const Room room = {table, worth, kept};
+    const Room room = {table, worth};
     choose<L, V, Q>(r, a.experts, l, v, bias, room, id, p);
     double sum = 0.0;
 #pragma unroll
@@ -369,11 +392,10 @@ __global__ __launch_bounds__(kWavesHere * 64) void gate_kernel(GateArgs a)
         // the gradient, where the scores run out of exponents (fp32 weights reach down to 2^-149).
         if (r.scores == BLOCK_SCORES_SOFTMAX && __any(sum < 0x1p-840)) {
             double x[Q], own[Q];
+            logits_at<SRC, Q>(a, row, id, x);
 #pragma unroll
-            for (int q = 0; q < Q; ++q) {
-                const double chosen = logit<SRC>(a.logits, row + id[q], part, a.parts);
-                x[q] = q * L + l < r.top_k ? chosen : -INFINITY;
-            }
+            for (int q = 0; q < Q; ++q)
+                x[q] = q * L + l < r.top_k ? x[q] : -INFINITY;
             softmax<L, Q>(x, own);
 #pragma unroll
             for (int q = 0; q < Q; ++q)
