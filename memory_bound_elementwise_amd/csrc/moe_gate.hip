@@ -141,7 +141,7 @@ __device__ __forceinline__ double sigmoid(double v)
 }
 
 // The logits at row + at[i]. Loads go out together, of partial sums those of several parts (a
-// logit after the other, one token's 256 of seven parts took 1.4 us more); the parts are added in
+// logit after the other, one token's 256 took 1.2 us more); the parts are added in
 // order.
 template <int SRC, int N>
 __device__ __forceinline__ void logits_at(const GateArgs &a, int64_t row, const int (&at)[N], double (&v)[N])
