@@ -251,7 +251,9 @@ int64_t tile_count(int64_t m, int64_t n, const Plan &p) { return ceil_div(m, 16 
 // larger tiles, 19.0 + 4.0 and 16.4 + 4.0; 256 x 1408 x 7168, 224 tiles, 16.0 + 4.1 and 11.0; 512 x 1408 x
 // 7168, 448 tiles, 15.2 and 15.8; 1009 x 7168 x 4096, 512 tiles, 56.4 and 61.5; 17 rows fill half of
 // a tile of 64: 10.3 and 9.0.) The smaller ones share their k where they are too few for two
-// workgroups a CU (64 x 7168 x 4096 in one part 42.7, in eight 13.4 + 4.0).
+// workgroups a CU and k is long, as the joining kernel is a launch more. (Wall time a call in one part
+// and in two, 64 x 2048 x 4096 9.5 and 12.4, 64 x 1408 x 7168 8.0 and 12.8; 64 x 7168 x 2048 18.4 and 12.9,
+// in eight 12.3. Kernels alone, 17 x 7168 x 4096: 12.3 + 4.0 in four, 9.0 + 4.0 in eight.)
 Plan plan(int64_t m, int64_t n, int64_t k)
 {
     Plan p = {4, 4, 1};
@@ -261,7 +263,7 @@ Plan plan(int64_t m, int64_t n, int64_t k)
             p.fm = 2;
     }
     const int64_t steps = ceil_div(k, kFp4K), tiles = tile_count(m, n, p);
-    while (p.fn == 2 && p.parts < 16 && tiles * p.parts * 2 <= 512 && p.parts * 8 <= steps)
+    while (p.fn == 2 && steps >= 24 && p.parts < 16 && tiles * p.parts * 2 <= 512 && p.parts * 8 <= steps)
         p.parts *= 2;
     return p;
 }
