@@ -19,12 +19,11 @@ struct Args : LinearArgs {
 // ---------------------------------------------------------------------------
 // Few rows
 // ---------------------------------------------------------------------------
-// Up to 16 rows of x: the cost is reading W once. A workgroup takes 16 rows of W, its waves split k,
-// and their sums meet in shared memory. 16 waves, so that 7168 x 4096, a workgroup a CU, has all
-// its loads in flight at once: one row 5.5 us for 15.6 MB, which is mostly the start and the end of
-// that one round. (us, this and tiles with their joining kernel, 7168 x 4096: 8 rows 7.5 and 7.8 + 3.7,
-// 16 rows 8.6 and 9.1 + 3.8.) Up to four rows are one load a step and leave room for four steps in
-// flight, more are four (4 rows 6.9 and 8.2 us, 2 rows 6.2 and 10.2).
+// Up to 16 rows of x and W not too wide (few_rows below): the cost is reading W once. A workgroup
+// takes 16 rows of W, its waves split k, and their sums meet in shared memory. 16 waves, so that 7168 x
+// 4096, a workgroup a CU, has all its loads in flight at once: one row 5.5 us for 15.6 MB, which is
+// mostly the start and the end of that one round. Up to four rows are one load a step and leave room
+// for four steps in flight, more are four (4 rows 6.9 and 8.2 us, 2 rows 6.2 and 10.2).
 constexpr int kWaves = 16;
 
 template <int NX, int D>
@@ -229,7 +228,12 @@ __global__ __launch_bounds__(kTileWaves * 64, FN == 4 ? 3 : 4) void fp4_linear_t
 // ---------------------------------------------------------------------------
 // Host
 // ---------------------------------------------------------------------------
-constexpr int kFewRows = 16;
+// Whether a workgroup takes 16 rows of W (the first kernel) or a tile: up to 16 rows of x, and W no wider
+// than two such workgroups a CU, or four where a step is one load (its lines of 16 waves cost more to
+// start than they read). (us, this and tiles: 16 rows, 2048 x 4096 5.6 and 9.8, 2048 x 16384 13.9 and
+// 12.1, 7168 x 16384 24.4 and 14.5 + 3.8, 2048 x 65536 48 and 15.6; one row, 7168 x 16384 15.2 and 13.6 +
+// 3.8, 4096 x 32768 24.2 and 14.9 + 3.8.)
+bool few_rows(int64_t m, int64_t n) { return m <= 16 && n <= (m <= 4 ? 16384 : 8192); }
 
 bool good_sizes(int64_t m, int64_t n, int64_t k)
 {
@@ -295,7 +299,7 @@ extern "C" {
 
 int64_t block_linear_act_fp4_workspace(int64_t m, int64_t n, int64_t k)
 {
-    if (!good_sizes(m, n, k) || k % 32 || n % 8 || m <= kFewRows)
+    if (!good_sizes(m, n, k) || k % 32 || n % 8 || few_rows(m, n))
         return 0;
     const Plan p = plan(m, n, k);
     return p.parts > 1 ? p.parts * m * n * 4 : 0;
@@ -322,7 +326,7 @@ block_status_t block_linear_act_fp4(const uint16_t *x, const uint8_t *codes, con
                           {{x, m * k * 2}, {codes, s.codes()}, {scales, s.scales()}, {bias, n * 2}, {residual, m * n * 2}}))
         return BLOCK_ERR_INVALID_ARG;
     const Args a = {{x, nullptr, bias, residual, y, (int)m, (int)n, (int)k, act}, codes, scales};
-    if (m > kFewRows)
+    if (!few_rows(m, n))
         return run_many(a, static_cast<float *>(workspace), stream);
     const dim3 grid((unsigned)s.row_tiles()), threads(kWaves * 64);
     return m <= 4 ? launch(fp4_linear_few_kernel<1, 4>, grid, threads, 0, stream, a)

@@ -155,13 +155,13 @@ def test_linear_refusals():
     for bad in (dict(n=12), dict(k=40), dict(x=A + 2), dict(codes=at(1) + 8), dict(scales=at(2) + 4), dict(b=at(3) + 2),
                 dict(r=at(4) + 4), dict(y=at(5) + 2)):
         assert linear(**bad) == ALIGN, bad
-    for m, n, k in ((17, 4096, 7168), (100, 64, 7168), (40, 72, 1 << 20)):     # split sums
+    for m, n, k in ((17, 4096, 7168), (100, 64, 7168), (40, 72, 1 << 20), (16, 16384, 7168), (1, 16392, 7168)):  # split sums
         need = mbe.linear_act_fp4_workspace(m, n, k)
         assert need > 0 and need % (2 * m * n * 4) == 0
         assert linear(m=m, n=n, k=k, size=need - 1) == linear(m=m, n=n, k=k, ws=None) == INVALID
         assert linear(m=m, n=n, k=k, ws=at(1)) == linear(m=m, n=n, k=k, ws=at(2)) == INVALID
         assert linear(m=m, n=n, k=k, ws=at(6) + 4) == ALIGN
-    for m, n, k in ((-1, 16, 64), (100, 12, 64), (100, 16, 40), (0, 16, 64), (16, 64, 7168), (65, 16, 64), (4096, 4096, 4096)):
+    for m, n, k in ((-1, 16, 64), (100, 12, 64), (100, 16, 40), (0, 16, 64), (16, 64, 7168), (4, 16384, 7168), (16, 8192, 7168), (65, 16, 64), (4096, 4096, 4096)):
         assert mbe.linear_act_fp4_workspace(m, n, k) == 0
 
 

@@ -75,7 +75,8 @@ def test_linear_epilogue(m, act):
 
 @pytest.mark.parametrize("m,n,k", [(1, 64, 7168), (1, 16, 16384), (2, 4096, 2048), (5, 2056, 1408), (16, 1040, 4096),
                                    (40, 72, 4096), (64, 264, 7168), (96, 64, 7168), (600, 520, 1408),
-                                   (1100, 8200, 288), (600, 4104, 1056), (1009, 2048, 4096), (50, 4104, 160)])
+                                   (1100, 8200, 288), (600, 4104, 1056), (1009, 2048, 4096), (50, 4104, 160), (1, 16400, 160), (4, 16384, 96), (5, 8200, 288),
+                                   (7, 8232, 3104), (16, 8192, 64)])
 def test_linear_long_and_wide(m, n, k):
     _check_linear(m, n, k, "silu")
 
