@@ -7,12 +7,12 @@
 // combine 5.4).
 //   up       one workgroup a (chosen expert, block of columns of the activation); the activation
 //            times the probability goes to the workspace as three bf16 terms, which keep its 24 bits
-//   down     the terms are columns of their own. For up to 64 pairs one workgroup 16 columns of
-//            the output, all experts: their sums meet in shared memory. Otherwise one a (chosen
-//            expert, block of columns of the output), and a pair's fp32 products go to the workspace
+//   down     the terms are columns of their own. For a few pairs one workgroup 16 columns of
+//            the output, all experts: their sums meet in shared memory. Otherwise units of an
+//            expert and a block of columns of the output, and a pair's fp32 products go to the workspace
 //   combine  adds a token's pairs in slot order, so no atomics are needed and the bits never change
-// Workgroups of few columns split k among their waves; where that leaves enough workgroups, the
-// waves have rows of W of their own and share the columns instead.
+// Workgroups of few columns split k among their waves; where there are more, the waves have rows of W of
+// their own and share the columns instead.
 #include <hip/hip_runtime.h>
 
 #include <stdint.h>
@@ -415,49 +415,6 @@ __global__ __launch_bounds__(kFewWaves * 64) void fp4_down_few_kernel(ExpertArgs
     }
 }
 
-// More pairs than that, and too few blocks for waves that share columns: up to five pairs of an
-// expert share one read of its weights. (16 tokens, 512 x 256, 64 experts, top 8: 8.0 us.)
-__global__ __launch_bounds__(kWaves * 64) void fp4_down_kernel(ExpertArgs a)
-{
-    constexpr int NX = 4;
-    __shared__ u32x4 shared[kWaves * NX * 64];  // the waves' stages, then their sums
-    __shared__ uint16_t list[kMaxPairs];
-    __shared__ int counts[kMaxPairs / 64];
-    const int lane = lane_id(), wave = wave_in_block(), k_tiles = (a.inter + kFp4K - 1) / kFp4K;
-    const int pairs = live_tokens(a.valid, a.tokens) * a.top_k, e = own_expert(a, pairs);
-    if (e < 0)
-        return;
-    const Tiles w[1] = {tiles_of(a.down_codes, a.down_scales, (int64_t)e * (a.hidden / 16) + blockIdx.x, k_tiles)};
-    Stream<1, NX, 2> stream;
-    stream.start(w, wave, kWaves);
-    const int n = expert_pairs<kWaves>(a, pairs, e, list, counts);
-    const rsrc_t h = terms_of(a);
-    for (int s0 = 0; s0 < n; s0 += kPairs) {
-        uint32_t col[NX];
-#pragma unroll
-        for (int i = 0; i < NX; ++i)
-            col[i] = term_column(a, list, n, s0, 4 * i + lane / 16) + lane % 16 * 16;
-        if (s0 > 0) {
-            __syncthreads();  // the sums have been read
-            stream.start(w, wave, kWaves);
-        }
-        f32x4 acc[1] = {};
-        stream.run(acc, w, h, col, a.inter, wave, kWaves, shared + wave * NX * 64);
-        __syncthreads();
-        f32x4 *joined = reinterpret_cast<f32x4 *>(shared);
-        joined[wave * 64 + lane] = join_terms(acc[0]);
-        __syncthreads();
-        const int row = threadIdx.x % 16, s = s0 + threadIdx.x / 16;
-        if (s >= n || (int)threadIdx.x / 16 >= kPairs)
-            continue;
-        float z = 0.0f;
-#pragma unroll
-        for (int q = 0; q < kWaves; ++q)
-            z += joined[q * 64 + row / 4 * 16 + (s - s0) * 3][row % 4];
-        a.z[(int64_t)list[s] * a.hidden + blockIdx.x * 16 + row] = z;
-    }
-}
-
 // Down products where experts have many tokens: units of one expert, up to G * 5 of its pairs and
 // eight waves of two row tiles (256 columns of the output). A workgroup takes every gridDim.x-th unit,
 // and its walk over one ends by sending for the next one's first steps: k is short here (2048: 16
@@ -652,21 +609,38 @@ int pair_groups(const ExpertSizes &s, int group)
     return each <= group ? 1 : (each <= 2 * group ? 2 : (each <= 3 * group ? 3 : 4));
 }
 
-// Whether the waves of a workgroup take rows of their own and share the columns: where that
-// still leaves a workgroup for every CU, and for more tokens than a few. (7168 x 2048, 8 of 64
-// experts, us, shared and split k: up, 2 tokens 43.9 and 39.7, 4 tokens 67.8 and 66.5, 8 tokens 123.6
-// and 127.0, 64 tokens 160 and 211; down, 2 tokens 29.1 + 4.6 for its combine and 38.2, 16 tokens 82
-// and 150, 64 tokens 107 and 331.)
-bool shares_columns(int64_t rows_of_w, unsigned experts)
+// Whether the up product's workgroups take many rows of W, whose waves share the columns, or 16 rows,
+// whose waves split k: the former for more tokens than a few, where that leaves two workgroups a CU, or
+// one for every other CU where experts may have so many tokens that the latter read their weights
+// again. (us, shared and split k: 7168 x 2048, 8 of 64 experts, 2 tokens 43.9 and 39.7, 4 tokens 67.8
+// and 66.5, 8 tokens, 736 workgroups, 123.6 and 127.0, 64 tokens 160 and 211; 8 tokens, 2048 x 8192, 4 of
+// 8, 512 workgroups 27.7 and 33.8; 4096 x 4096, 2 of 8, 256 workgroups, 12 tokens 34.8 and 28.5, 64
+// tokens 37.4 and 48.6; 128 tokens, 2048 x 1408, 8 of 16, 176 workgroups 55.4 and 69.9; 100 tokens, 4096 x
+// 512, 2 of 8, 32 workgroups 36.1 and 17.6.)
+bool up_shares(const ExpertArgs &a, int columns, unsigned experts)
 {
-    return ceil_div(rows_of_w, kManyWaves * 32) * experts >= 256;
+    const bool many = a.tokens * a.top_k > kFewPairs;
+    return (a.tokens > 4 || many) && ceil_div(a.inter, kManyWaves * columns) * experts >= (many ? 128 : 512);
+}
+
+// Whether the down product goes expert by expert, with a combine behind it, or in one kernel, 16 columns
+// of the output a workgroup: the former for more pairs than the latter holds, where there are units
+// for every CU, and where the waves' turns in the latter are long. (us, with 4 to 5 for the combine not
+// added, and in one: 2 tokens, 7168 x 2048, 8 of 64 experts 29.1 and 38.2; 2 of 8 experts of 4096 x
+// 4096, 6 tokens 24.7 and 24.1, 12 tokens 25.2 and 40.4, 32 tokens 31.8 and 58.8; 16 tokens, 4 of 16
+// experts of 1024 x 512 7.9 and 12.9, of 1024 x 1024 10.5 and 18.1.)
+bool down_by_expert(const ExpertArgs &a, unsigned experts)
+{
+    const int pairs = a.tokens * a.top_k;
+    return pairs > kFewPairs || (a.tokens > 1 && ceil_div(a.hidden, kDownWaves * kDownTiles * 16) * experts >= 256) ||
+           (pairs > 16 && pairs * a.inter > (1 << 15));
 }
 
 template <int ACT>
 block_status_t launch_up(const ExpertArgs &a, int groups, unsigned each, hipStream_t st)
 {
     constexpr int kCols = ACT == ACT_SWIGLU ? 16 : 32;
-    if (shares_columns((int64_t)a.inter * 32 / kCols, each) && (a.tokens > 4 || a.tokens * a.top_k > kFewPairs)) {
+    if (up_shares(a, kCols, each)) {
         const dim3 grid((unsigned)ceil_div(a.inter, kManyWaves * kCols), each), threads(kManyWaves * 64);
         if (groups == 1)
             return launch(fp4_up_many_kernel<ACT, 1>, grid, threads, 0, st, a);
@@ -697,7 +671,7 @@ block_status_t launch_down(const ExpertArgs &a, int groups, unsigned each, hipSt
 {
     const int pairs = a.tokens * a.top_k;
     block_status_t r;
-    if (shares_columns(a.hidden, each) && a.tokens > 1) {
+    if (down_by_expert(a, each)) {
         // as many workgroups as fit, and of these as many as have the same number of units
         const int64_t units = ceil_div(a.hidden, kDownWaves * kDownTiles * 16) * (each + pairs / (groups * kPairs));
         const int64_t fit = 256 * 2;
@@ -710,12 +684,10 @@ block_status_t launch_down(const ExpertArgs &a, int groups, unsigned each, hipSt
             r = launch(fp4_down_many_kernel<3>, grid, threads, 0, st, a);
         else
             r = launch(fp4_down_many_kernel<4>, grid, threads, 0, st, a);
-    } else if (pairs <= kFewPairs) {
+    } else {
         const dim3 grid((unsigned)(a.hidden / 16)), threads(kFewWaves * 64);
         return a.tokens == 1 ? launch(fp4_down_few_kernel<YDT, 1>, grid, threads, 0, st, a, few_parts(a))
                              : launch(fp4_down_few_kernel<YDT, 4>, grid, threads, 0, st, a, few_parts(a));
-    } else {
-        r = launch(fp4_down_kernel, dim3((unsigned)(a.hidden / 16), each), dim3(kWaves * 64), 0, st, a);
     }
     return r ? r : launch(fp4_combine_kernel<YDT>, dim3((unsigned)ceil_div((int64_t)a.tokens * a.hidden, 1024)), dim3(256), 0, st, a);
 }
