@@ -48,8 +48,8 @@ struct ExpertArgs {
     char *y;
     const int *valid;
     uint16_t *h;  // [3][pairs][inter]
-    float *z;     // [pairs][hidden]
-    int tokens, hidden, inter, experts, top_k, by_pair;
+    float *z;     // [parts][pairs][hidden]
+    int tokens, hidden, inter, experts, top_k, by_pair, parts;
     float limit;
 };
 
@@ -251,8 +251,9 @@ __device__ __forceinline__ void up_many_pass(const ExpertArgs &a, UpWalk<G> &wal
     }
     f32x4 acc[2][G];
     clear(acc);
-    walk.start_columns(x, ends, a.hidden);
-    walk.run(acc, x, ends, ends, a.hidden, (n + 15) / 16, xs);
+    ends.K = a.hidden;
+    walk.start_columns(x, ends);
+    walk.run(acc, x, ends, ends, (n + 15) / 16, xs);
     if (c0 >= a.inter)
         return;
     const int64_t plane = (int64_t)a.tokens * a.top_k * a.inter;
@@ -415,8 +416,8 @@ __global__ __launch_bounds__(kFewWaves * 64) void fp4_down_few_kernel(ExpertArgs
     }
 }
 
-// Down products where experts have many tokens: units of one expert, up to G * 5 of its pairs and
-// eight waves of two row tiles (256 columns of the output). A workgroup takes every gridDim.x-th unit,
+// Down products where experts have many tokens: units of one expert, up to G * 5 of its pairs, eight
+// waves of two row tiles (256 columns of the output) and one of `parts` parts of k. A workgroup takes every gridDim.x-th unit,
 // and its walk over one ends by sending for the next one's first steps: k is short here (2048: 16
 // steps). Its pairs' terms come from cache, 12 KB a pair and unit beside the unit's 278 KB of weights.
 // 64 tokens, 7168 x 2048, 64 experts: 107 us; a workgroup a unit 126; the weights' stream and the
@@ -494,20 +495,24 @@ __global__ __launch_bounds__(kDownWaves * 64, 4) void fp4_down_many_kernel(Exper
     __syncthreads();
 
     const int blocks = a.hidden / 16, row_units = (blocks + kDownWaves * kDownTiles - 1) / (kDownWaves * kDownTiles);
-    const int units = unit_count * row_units, k_tiles = (a.inter + kFp4K - 1) / kFp4K;
+    const int each = row_units * a.parts, units = unit_count * each, k_tiles = (a.inter + kFp4K - 1) / kFp4K;
+    const int part_tiles = (k_tiles + a.parts - 1) / a.parts;
     const rsrc_t h = terms_of(a);
-    auto block_of = [&](int u) { return (u % row_units * kDownWaves + wave) * kDownTiles; };
+    auto block_of = [&](int u) { return (u % each / a.parts * kDownWaves + wave) * kDownTiles; };
     auto ends_of = [&](typename DownWalk::Ends &ends, int u) {
         const bool there = u < units;  // past the last one: nothing is loaded
-        const int at = there ? u / row_units : 0;
+        const int at = there ? u / each : 0;
         const int e = __builtin_amdgcn_readfirstlane(unit_expert[at]), b0 = block_of(u);
         const int from = __builtin_amdgcn_readfirstlane(unit_at[at]), n = __builtin_amdgcn_readfirstlane(unit_end[at]) - from;
         const int rows = !there || b0 >= blocks ? 0 : (blocks - b0 < kDownTiles ? blocks - b0 : kDownTiles);
-        ends.w = run_of(a.down_codes, a.down_scales, rows ? (int64_t)e * blocks + b0 : 0, k_tiles, rows);
+        const int t0 = u % a.parts * part_tiles, left = k_tiles - t0;  // parts are no more than would leave one empty
+        ends.w = run_of(a.down_codes, a.down_scales, rows ? (int64_t)e * blocks + b0 : 0, k_tiles, rows, t0,
+                        left < part_tiles ? left : part_tiles);
+        ends.K = left <= part_tiles ? a.inter - t0 * kFp4K : part_tiles * kFp4K;
 #pragma unroll
         for (int i = 0; i < DownWalk::kLoads; ++i) {
             const int c = 4 * (wave + i * kDownWaves) + lane / 16;
-            ends.col[i] = there ? term_column(a, list + from, n, c / 16 * kPairs, c % 16) + lane % 16 * 16 : kNowhere;
+            ends.col[i] = there ? term_column(a, list + from, n, c / 16 * kPairs, c % 16) + t0 * kFp4K * 2 + lane % 16 * 16 : kNowhere;
         }
     };
     int u = blockIdx.x;
@@ -517,14 +522,15 @@ __global__ __launch_bounds__(kDownWaves * 64, 4) void fp4_down_many_kernel(Exper
     DownWalk walk;
     ends_of(ends, u);
     walk.start_tiles(ends);
-    walk.start_columns(h, ends, a.inter);
+    walk.start_columns(h, ends);
     for (; u < units; u += gridDim.x) {
-        const int at = u / row_units, b0 = block_of(u);
+        const int at = u / each, b0 = block_of(u);
         const int from = __builtin_amdgcn_readfirstlane(unit_at[at]), n = __builtin_amdgcn_readfirstlane(unit_end[at]) - from;
         ends_of(next, u + gridDim.x);
         f32x4 acc[kDownTiles][G];
         clear(acc);
-        walk.run(acc, h, ends, next, a.inter, (n + kPairs - 1) / kPairs, xs);
+        walk.run(acc, h, ends, next, (n + kPairs - 1) / kPairs, xs);
+        float *to = a.z + (int64_t)(u % a.parts) * a.tokens * a.top_k * a.hidden + b0 * 16 + lane / 16 * 4;
 #pragma unroll
         for (int g = 0; g < G; ++g) {
             const int c = lane % 16, s = g * kPairs + c / 3;
@@ -532,7 +538,7 @@ __global__ __launch_bounds__(kDownWaves * 64, 4) void fp4_down_many_kernel(Exper
             for (int i = 0; i < kDownTiles; ++i) {
                 const f32x4 z = join_terms(acc[i][g]);
                 if (c < 15 && c % 3 == 0 && s < n && b0 + i < blocks)
-                    *reinterpret_cast<f32x4 *>(a.z + (int64_t)list[from + s] * a.hidden + (b0 + i) * 16 + lane / 16 * 4) = z;
+                    *reinterpret_cast<f32x4 *>(to + (int64_t)list[from + s] * a.hidden + i * 16) = z;
             }
         }
         ends = next;
@@ -550,14 +556,17 @@ __global__ __launch_bounds__(256) void fp4_combine_kernel(ExpertArgs a)
     const u32x2 residual = a.residual ? *reinterpret_cast<const u32x2 *>(a.residual + i) : u32x2{0, 0};
     f32x4 v = {0, 0, 0, 0};
     constexpr int kTogether = 8;  // loads that go out together
-    for (int j0 = 0; j0 < a.top_k; j0 += kTogether) {
+    const int all = a.top_k * a.parts;  // a slot's parts follow each other
+    const int64_t plane = (int64_t)a.tokens * a.top_k * a.hidden;
+    for (int j0 = 0; j0 < all; j0 += kTogether) {
         f32x4 z[kTogether];
         bool in[kTogether];
 #pragma unroll
         for (int j = 0; j < kTogether; ++j) {
-            const int pair = t * a.top_k + (j0 + j < a.top_k ? j0 + j : 0), e = a.ids[pair];
-            in[j] = j0 + j < a.top_k && e >= 0 && e < a.experts;
-            z[j] = *reinterpret_cast<const f32x4 *>(a.z + (int64_t)pair * a.hidden + c);  // unwritten where the id is none
+            const int item = j0 + j < all ? j0 + j : 0, pair = t * a.top_k + item / a.parts, e = a.ids[pair];
+            in[j] = j0 + j < all && e >= 0 && e < a.experts;
+            // unwritten where the id is none
+            z[j] = *reinterpret_cast<const f32x4 *>(a.z + item % a.parts * plane + (int64_t)pair * a.hidden + c);
         }
 #pragma unroll
         for (int j = 0; j < kTogether; ++j)
@@ -595,10 +604,6 @@ block_status_t check_experts(const ExpertSizes &s, block_act_t act, float limit)
     return BLOCK_OK;
 }
 
-// Workspace: the activations' terms, then the pairs' products.
-int64_t h_bytes(const ExpertSizes &s) { return round_up(s.tokens * s.top_k * s.inter * 6, 16); }
-int64_t expert_bytes(const ExpertSizes &s) { return h_bytes(s) + s.tokens * s.top_k * s.hidden * 4; }
-
 // Groups of pairs that share a read of an expert's weights: enough for one and a half times the
 // pairs an expert has on average. (Enough for the average, and for twice it: up, 128 tokens, 7168 x
 // 2048, 64 experts, top 8, 264 and 185 us for 185; down, 32 tokens, 113 and 99 for 101.)
@@ -623,18 +628,41 @@ bool up_shares(const ExpertArgs &a, int columns, unsigned experts)
     return (a.tokens > 4 || many) && ceil_div(a.inter, kManyWaves * columns) * experts >= (many ? 128 : 512);
 }
 
+// Experts that may have a token, times the blocks of rows of their down product.
+int64_t down_units(const ExpertSizes &s)
+{
+    const int64_t pairs = s.tokens * s.top_k;
+    return ceil_div(s.hidden, kDownWaves * kDownTiles * 16) * (pairs < s.experts ? pairs : s.experts);
+}
+
 // Whether the down product goes expert by expert, with a combine behind it, or in one kernel, 16 columns
 // of the output a workgroup: the former for more pairs than the latter holds, where there are units
-// for every CU, and where the waves' turns in the latter are long. (us, with 4 to 5 for the combine not
-// added, and in one: 2 tokens, 7168 x 2048, 8 of 64 experts 29.1 and 38.2; 2 of 8 experts of 4096 x
-// 4096, 6 tokens 24.7 and 24.1, 12 tokens 25.2 and 40.4, 32 tokens 31.8 and 58.8; 16 tokens, 4 of 16
-// experts of 1024 x 512 7.9 and 12.9, of 1024 x 1024 10.5 and 18.1.)
-bool down_by_expert(const ExpertArgs &a, unsigned experts)
+// for every CU, and where the latter's waves have several long turns. (us, with 4 to 5 for the combine
+// not added, and in one: 2 tokens, 7168 x 2048, 8 of 64 experts 29.1 and 38.2; 2 of 8 experts of 4096 x
+// 4096, 4 tokens 17.1 and 18.4, 8 tokens 18.4 and 30.6, 32 tokens 31.8 and 58.8; 4 tokens, 4 of 8 of 2048 x
+// 8192 18.3 and 42.9; 16 tokens, 4 of 16 of 1024 x 512 7.9 and 12.9, of 1024 x 1024 10.5 and 18.1.)
+bool down_by_expert(const ExpertSizes &s)
 {
-    const int pairs = a.tokens * a.top_k;
-    return pairs > kFewPairs || (a.tokens > 1 && ceil_div(a.hidden, kDownWaves * kDownTiles * 16) * experts >= 256) ||
-           (pairs > 16 && pairs * a.inter > (1 << 15));
+    const int64_t pairs = s.tokens * s.top_k;
+    return pairs > kFewPairs || (s.tokens > 1 && down_units(s) >= 256) || (pairs > kFewWaves && pairs * s.inter >= (1 << 16));
 }
+
+// Parts of k of the down product by expert: more where the units are fewer than two a CU, of eight steps
+// at least. (us, in one and in parts: 4096 x 14336, 2 of 8 experts, 16 tokens 89 and 54.5, 64 tokens 125
+// and 82.5, 128 tokens 166 and 132; 8 tokens, 2048 x 8192, 4 of 8 48.8 and 19.7; 64 tokens, 4096 x 2048, 2
+// of 8 23.6 and 21.4.)
+int down_parts(const ExpertSizes &s)
+{
+    const int64_t steps = ceil_div(s.inter, kFp4K);
+    int parts = 1;
+    while (down_by_expert(s) && parts < 8 && down_units(s) * parts * 2 <= 512 && steps >= parts * 16)
+        parts *= 2;
+    return parts;
+}
+
+// Workspace: the activations' terms, then the pairs' products.
+int64_t h_bytes(const ExpertSizes &s) { return round_up(s.tokens * s.top_k * s.inter * 6, 16); }
+int64_t expert_bytes(const ExpertSizes &s) { return h_bytes(s) + down_parts(s) * s.tokens * s.top_k * s.hidden * 4; }
 
 template <int ACT>
 block_status_t launch_up(const ExpertArgs &a, int groups, unsigned each, hipStream_t st)
@@ -667,13 +695,13 @@ int few_parts(const ExpertArgs &a)
 }
 
 template <int YDT>
-block_status_t launch_down(const ExpertArgs &a, int groups, unsigned each, hipStream_t st)
+block_status_t launch_down(const ExpertArgs &a, const ExpertSizes &s, unsigned each, hipStream_t st)
 {
-    const int pairs = a.tokens * a.top_k;
+    const int pairs = a.tokens * a.top_k, groups = pair_groups(s, kPairs);
     block_status_t r;
-    if (down_by_expert(a, each)) {
+    if (down_by_expert(s)) {
         // as many workgroups as fit, and of these as many as have the same number of units
-        const int64_t units = ceil_div(a.hidden, kDownWaves * kDownTiles * 16) * (each + pairs / (groups * kPairs));
+        const int64_t units = ceil_div(a.hidden, kDownWaves * kDownTiles * 16) * (each + pairs / (groups * kPairs)) * a.parts;
         const int64_t fit = 256 * 2;
         const dim3 grid((unsigned)ceil_div(units, ceil_div(units, fit))), threads(kDownWaves * 64);
         if (groups == 1)
@@ -743,7 +771,7 @@ block_status_t block_moe_experts_fp4(const uint16_t *x, const uint8_t *up_codes,
     a.h = static_cast<uint16_t *>(workspace);
     a.z = reinterpret_cast<float *>(static_cast<char *>(workspace) + h_bytes(s));
     a.tokens = (int)tokens, a.hidden = (int)hidden, a.inter = (int)inter, a.experts = n_experts, a.top_k = top_k;
-    a.limit = limit;
+    a.limit = limit, a.parts = down_parts(s);
     const int64_t pairs = tokens * top_k;
     a.by_pair = pairs < n_experts;
     const unsigned each = (unsigned)(a.by_pair ? pairs : n_experts);
@@ -751,9 +779,7 @@ block_status_t block_moe_experts_fp4(const uint16_t *x, const uint8_t *up_codes,
     if (const block_status_t r = act == BLOCK_ACT_SWIGLU ? launch_up<ACT_SWIGLU>(a, groups, each, stream)
                                                          : launch_up<ACT_SQUARED_RELU>(a, groups, each, stream))
         return r;
-    const int pair_columns = pair_groups(s, kPairs);
-    return y_dtype == BLOCK_FP32 ? launch_down<DT_F32>(a, pair_columns, each, stream)
-                                 : launch_down<DT_BF16>(a, pair_columns, each, stream);
+    return y_dtype == BLOCK_FP32 ? launch_down<DT_F32>(a, s, each, stream) : launch_down<DT_BF16>(a, s, each, stream);
 }
 
 }  // extern "C"

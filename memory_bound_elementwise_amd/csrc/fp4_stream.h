@@ -27,19 +27,22 @@ __device__ __forceinline__ Tiles tiles_of(const uint8_t *codes, const uint8_t *s
             make_rsrc(scales + block * k_tiles * kFp4Scales, there ? (uint32_t)k_tiles * kFp4Scales : 0u)};
 }
 
-// Neighbouring row blocks of one matrix: the first one's tiles and the distance of the blocks, in k
-// tiles. (A resource a block would take four times the scalar registers.)
+// Neighbouring row blocks of one matrix over a range of its k tiles: the first one's tiles, the distance
+// of the blocks in tiles and how many of each there are. (A resource a block would take four times the
+// scalar registers.)
 struct TileRun {
     Tiles first;
-    int k_tiles;
+    int k_tiles, own;
 };
 
-// rows: the blocks that are there, of those that are asked for.
-__device__ __forceinline__ TileRun run_of(const uint8_t *codes, const uint8_t *scales, int64_t block, int k_tiles, int there)
+// there: the blocks that are there, of those that are asked for; own: k tiles from `from` on.
+__device__ __forceinline__ TileRun run_of(const uint8_t *codes, const uint8_t *scales, int64_t block, int k_tiles, int there,
+                                          int from, int own)
 {
-    return {{make_rsrc(codes + block * k_tiles * kFp4Codes, (uint32_t)(there * k_tiles) * kFp4Codes),
-             make_rsrc(scales + block * k_tiles * kFp4Scales, (uint32_t)(there * k_tiles) * kFp4Scales)},
-            k_tiles};
+    const int64_t tile = block * k_tiles + from;
+    const uint32_t tiles = there ? (uint32_t)((there - 1) * k_tiles + own) : 0u;
+    return {{make_rsrc(codes + tile * kFp4Codes, tiles * kFp4Codes), make_rsrc(scales + tile * kFp4Scales, tiles * kFp4Scales)},
+            k_tiles, own};
 }
 
 // A wave's next tiles of RT row blocks, in flight. A tile past the last reads zeros.
@@ -61,7 +64,7 @@ struct Ahead {
     __device__ __forceinline__ void load(const TileRun &w, int t)
     {
         const int lane = lane_id();
-        const uint32_t at = t < w.k_tiles ? lane * 16 : kNowhere, scale_at = t < w.k_tiles ? lane % 16 * 4 : kNowhere;
+        const uint32_t at = t < w.own ? lane * 16 : kNowhere, scale_at = t < w.own ? lane % 16 * 4 : kNowhere;
 #pragma unroll
         for (int i = 0; i < RT; ++i) {
             const int tile = i * w.k_tiles + t;
@@ -150,7 +153,7 @@ struct Stream {
     }
 };
 
-// acc[i][g] += 16 rows of W (w[i]) times 16 columns (group g) over all k, with the columns shared: W
+// acc[i][g] += 16 rows of W (w[i]) times 16 columns (group g) over K, with the columns shared: W
 // waves, each with rows of its own, walk k together. A wave loads its part of the columns' next 128
 // k (load i of wave w takes columns 4 (w + i W) ..+4 of them: col[i], the start of column lane / 16
 // of these plus 16 (lane % 16) bytes), and they meet in shared memory: xs, two sets of G * 256
@@ -174,6 +177,7 @@ struct Walk {
     struct Ends {
         typename std::conditional<CHAIN, TileRun, TileSet<RT>>::type w;
         uint32_t col[kLoads];
+        int K;
     };
     Ahead<RT> tiles[D];
     u32x4 columns[2][kLoads];
@@ -185,26 +189,25 @@ struct Walk {
             load_tiles(tiles[d], of.w, d);
     }
 
-    __device__ __forceinline__ void fetch(u32x4 (&to)[kLoads], rsrc_t x, const Ends &of, int K, int t)
+    __device__ __forceinline__ void fetch(u32x4 (&to)[kLoads], rsrc_t x, const Ends &of, int t)
     {
         const int k = t * kFp4K + lane_id() % 16 * 8;
 #pragma unroll
         for (int i = 0; i < kLoads; ++i)
-            to[i] = __builtin_amdgcn_raw_buffer_load_b128(x, k < K ? of.col[i] : kNowhere, t * kFp4K * 2, 0);
+            to[i] = __builtin_amdgcn_raw_buffer_load_b128(x, k < of.K ? of.col[i] : kNowhere, t * kFp4K * 2, 0);
     }
 
-    __device__ __forceinline__ void start_columns(rsrc_t x, const Ends &of, int K)
+    __device__ __forceinline__ void start_columns(rsrc_t x, const Ends &of)
     {
-        fetch(columns[0], x, of, K, 0);
-        fetch(columns[1], x, of, K, 1);
+        fetch(columns[0], x, of, 0);
+        fetch(columns[1], x, of, 1);
     }
 
     // groups: those of the G that have columns.
-    __device__ __forceinline__ void run(f32x4 (&acc)[RT][G], rsrc_t x, const Ends &of, const Ends &next, int K, int groups,
-                                        u32x4 *xs)
+    __device__ __forceinline__ void run(f32x4 (&acc)[RT][G], rsrc_t x, const Ends &of, const Ends &next, int groups, u32x4 *xs)
     {
         static_assert(W % 2 == 0, "the columns of a wave's loads have one c % 8");
-        const int lane = lane_id(), wave = wave_in_block(), k_tiles = (K + kFp4K - 1) / kFp4K;
+        const int lane = lane_id(), wave = wave_in_block(), k_tiles = (of.K + kFp4K - 1) / kFp4K;
         const int i16 = lane % 16, q = lane / 16;
         const int put = put_at(4 * wave + q);                         // load i: 64 W i further
         const int get = i16 * 16 + (q ^ i16 % 8), get_odd = get ^ 4;  // word j: 8 (j / 2) further
@@ -250,7 +253,7 @@ struct Walk {
             __attribute__((always_inline)) {
             multiply(tiles[d], columns[d % 2], xs + d % 2 * G * 256);
             // loads come back in order: columns that are sent for behind later tiles would wait for those
-            fetch(columns[d % 2], x, column_of, K, column);
+            fetch(columns[d % 2], x, column_of, column);
             load_tiles(tiles[d], tile_of.w, tile);
         };
         int t = 0;

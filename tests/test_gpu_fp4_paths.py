@@ -46,6 +46,31 @@ def test_top_k_of_sixty_four(tokens):
     _check_experts(tokens, 64, 64, 64, 64, "squared_relu")
 
 
+# inter of 16 steps and more, in two, four and eight parts, the last one shorter or not
+@pytest.mark.parametrize("inter", [2048, 2080, 2176, 4224, 8192, 8224])
+@pytest.mark.parametrize("tokens", [9, 40])
+def test_down_in_parts(tokens, inter):
+    _check_experts(tokens, 96, inter, 8, 4, "squared_relu")
+    ids = _skewed(tokens, 8, 4, inter)
+    ids[3] = -1
+    ids[5:7, 1:] = 8
+    _check_experts(tokens, 544, inter, 8, 4, "swiglu", 7.0, dtype=torch.float32, residual=False, ids=ids)
+
+
+@pytest.mark.parametrize("valid", [0, 5, 20])
+def test_down_in_parts_of_some_tokens(valid):
+    g = torch.Generator().manual_seed(valid)
+    tokens, hidden, inter, experts, top_k = 20, 96, 4224, 8, 4
+    (_, wu), (_, wd) = _layer(g, experts, hidden, inter, "swiglu")
+    x, (ids, probs) = _normal(g, tokens, hidden).to(DEV), (t.to(DEV) for t in _choice(g, tokens, experts, top_k))
+    whole = moe_experts_fp4(x, *wu, *wd, ids, probs, torch.empty(tokens, hidden, device=DEV), limit=7.0)
+    x[valid:] = float("nan")
+    ids[valid:] = 1 << 30
+    y = torch.full((tokens, hidden), 77.0, device=DEV)
+    moe_experts_fp4(x, *wu, *wd, ids, probs, y, limit=7.0, valid_tokens=torch.tensor([valid], dtype=torch.int32, device=DEV))
+    assert torch.equal(y[:valid], whole[:valid]) and (y[valid:] == 77).all()
+
+
 def test_bits_do_not_depend_on_the_batch():
     """A token's bits in a batch of one composition are those in another of the same sizes."""
     g = torch.Generator().manual_seed(3)
@@ -137,7 +162,8 @@ def test_experts_past_32_bits(tokens, top_k):
         return moe_experts_fp4(x, *wu, *wd, ids, probs, torch.empty(tokens, hidden, device=DEV), limit=7.0)
     y = run(wu, wd, ids + (experts - 16))
     assert torch.isfinite(y).all() and (y != 0).any()
-    assert torch.equal(y, run([t[-16:] for t in wu], [t[-16:] for t in wd], ids))
+    # the same experts at the front of a layer of the same sizes, which so takes the same variant
+    assert torch.equal(y, run([t.roll(16, 0) for t in wu], [t.roll(16, 0) for t in wd], ids))
 
 
 def test_linear_past_32_bits():
