@@ -49,7 +49,8 @@ struct ExpertArgs {
     const int *valid;
     uint16_t *h;  // [3][pairs][inter]
     float *z;     // [parts][pairs][hidden]
-    int tokens, hidden, inter, experts, top_k, by_pair, parts;
+    int tokens, hidden, inter, experts, top_k, by_pair;
+    int part_bits;  // of parts, a power of two
     float limit;
 };
 
@@ -495,17 +496,17 @@ __global__ __launch_bounds__(kDownWaves * 64, 4) void fp4_down_many_kernel(Exper
     __syncthreads();
 
     const int blocks = a.hidden / 16, row_units = (blocks + kDownWaves * kDownTiles - 1) / (kDownWaves * kDownTiles);
-    const int each = row_units * a.parts, units = unit_count * each, k_tiles = (a.inter + kFp4K - 1) / kFp4K;
-    const int part_tiles = (k_tiles + a.parts - 1) / a.parts;
+    const int parts = 1 << a.part_bits, each = row_units * parts, units = unit_count * each, k_tiles = (a.inter + kFp4K - 1) / kFp4K;
+    const int part_tiles = (k_tiles + parts - 1) >> a.part_bits;
     const rsrc_t h = terms_of(a);
-    auto block_of = [&](int u) { return (u % each / a.parts * kDownWaves + wave) * kDownTiles; };
+    auto block_of = [&](int u) { return ((u % each >> a.part_bits) * kDownWaves + wave) * kDownTiles; };
     auto ends_of = [&](typename DownWalk::Ends &ends, int u) {
         const bool there = u < units;  // past the last one: nothing is loaded
         const int at = there ? u / each : 0;
         const int e = __builtin_amdgcn_readfirstlane(unit_expert[at]), b0 = block_of(u);
         const int from = __builtin_amdgcn_readfirstlane(unit_at[at]), n = __builtin_amdgcn_readfirstlane(unit_end[at]) - from;
         const int rows = !there || b0 >= blocks ? 0 : (blocks - b0 < kDownTiles ? blocks - b0 : kDownTiles);
-        const int t0 = u % a.parts * part_tiles, left = k_tiles - t0;  // parts are no more than would leave one empty
+        const int t0 = (u & (parts - 1)) * part_tiles, left = k_tiles - t0;  // parts are no more than would leave one empty
         ends.w = run_of(a.down_codes, a.down_scales, rows ? (int64_t)e * blocks + b0 : 0, k_tiles, rows, t0,
                         left < part_tiles ? left : part_tiles);
         ends.K = left <= part_tiles ? a.inter - t0 * kFp4K : part_tiles * kFp4K;
@@ -530,7 +531,7 @@ __global__ __launch_bounds__(kDownWaves * 64, 4) void fp4_down_many_kernel(Exper
         f32x4 acc[kDownTiles][G];
         clear(acc);
         walk.run(acc, h, ends, next, (n + kPairs - 1) / kPairs, xs);
-        float *to = a.z + (int64_t)(u % a.parts) * a.tokens * a.top_k * a.hidden + b0 * 16 + lane / 16 * 4;
+        float *to = a.z + (int64_t)(u & (parts - 1)) * a.tokens * a.top_k * a.hidden + b0 * 16 + lane / 16 * 4;
 #pragma unroll
         for (int g = 0; g < G; ++g) {
             const int c = lane % 16, s = g * kPairs + c / 3;
@@ -556,17 +557,17 @@ __global__ __launch_bounds__(256) void fp4_combine_kernel(ExpertArgs a)
     const u32x2 residual = a.residual ? *reinterpret_cast<const u32x2 *>(a.residual + i) : u32x2{0, 0};
     f32x4 v = {0, 0, 0, 0};
     constexpr int kTogether = 8;  // loads that go out together
-    const int all = a.top_k * a.parts;  // a slot's parts follow each other
+    const int parts = 1 << a.part_bits, all = a.top_k * parts;  // a slot's parts follow each other
     const int64_t plane = (int64_t)a.tokens * a.top_k * a.hidden;
     for (int j0 = 0; j0 < all; j0 += kTogether) {
         f32x4 z[kTogether];
         bool in[kTogether];
 #pragma unroll
         for (int j = 0; j < kTogether; ++j) {
-            const int item = j0 + j < all ? j0 + j : 0, pair = t * a.top_k + item / a.parts, e = a.ids[pair];
+            const int item = j0 + j < all ? j0 + j : 0, pair = t * a.top_k + (item >> a.part_bits), e = a.ids[pair];
             in[j] = j0 + j < all && e >= 0 && e < a.experts;
             // unwritten where the id is none
-            z[j] = *reinterpret_cast<const f32x4 *>(a.z + item % a.parts * plane + (int64_t)pair * a.hidden + c);
+            z[j] = *reinterpret_cast<const f32x4 *>(a.z + (item & (parts - 1)) * plane + (int64_t)pair * a.hidden + c);
         }
 #pragma unroll
         for (int j = 0; j < kTogether; ++j)
@@ -651,18 +652,18 @@ bool down_by_expert(const ExpertSizes &s)
 // at least. (us, in one and in parts: 4096 x 14336, 2 of 8 experts, 16 tokens 89 and 54.5, 64 tokens 125
 // and 82.5, 128 tokens 166 and 132; 8 tokens, 2048 x 8192, 4 of 8 48.8 and 19.7; 64 tokens, 4096 x 2048, 2
 // of 8 23.6 and 21.4.)
-int down_parts(const ExpertSizes &s)
+int down_part_bits(const ExpertSizes &s)
 {
     const int64_t steps = ceil_div(s.inter, kFp4K);
-    int parts = 1;
-    while (down_by_expert(s) && parts < 8 && down_units(s) * parts * 2 <= 512 && steps >= parts * 16)
-        parts *= 2;
-    return parts;
+    int bits = 0;
+    while (down_by_expert(s) && bits < 3 && down_units(s) << (bits + 1) <= 512 && steps >= 16 << bits)
+        ++bits;
+    return bits;
 }
 
 // Workspace: the activations' terms, then the pairs' products.
 int64_t h_bytes(const ExpertSizes &s) { return round_up(s.tokens * s.top_k * s.inter * 6, 16); }
-int64_t expert_bytes(const ExpertSizes &s) { return h_bytes(s) + down_parts(s) * s.tokens * s.top_k * s.hidden * 4; }
+int64_t expert_bytes(const ExpertSizes &s) { return h_bytes(s) + (s.tokens * s.top_k * s.hidden * 4 << down_part_bits(s)); }
 
 template <int ACT>
 block_status_t launch_up(const ExpertArgs &a, int groups, unsigned each, hipStream_t st)
@@ -701,7 +702,7 @@ block_status_t launch_down(const ExpertArgs &a, const ExpertSizes &s, unsigned e
     block_status_t r;
     if (down_by_expert(s)) {
         // as many workgroups as fit, and of these as many as have the same number of units
-        const int64_t units = ceil_div(a.hidden, kDownWaves * kDownTiles * 16) * (each + pairs / (groups * kPairs)) * a.parts;
+        const int64_t units = ceil_div(a.hidden, kDownWaves * kDownTiles * 16) * (each + pairs / (groups * kPairs)) << a.part_bits;
         const int64_t fit = 256 * 2;
         const dim3 grid((unsigned)ceil_div(units, ceil_div(units, fit))), threads(kDownWaves * 64);
         if (groups == 1)
@@ -771,7 +772,7 @@ block_status_t block_moe_experts_fp4(const uint16_t *x, const uint8_t *up_codes,
     a.h = static_cast<uint16_t *>(workspace);
     a.z = reinterpret_cast<float *>(static_cast<char *>(workspace) + h_bytes(s));
     a.tokens = (int)tokens, a.hidden = (int)hidden, a.inter = (int)inter, a.experts = n_experts, a.top_k = top_k;
-    a.limit = limit, a.parts = down_parts(s);
+    a.limit = limit, a.part_bits = down_part_bits(s);
     const int64_t pairs = tokens * top_k;
     a.by_pair = pairs < n_experts;
     const unsigned each = (unsigned)(a.by_pair ? pairs : n_experts);
