@@ -261,7 +261,9 @@ block_status_t block_linear_act_fp4(const uint16_t *x, const uint8_t *codes, con
 /*
  * block_moe_experts with the weights in 4 bits: up_* hold experts matrices [2 inter, hidden] (or
  * [inter, hidden] for BLOCK_ACT_SQUARED_RELU), down_* experts matrices [hidden, inter]. hidden and
- * inter multiples of 32, 32 .. 2^16; everything else as there.
+ * inter multiples of 32, 32 .. 2^16; everything else as there. An infinite weight gives an infinity
+ * or a NaN as the product with it does; of the down product that of the activation, which counts as
+ * 0 below 2^-133.
  */
 int64_t block_moe_experts_fp4_workspace(int64_t tokens, int64_t hidden, int64_t inter, int experts, int top_k);
 block_status_t block_moe_experts_fp4(const uint16_t *x, const uint8_t *up_codes, const uint8_t *up_scales,

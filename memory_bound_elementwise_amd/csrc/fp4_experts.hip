@@ -55,8 +55,8 @@ struct ExpertArgs {
 };
 
 // An fp32 value as the sum of three bf16: its first 8 bits, the next 8 and the rest (nothing is
-// lost, but below 2^-109, where the last term runs out of exponents). Of an infinity or a NaN the
-// first term is one and the others zero.
+// lost, but below 2^-109, where the last term runs out of exponents; what is below 2^-133 is 0). Of
+// an infinity or a NaN the first term is one and the others zero.
 __device__ __forceinline__ void three_terms(float h, uint16_t (&term)[3])
 {
     const uint32_t bits = __float_as_uint(h);
@@ -320,12 +320,16 @@ __global__ __launch_bounds__(kManyWaves * 64, G == 1 ? 8 : 4) void fp4_up_many_k
 // pair's three is then in the lane of the first.
 constexpr int kPairs = 5;
 
+// An infinite weight, or activation, makes the first terms' sum infinite or NaN as the product of the
+// whole would be; the further terms may be zeros, which times an infinity would make a NaN of it.
 __device__ __forceinline__ f32x4 join_terms(const f32x4 &v)
 {
     f32x4 z;
 #pragma unroll
-    for (int r = 0; r < 4; ++r)  // row_shl: what the next lane and the one behind it hold
-        z[r] = v[r] + dpp<0x101>(v[r]) + dpp<0x102>(v[r]);
+    for (int r = 0; r < 4; ++r) {  // row_shl: what the next lane and the one behind it hold
+        const float all = v[r] + dpp<0x101>(v[r]) + dpp<0x102>(v[r]);
+        z[r] = __builtin_isinf(v[r]) ? v[r] : all;
+    }
     return z;
 }
 
