@@ -173,7 +173,10 @@ block_status_t block_moe_layer(const uint16_t *x, const void *router_weight, blo
  * experts the top_k of largest c are chosen, in descending order. Weights carry no bias:
  *     probs_j = scale s_j   or, with renormalize,   scale s_j / sum over the chosen s
  * Scores, ranks and sums are formed in fp64, each weight is rounded once to fp32. Equal ranks go in
- * increasing index, NaN before any number. An expert whose logit is -inf is masked: its score is 0
+ * increasing index, NaN before any number. Without a bias experts are ranked by their logits, and groups
+ * by the largest where group_top is 1: that is the scores' order, kept where the scores themselves
+ * run out of digits (the softmax's are 0 from 745 below the largest logit on, the sigmoid's 1 from 37
+ * on). In a sum with a bias or of two such scores count as the equal numbers that they are. An expert whose logit is -inf is masked: its score is 0
  * and its rank -inf whatever its bias, so that it is chosen (with weight 0) only where too few
  * others are left; where the chosen scores are all 0, so are the weights. (Renormalised softmax
  * weights are the softmax of the chosen logits, also far below the row's largest.)

@@ -173,7 +173,31 @@ __device__ __forceinline__ void logits_at(const GateArgs &a, int64_t row, const 
     }
 }
 
-// s = softmax(v) over a token's lanes; all zeros where every logit is -inf.
+// What a softmax takes from all of its logits: the largest, and one over the sum of e^(v - largest).
+struct Softmax {
+    double largest, share;
+    __device__ __forceinline__ double operator()(double v) const
+    {
+        return largest == -INFINITY ? 0.0 : exp_below(v - largest) * share;
+    }
+};
+
+// e = e^(v - largest) over a token's lanes, all zeros where every logit is -inf. top: of the order keys.
+template <int L, int V>
+__device__ __forceinline__ Softmax softmax_parts(const double (&v)[V], uint64_t top, double (&e)[V])
+{
+    const double m = of_key(lanes_max<L>(top));
+    double sum = 0.0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        e[i] = m == -INFINITY ? 0.0 : exp_below(v[i] - m);
+        sum += e[i];
+    }
+    sum = lanes_sum<L>(sum);
+    return {m, sum == 0.0 ? 0.0 : reciprocal(sum)};  // a sum is 0, or at least 1
+}
+
+// s = softmax(v) over a token's lanes.
 template <int L, int V>
 __device__ __forceinline__ void softmax(const double (&v)[V], double (&s)[V])
 {
@@ -181,15 +205,7 @@ __device__ __forceinline__ void softmax(const double (&v)[V], double (&s)[V])
 #pragma unroll
     for (int i = 0; i < V; ++i)
         top = larger(top, order_key(v[i]));
-    const double m = of_key(lanes_max<L>(top));
-    double sum = 0.0;
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-        s[i] = m == -INFINITY ? 0.0 : exp_below(v[i] - m);
-        sum += s[i];
-    }
-    sum = lanes_sum<L>(sum);
-    const double q = sum == 0.0 ? 0.0 : reciprocal(sum);  // a sum is 0, or at least 1
+    const double q = softmax_parts<L, V>(v, top, s).share;
 #pragma unroll
     for (int i = 0; i < V; ++i)
         s[i] *= q;
@@ -210,24 +226,48 @@ __device__ __forceinline__ int lanes_a_group(int groups)
 
 // The choice, in fp64: lane l gets the experts of slots l, L + l, ... and their scores. v: the
 // logits, -inf past the last expert.
-template <int L, int V, int Q>
+//
+// Without a bias (BIASED false) experts are ranked by their logits: the scores have the same order, but
+// run out of exponents (the softmax's) or come to 1 (the sigmoid's) and then tie. Scores are formed for
+// the chosen ones alone, and for the worth of a group that is a sum of two.
+template <int L, int V, int Q, bool BIASED>
 __device__ __forceinline__ void choose(const GateRule &r, int experts, int l, const double (&v)[V], const float (&bias)[V],
                                        const Room &room, int (&id)[Q], double (&p)[Q])
 {
     constexpr int T = 64 / L;
     double s[V];
-    if (r.scores == BLOCK_SCORES_SIGMOID) {
+    uint64_t key[V];  // of the rank; 0, below every number's, for what cannot be chosen
+    Softmax all = {0.0, 0.0};
+    const auto score_of = [&](double x) __attribute__((always_inline)) {
+        return r.scores == BLOCK_SCORES_SIGMOID ? sigmoid(x) : all(x);
+    };
+    if constexpr (BIASED) {
+        if (r.scores == BLOCK_SCORES_SIGMOID) {
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                s[i] = sigmoid(v[i]);
+        } else {
+            softmax<L, V>(v, s);
+        }
 #pragma unroll
         for (int i = 0; i < V; ++i)
-            s[i] = sigmoid(v[i]);
+            key[i] = i * L + l < experts ? order_key(v[i] == -INFINITY ? v[i] : s[i] + (double)bias[i]) : 0;
     } else {
-        softmax<L, V>(v, s);
-    }
-    uint64_t key[V];  // of the rank; 0, below every number's, for what cannot be chosen
+        uint64_t top = 0;
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const int e = i * L + l;
-        key[i] = e < experts ? order_key(v[i] == -INFINITY ? v[i] : s[i] + (double)bias[i]) : 0;
+        for (int i = 0; i < V; ++i) {
+            key[i] = order_key(v[i]);
+            top = larger(top, key[i]);
+            key[i] = i * L + l < experts ? key[i] : 0;
+        }
+        if (r.scores != BLOCK_SCORES_SIGMOID) {
+            all = softmax_parts<L, V>(v, top, s);
+            if (__any(all.share != all.share)) {  // a NaN, or an infinity: all scores are NaN but of masked experts
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+                    key[i] = all.share != all.share && key[i] > order_key(-INFINITY) ? ~(uint64_t)0 : key[i];
+            }
+        }
     }
     if (r.groups > 1) {
         const int size = experts / r.groups;
@@ -261,9 +301,17 @@ __device__ __forceinline__ void choose(const GateRule &r, int experts, int l, co
                 second_key = larger(larger(second_key, q), f < first_key ? f : first_key);
                 first_key = larger(first_key, f);
             }
-            const double w = of_key(first_key);
+            double w = of_key(first_key);
+            if (r.group_top == 2) {
+                double other = of_key(second_key);
+                if (!BIASED) {
+                    w = w == -INFINITY ? w : score_of(w);
+                    other = other == -INFINITY ? other : score_of(other);
+                }
+                w += other;
+            }
             if (g < r.groups && l % each == 0)
-                room.worth[g] = order_key(r.group_top == 2 ? w + of_key(second_key) : w);
+                room.worth[g] = order_key(w);
         }
         wave_fence();
         uint64_t kept = 0;  // a bit a group
@@ -284,6 +332,11 @@ __device__ __forceinline__ void choose(const GateRule &r, int experts, int l, co
             key[i] = word >> g % 32 & 1 ? key[i] : 0;  // experts past the last one have 0 already
         }
         wave_fence();
+    }
+    if (!BIASED && r.groups == 1) {  // where the chosen ones' logits are found
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            room.table[i * L + l] = key[i];
     }
     // The upper halves of the keys decide where the largest is there once for each token of the wave;
     // otherwise the lower halves of those that share it, then the index. (The comparisons serve twice,
@@ -337,16 +390,23 @@ __device__ __forceinline__ void choose(const GateRule &r, int experts, int l, co
     }
     wave_fence();
     double *score = reinterpret_cast<double *>(room.table);
+    if constexpr (BIASED) {
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-        score[i * L + l] = s[i];
-    wave_fence();
+        for (int i = 0; i < V; ++i)
+            score[i * L + l] = s[i];
+        wave_fence();
+    }
 #pragma unroll
-    for (int q = 0; q < Q; ++q)
-        p[q] = q * L + l < r.top_k ? score[id[q]] : 0.0;
+    for (int q = 0; q < Q; ++q) {
+        p[q] = 0.0;
+        if (q * L < r.top_k) {
+            const double x = BIASED ? score[id[q]] : score_of(of_key(room.table[id[q]]));
+            p[q] = q * L + l < r.top_k ? x : 0.0;
+        }
+    }
 }
 
-template <int SRC, int L, int V>
+template <int SRC, int L, int V, bool BIASED>
 __global__ __launch_bounds__(kWavesHere * 64) void gate_kernel(GateArgs a)
 {
     constexpr int T = 64 / L;
@@ -372,12 +432,7 @@ __global__ __launch_bounds__(kWavesHere * 64) void gate_kernel(GateArgs a)
     float bias[V];
 #pragma unroll
     for (int i = 0; i < V; ++i)
-        bias[i] = 0.0f;
-    if (a.bias) {
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-            bias[i] = a.bias[at[i]];
-    }
+        bias[i] = BIASED ? a.bias[at[i]] : 0.0f;
     double v[V];
     logits_at<SRC, V>(a, row, at, v);
 #pragma unroll
@@ -387,7 +442,7 @@ __global__ __launch_bounds__(kWavesHere * 64) void gate_kernel(GateArgs a)
     int id[Q];  // lane l has slots l, L + l, ...
     double p[Q];
     const Room room = {table, worth};
-    choose<L, V, Q>(r, a.experts, l, v, bias, room, id, p);
+    choose<L, V, Q, BIASED>(r, a.experts, l, v, bias, room, id, p);
     double sum = 0.0;
 #pragma unroll
     for (int q = 0; q < Q; ++q)
@@ -563,20 +618,26 @@ constexpr int kFewTokens = 2048;
 
 unsigned groups_of(int64_t tokens, int lanes) { return (unsigned)ceil_div(tokens, kWavesHere * (64 / lanes)); }
 
-template <int SRC>
+template <int SRC, bool BIASED>
 block_status_t run_gate(const GateArgs &a, hipStream_t st)
 {
     const dim3 threads(kWavesHere * 64);
     const unsigned few = groups_of(a.tokens, 64);
     if (a.experts <= 64)
         return a.tokens <= kFewTokens
-                   ? launch(gate_kernel<SRC, 64, 1>, dim3(few), threads, 0, st, a)
-                   : launch(gate_kernel<SRC, 16, 4>, dim3(groups_of(a.tokens, 16)), threads, 0, st, a);
+                   ? launch(gate_kernel<SRC, 64, 1, BIASED>, dim3(few), threads, 0, st, a)
+                   : launch(gate_kernel<SRC, 16, 4, BIASED>, dim3(groups_of(a.tokens, 16)), threads, 0, st, a);
     if (a.experts <= 256)
         return a.tokens <= kFewTokens
-                   ? launch(gate_kernel<SRC, 64, 4>, dim3(few), threads, 0, st, a)
-                   : launch(gate_kernel<SRC, 32, 8>, dim3(groups_of(a.tokens, 32)), threads, 0, st, a);
-    return launch(gate_kernel<SRC, 64, 16>, dim3(few), threads, 0, st, a);
+                   ? launch(gate_kernel<SRC, 64, 4, BIASED>, dim3(few), threads, 0, st, a)
+                   : launch(gate_kernel<SRC, 32, 8, BIASED>, dim3(groups_of(a.tokens, 32)), threads, 0, st, a);
+    return launch(gate_kernel<SRC, 64, 16, BIASED>, dim3(few), threads, 0, st, a);
+}
+
+template <int SRC>
+block_status_t run_gate(const GateArgs &a, hipStream_t st)
+{
+    return a.bias ? run_gate<SRC, true>(a, st) : run_gate<SRC, false>(a, st);
 }
 
 template <int DT, bool DENSE>
