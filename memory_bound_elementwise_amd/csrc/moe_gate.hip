@@ -476,6 +476,34 @@ __global__ __launch_bounds__(kWavesHere * 64) void gate_kernel(GateArgs a)
     }
 }
 
+// v as fp32, but so that its rounding to DT is v's own. fp32's nearest number to v may be the middle
+// between two of DT, on whose one side v lies. For bf16 that is seen in its bits, once in 2^16 values,
+// and a step to that side will do; for fp16, whose subnormals have other middles, v is cut off to fp32 and
+// its last bit set where anything was lost. (bf16 by cutting off too: 50,000 x 256, softmax of all
+// 30.3 -> 32.1 us; the nearest fp32 of fp16's conversion from fp64 took 40.0, this takes 32.4.)
+template <int DT, int V>
+__device__ __forceinline__ void round_once(const double (&v)[V], float (&f)[V])
+{
+    bool middle = false;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        f[i] = (float)v[i];
+        middle |= DT == DT_BF16 && (uint16_t)__float_as_uint(f[i]) == 0x8000;
+    }
+    if (DT == DT_F32 || (DT == DT_BF16 && !__any(middle)))
+        return;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const uint32_t bits = __float_as_uint(f[i]);
+        const double d = (double)f[i];
+        const bool lost = d != v[i], past = __builtin_fabs(d) > __builtin_fabs(v[i]);
+        if (DT == DT_F16)
+            f[i] = __uint_as_float(lost ? (bits - (past ? 1 : 0)) | 1 : bits);
+        else if (lost && (uint16_t)bits == 0x8000)
+            f[i] = __uint_as_float(past ? bits - 1 : bits + 1);
+    }
+}
+
 struct GateGradArgs {
     const void *logits;
     const int *ids;
@@ -598,11 +626,17 @@ __global__ __launch_bounds__(kWavesHere * 64) void gate_grad_kernel(GateGradArgs
             table[e] += value[j];
     }
     wave_fence();
+    double grad[V];
+    float once[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        grad[i] = table[i * L + l] - (DENSE ? s[i] * dot : 0.0);
+    round_once<DT, V>(grad, once);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int e = i * L + l;
         if (mine && e < a.experts)
-            store1<DT>(a.grad_logits, row + e, (float)(table[e] - (DENSE ? s[i] * dot : 0.0)));
+            store1<DT>(a.grad_logits, row + e, once[i]);
     }
 }
 
