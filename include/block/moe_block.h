@@ -179,7 +179,8 @@ block_status_t block_moe_layer(const uint16_t *x, const void *router_weight, blo
  * on). In a sum with a bias or of two such scores count as the equal numbers that they are. An expert whose logit is -inf is masked: its score is 0
  * and its rank -inf whatever its bias, so that it is chosen (with weight 0) only where too few
  * others are left; where the chosen scores are all 0, so are the weights. (Renormalised softmax
- * weights are the softmax of the chosen logits, also far below the row's largest.)
+ * weights are the softmax of the chosen logits, also far below the row's largest; so are those of
+ * sigmoid scores down to the least one that is not 0, which near it are e^l.)
  *   logits: [tokens, experts] of logits_dtype, any of block_dtype_t; bias: fp32 [experts] or NULL;
  *   ids: int32 [tokens, top_k]; probs: fp32 [tokens, top_k].
  *   valid_tokens: device int32 scalar or NULL (= tokens), clamped to 0 .. tokens; rows of ids and

@@ -406,6 +406,13 @@ __device__ __forceinline__ void choose(const GateRule &r, int experts, int l, co
     }
 }
 
+// Whether a sum of chosen scores is so small that some of them have lost digits or are gone, and their
+// shares are better had from their logits. (Sigmoid scores that are all 0 have shares of 0.)
+__device__ __forceinline__ bool near_the_end(int scores, double sum)
+{
+    return sum < 0x1p-840 && (scores == BLOCK_SCORES_SOFTMAX || sum > 0.0);
+}
+
 template <int SRC, int L, int V, bool BIASED>
 __global__ __launch_bounds__(kWavesHere * 64) void gate_kernel(GateArgs a)
 {
@@ -452,9 +459,10 @@ __global__ __launch_bounds__(kWavesHere * 64) void gate_kernel(GateArgs a)
 #pragma unroll
         for (int q = 0; q < Q; ++q)
             p[q] = sum == 0.0 ? 0.0 : p[q] / sum;
-        // Chosen for their bias, hundreds below the largest logit: from the chosen logits alone, as in
-        // the gradient, where the scores run out of exponents (fp32 weights reach down to 2^-149).
-        if (r.scores == BLOCK_SCORES_SOFTMAX && __any(sum < 0x1p-840)) {
+        // Chosen for their bias, hundreds below the largest logit, or sigmoid scores that are e^logit: from
+        // the chosen logits alone, as in the gradient, where the scores run out of exponents (fp32
+        // weights reach down to 2^-149).
+        if (__any(near_the_end(r.scores, sum))) {
             double x[Q], own[Q];
             logits_at<SRC, Q>(a, row, id, x);
 #pragma unroll
@@ -463,7 +471,7 @@ __global__ __launch_bounds__(kWavesHere * 64) void gate_kernel(GateArgs a)
             softmax<L, Q>(x, own);
 #pragma unroll
             for (int q = 0; q < Q; ++q)
-                p[q] = sum < 0x1p-840 ? own[q] : p[q];
+                p[q] = near_the_end(r.scores, sum) ? own[q] : p[q];
         }
     }
 #pragma unroll
@@ -599,10 +607,18 @@ __global__ __launch_bounds__(kWavesHere * 64) void gate_grad_kernel(GateGradArgs
                 sum += p[q];
             sum = lanes_sum<L>(sum);
 #pragma unroll
-            for (int q = 0; q < Q; ++q) {
+            for (int q = 0; q < Q; ++q)
                 p[q] = sum == 0.0 ? 0.0 : p[q] / sum;
-                dot += id[q] < 0 ? 0.0 : g[q] * p[q];
+            if (a.scores == BLOCK_SCORES_SIGMOID && __any(near_the_end(a.scores, sum))) {
+                double own[Q];
+                softmax<L, Q>(x, own);
+#pragma unroll
+                for (int q = 0; q < Q; ++q)
+                    p[q] = near_the_end(a.scores, sum) ? own[q] : p[q];
             }
+#pragma unroll
+            for (int q = 0; q < Q; ++q)
+                dot += id[q] < 0 ? 0.0 : g[q] * p[q];
             dot = lanes_sum<L>(dot);
         }
 #pragma unroll

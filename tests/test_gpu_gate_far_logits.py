@@ -1,11 +1,12 @@
 """The gate where fp64 scores cannot tell logits apart: softmax scores that run out of exponents,
-sigmoid scores of 1. Expected values are formed from the logits themselves, on the CPU in 64 bits."""
+sigmoid scores of 1, sums of scores near the end of fp64. Expected values are formed from the logits
+themselves, on the CPU in 64 bits."""
 import pytest
 import torch
 
 import block_reference as ref
 import gated_reference as gated
-from memory_bound_elementwise_amd import moe_gate_fwd, moe_route
+from memory_bound_elementwise_amd import MoeGate, moe_gate_bwd, moe_gate_fwd, moe_route
 from parity import say
 
 pytestmark = pytest.mark.gpu
@@ -102,3 +103,35 @@ def test_not_a_number_comes_first():
     logits[0, 2] = float("nan")
     ids, _ = _gate(logits, 2, scores="sigmoid")
     assert ids.tolist() == [[2, 4], [4, 0]]
+
+
+# sums of sigmoid scores between fp64's smallest number and 2^-840
+@pytest.mark.parametrize("tokens,experts", [(6, 30), (6, 200), (2060, 30), (2060, 200), (6, 600)])
+def test_sigmoid_near_the_end_of_fp64(tokens, experts):
+    """There s = e^l within fp64, and the renormalised weights are the softmax of the chosen logits; the
+    gradient is that of these weights."""
+    g = torch.Generator().manual_seed(tokens + experts)
+    logits = torch.randn(tokens, experts, generator=g) * 2
+    logits[::2] -= torch.linspace(590, 738, len(logits[::2]))[:, None]
+    how = dict(scores="sigmoid", renormalize=True, scale=1.5)
+    far = torch.arange(0, tokens, 2)
+    up = torch.randn(tokens, 5, generator=g)
+    for bias in (None, torch.randn(experts, generator=g)):
+        ids, probs = _gate(logits, 5, bias=None if bias is None else bias.to(DEV), **how)
+        mine = logits.double().gather(1, ids.long())
+        s = torch.sigmoid(mine)
+        p = s / s.sum(1, keepdim=True)
+        p[far] = torch.softmax(mine[far], 1)
+        v = p * 1.5
+        ref.check(probs, v, ref.rounded(v, v.abs() * gated.WIDE, torch.float32), "probs")
+        got = moe_gate_bwd(logits.to(DEV), ids.to(DEV), up.to(DEV), torch.empty_like(logits, device=DEV), **how)
+        u = 1.5 * up.double()
+        mass = p * (u.abs() + (u * p).abs().sum(1, keepdim=True)) * torch.sigmoid(-mine)
+        want = torch.zeros(tokens, experts, dtype=torch.float64)
+        want.scatter_(1, ids.long(), p * (u - (u * p).sum(1, keepdim=True)) * torch.sigmoid(-mine))
+        loss = torch.zeros_like(want).scatter_(1, ids.long(), mass * gated.WIDE)
+        ref.check(got, want, ref.rounded(want, loss, torch.float32), "grad_logits")
+        leaf = logits.to(DEV).requires_grad_()
+        again, _ = MoeGate.apply(leaf, 5, None if bias is None else bias.to(DEV), "sigmoid", 1, None, 1, True, 1.5)
+        again.backward(up.to(DEV))
+        assert torch.equal(again.detach().cpu(), probs) and torch.equal(leaf.grad, got)
