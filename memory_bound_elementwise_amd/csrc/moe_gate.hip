@@ -19,6 +19,7 @@
 #include <cmath>
 
 #include "gate.h"
+#include "gate_math.h"
 #include "route_device.h"
 
 namespace {
@@ -108,23 +109,6 @@ __device__ __forceinline__ double lanes_sum(double v)
 // The wave's accesses to its shared memory stay in order; this keeps the compiler from moving
 // them across.
 __device__ __forceinline__ void wave_fence() { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront"); }
-
-// e^v for v <= 0, within about a step of fp64: v = n ln 2 + r with |r| <= ln 2 / 2, and the series of
-// e^r to its 13th power (what follows is below 2^-57). Half of the library function's
-// instructions, which has to deal with larger v.
-__device__ __forceinline__ double exp_below(double v)
-{
-    v = v < -800.0 ? -800.0 : v;  // 0 from there on; keeps NaN
-    const double n = __builtin_rint(v * 1.4426950408889634);
-    const double r = __builtin_fma(n, -1.9082149292705877e-10, __builtin_fma(n, -0.6931471803691238, v));
-    constexpr double c[] = {1.0 / 6227020800, 1.0 / 479001600, 1.0 / 39916800, 1.0 / 3628800, 1.0 / 362880, 1.0 / 40320,
-                            1.0 / 5040, 1.0 / 720, 1.0 / 120, 1.0 / 24, 1.0 / 6, 0.5, 1.0, 1.0};
-    double e = c[0];
-#pragma unroll
-    for (int i = 1; i < 14; ++i)
-        e = __builtin_fma(e, r, c[i]);
-    return __builtin_amdgcn_ldexp(e, (int)n);
-}
 
 // 1 / d to a step or so, for d that neither overflows nor underflows.
 __device__ __forceinline__ double reciprocal(double d)
