@@ -14,9 +14,13 @@ namespace block {
 // (tensors of these products stay below 2^31 bytes a resource).
 constexpr uint32_t kNowhere = 0x80000000u;
 
-// One matrix's row blocks for a wave: W's tiles and their scales.
+// One block of rows of a matrix for a wave: W's tiles, their scales and how many there are. A load's
+// scalar offset is a tile's place, the lane's offset one in it. The range check is on the lane's offset
+// against the resource's bytes less the scalar offset, so a tile past the last is read at the
+// resource's very end: nothing is left there for any lane, and the load returns zeros.
 struct Tiles {
     rsrc_t codes, scales;
+    int own;
 };
 
 // there: whether the matrix has such a block (its tiles read zeros otherwise).
@@ -24,15 +28,15 @@ __device__ __forceinline__ Tiles tiles_of(const uint8_t *codes, const uint8_t *s
                                           bool there = true)
 {
     return {make_rsrc(codes + block * k_tiles * kFp4Codes, there ? (uint32_t)k_tiles * kFp4Codes : 0u),
-            make_rsrc(scales + block * k_tiles * kFp4Scales, there ? (uint32_t)k_tiles * kFp4Scales : 0u)};
+            make_rsrc(scales + block * k_tiles * kFp4Scales, there ? (uint32_t)k_tiles * kFp4Scales : 0u), there ? k_tiles : 0};
 }
 
-// Neighbouring row blocks of one matrix over a range of its k tiles: the first one's tiles, the distance
-// of the blocks in tiles and how many of each there are. (A resource a block would take four times the
-// scalar registers.)
+// Neighbouring row blocks of one matrix over a range of its k tiles: all of their tiles from the first
+// one's first to the last one's last, the distance of the blocks in tiles, the range's length and the
+// number of blocks. (A resource a block would take four times the scalar registers.)
 struct TileRun {
-    Tiles first;
-    int k_tiles, own;
+    Tiles all;
+    int k_tiles, own, blocks;
 };
 
 // there: the blocks that are there, of those that are asked for; own: k tiles from `from` on.
@@ -40,9 +44,10 @@ __device__ __forceinline__ TileRun run_of(const uint8_t *codes, const uint8_t *s
                                           int from, int own)
 {
     const int64_t tile = block * k_tiles + from;
-    const uint32_t tiles = there ? (uint32_t)((there - 1) * k_tiles + own) : 0u;
-    return {{make_rsrc(codes + tile * kFp4Codes, tiles * kFp4Codes), make_rsrc(scales + tile * kFp4Scales, tiles * kFp4Scales)},
-            k_tiles, own};
+    const int tiles = there ? (there - 1) * k_tiles + own : 0;
+    return {{make_rsrc(codes + tile * kFp4Codes, (uint32_t)tiles * kFp4Codes),
+             make_rsrc(scales + tile * kFp4Scales, (uint32_t)tiles * kFp4Scales), tiles},
+            k_tiles, own, there};
 }
 
 // A wave's next tiles of RT row blocks, in flight. A tile past the last reads zeros.
@@ -50,27 +55,26 @@ template <int RT>
 struct Ahead {
     u32x4 codes[RT];
     uint32_t scales[RT];
+    template <int kAux>
+    __device__ __forceinline__ void load(int i, const Tiles &w, int tile)
+    {
+        const int lane = lane_id();
+        codes[i] = __builtin_amdgcn_raw_buffer_load_b128(w.codes, lane * 16, tile * kFp4Codes, kAux);
+        scales[i] = __builtin_amdgcn_raw_buffer_load_b32(w.scales, lane % 16 * 4, tile * kFp4Scales, 0);
+    }
     // kCached: of weights that other workgroups read too; past the caches otherwise.
     template <bool kCached = false>
     __device__ __forceinline__ void load(const Tiles (&w)[RT], int t)
     {
-        const int lane = lane_id();
 #pragma unroll
-        for (int i = 0; i < RT; ++i) {
-            codes[i] = __builtin_amdgcn_raw_buffer_load_b128(w[i].codes, lane * 16, t * kFp4Codes, kCached ? 0 : kLoadAux);
-            scales[i] = __builtin_amdgcn_raw_buffer_load_b32(w[i].scales, lane % 16 * 4, t * kFp4Scales, 0);
-        }
+        for (int i = 0; i < RT; ++i)
+            load<kCached ? 0 : kLoadAux>(i, w[i], t < w[i].own ? t : w[i].own);
     }
     __device__ __forceinline__ void load(const TileRun &w, int t)
     {
-        const int lane = lane_id();
-        const uint32_t at = t < w.own ? lane * 16 : kNowhere, scale_at = t < w.own ? lane % 16 * 4 : kNowhere;
 #pragma unroll
-        for (int i = 0; i < RT; ++i) {
-            const int tile = i * w.k_tiles + t;
-            codes[i] = __builtin_amdgcn_raw_buffer_load_b128(w.first.codes, at, tile * kFp4Codes, kLoadAux);
-            scales[i] = __builtin_amdgcn_raw_buffer_load_b32(w.first.scales, scale_at, tile * kFp4Scales, 0);
-        }
+        for (int i = 0; i < RT; ++i)
+            load<kLoadAux>(i, w.all, t < w.own && i < w.blocks ? i * w.k_tiles + t : w.all.own);
     }
 };
 
