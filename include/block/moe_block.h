@@ -237,6 +237,10 @@ block_status_t block_moe_route_gated(const uint16_t *x, const void *router_weigh
  *   max |w| < 7 2^power (at least 2^-127, at most 2^125), and each element the nearest one to w /
  *   2^power, ties to the even code, past 6 to 6: |w - value| <= 2^power / 4 up to 2 2^power, / 2 up to
  *   4 2^power, 2^power up to 7 2^power. A group of zeros has b = 127; one with an infinity or a NaN b = 255.
+ *   (The format's specification describes another choice, the largest power up to max |w| / 4, with
+ *   elements past 6 cut off at 6. It differs for groups whose largest is from 7 to 8 of those powers: they
+ *   get twice the power here, and the largest is off by one of those at most, not by up to two. pack
+ *   takes either.)
  * pack: from the row-major form of checkpoints: elements [matrices, n, k / 2], two a byte, the
  *   first in its lower half; exponents [matrices, n, k / 32].
  * dequantize: the bf16 values, [matrices, n, k].

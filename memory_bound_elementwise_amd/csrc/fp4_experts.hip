@@ -3,8 +3,8 @@
 //
 // y = residual + sum over a token's slots of down (act(up x) p), sums fp32. For a few tokens the cost is
 // reading each chosen expert's weights once: 187 MB for one token of 8 of 64 experts, hidden 7168, inter
-// 2048 (up 21.3 us, 5.9 TB/s; down 15.9, 3.9 TB/s), 1.5 GB for 64 tokens (160, 6.2 TB/s; 107, 4.7;
-// combine 5.4).
+// 2048 (up 21.4 us, 5.8 TB/s; down 15.8, 3.9 TB/s), 1.5 GB for 64 tokens (162, 6.2 TB/s; 115, 4.3;
+// combine 5.3).
 //   up       one workgroup a (chosen expert, block of columns of the activation); the activation
 //            times the probability goes to the workspace as three bf16 terms, which keep its 24 bits
 //   down     the terms are columns of their own. For a few pairs one workgroup 16 columns of
@@ -231,7 +231,7 @@ __global__ __launch_bounds__(kWaves * 64) void fp4_up_kernel(ExpertArgs a)
 // Up products where experts have many tokens: a workgroup takes one expert and kManyWaves times two
 // row tiles, which walk k together (Walk), so that x is read once for all of them. A wave has gate
 // and up of 16 columns of the activation, or 32 columns of one product. Bound by the stream of weights:
-// 64 tokens, 7168 x 2048, 64 experts 160 us. (Four steps in flight 164; weights kept in the caches
+// 64 tokens, 7168 x 2048, 64 experts 162 us. (Four steps in flight 164; weights kept in the caches
 // 180; without the scales' loads 150.)
 constexpr int kManyWaves = 8;
 
@@ -349,7 +349,7 @@ __device__ __forceinline__ rsrc_t terms_of(const ExpertArgs &a)
 // Down product of up to 64 pairs: a workgroup takes 16 columns of the output, its waves the chosen
 // experts in turn, each in `parts` parts of k so that all have work; the pairs' sums meet in
 // shared memory and are added in slot order. NX 1: a pair at a time, 4: five. One token's eight
-// experts are one round of 3.5 waves a SIMD, whose start and end are half of its 15.9 us. (Six or
+// experts are one round of 3.5 waves a SIMD, whose start and end are half of its 15.8 us. (Six or
 // eight steps in flight 17.3, sixteen waves a workgroup 18.2.)
 constexpr int kFewWaves = 8, kFewPairs = 64;
 
@@ -425,8 +425,8 @@ __global__ __launch_bounds__(kFewWaves * 64) void fp4_down_few_kernel(ExpertArgs
 // waves of two row tiles (256 columns of the output) and one of `parts` parts of k. A workgroup takes every gridDim.x-th unit,
 // and its walk over one ends by sending for the next one's first steps: k is short here (2048: 16
 // steps). Its pairs' terms come from cache, 12 KB a pair and unit beside the unit's 278 KB of weights.
-// 64 tokens, 7168 x 2048, 64 experts: 107 us; a workgroup a unit 126; the weights' stream and the
-// stores of z alone 93. (Four waves of four tiles 115, four of two 158, sixteen of one 141, four steps
+// 64 tokens, 7168 x 2048, 64 experts: 115 us in a trace, 105 at best; when that was 107, a workgroup a
+// unit took 126, and the weights' stream and the stores of z alone 93. (Four waves of four tiles 115, four of two 158, sixteen of one 141, four steps
 // in flight 118.)
 constexpr int kDownWaves = 8, kDownTiles = 2;
 
@@ -623,7 +623,7 @@ int pair_groups(const ExpertSizes &s, int group)
 // whose waves split k: the former for more tokens than a few, where that leaves two workgroups a CU, or
 // one for every other CU where experts may have so many tokens that the latter read their weights
 // again. (us, shared and split k: 7168 x 2048, 8 of 64 experts, 2 tokens 43.9 and 39.7, 4 tokens 67.8
-// and 66.5, 8 tokens, 736 workgroups, 123.6 and 127.0, 64 tokens 160 and 211; 8 tokens, 2048 x 8192, 4 of
+// and 66.5, 8 tokens, 1024 workgroups, of which 736 found an expert, 123.6 and 127.0, 64 tokens 160 and 211; 8 tokens, 2048 x 8192, 4 of
 // 8, 512 workgroups 27.7 and 33.8; 4096 x 4096, 2 of 8, 256 workgroups, 12 tokens 34.8 and 28.5, 64
 // tokens 37.4 and 48.6; 128 tokens, 2048 x 1408, 8 of 16, 176 workgroups 55.4 and 69.9; 100 tokens, 4096 x
 // 512, 2 of 8, 32 workgroups 36.1 and 17.6.)

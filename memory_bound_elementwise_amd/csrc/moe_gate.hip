@@ -6,8 +6,8 @@
 // values; what has to be seen by other lanes goes through the wave's own shared memory, and no
 // kernel here has a barrier.
 //
-// Few tokens take 2.7 to 6 us: a launch, a chain of exchanges for groups (1.3) and one for each slot
-// (0.15). Many are bound by vector instructions, not by memory: with 256 experts in 8 groups of which 4
+// Few tokens of up to 256 experts take 2.8 to 5.7 us: a launch, a chain of exchanges for groups (1.3) and
+// one for each slot (0.15); of 512 experts up to 10.4. Many are bound by vector instructions, not by memory: with 256 experts in 8 groups of which 4
 // are kept, top 8, a wave of two tokens issues 1400 of them, and 6720 tokens (13.8 us for 6.9 MB) leave
 // some of the 1024 SIMDs four waves and others three. (Sixteen lanes a token 13.9 us, a wave each
 // 14.6; the same choice in fp32 where its gaps certify it 1196 instructions and 13.8; the winner's
@@ -645,9 +645,9 @@ __global__ __launch_bounds__(kWavesHere * 64) void gate_grad_kernel(GateGradArgs
 // ---------------------------------------------------------------------------
 // Up to so many tokens take a wave each, more share one by two or, with up to 64 experts, by four: a
 // wave of its own has the shorter way to the answer, shared ones spend fewer instructions a
-// token. (us, own and shared: 1024 tokens of 64 experts 3.7 and 4.5, of 256 4.7 and 5.8; 2048 tokens
-// 4.0 and 4.5, 5.5 and 6.0; 4096 tokens 5.1 and 4.6, 7.7 and 7.3. The gradient's: 3.6 and 4.2, 4.3
-// and 5.1; 3.9 and 4.2, 5.0 and 5.4; 4.8 and 4.4, 6.4 and 6.4.)
+// token. (us, own and shared, softmax, top 8: 1024 tokens of 64 experts 3.8 and 4.7, of 256 4.9 and 6.1;
+// 2048 tokens 4.1 and 4.8, 5.5 and 6.2; 4096 tokens 5.6 and 4.8, 7.5 and 6.9. The gradient's, of every logit:
+// 3.2 and 3.7, 3.9 and 4.5; 3.5 and 3.7, 4.5 and 4.7; 4.2 and 3.8, 5.8 and 5.6.)
 constexpr int kFewTokens = 2048;
 
 unsigned groups_of(int64_t tokens, int lanes) { return (unsigned)ceil_div(tokens, kWavesHere * (64 / lanes)); }

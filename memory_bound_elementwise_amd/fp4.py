@@ -46,7 +46,9 @@ def fp4_quantize(weight, codes, scales, *, stream=None):
     """``weight`` ([n, k] or [matrices, n, k]; bf16, fp16 or fp32) to 4 bits: each 32 neighbours of
     a row share the smallest power of two for which 6, the largest element, is the nearest one to
     all of them; each becomes the nearest of 0, 0.5, 1, 1.5, 2, 3, 4, 6 times it, ties to the even
-    code. A group that holds an infinity or a NaN becomes NaN."""
+    code. A group that holds an infinity or a NaN becomes NaN. (A tool that takes the largest power up to
+    a quarter of the largest magnitude instead gives other codes where that magnitude is from 7 to 8
+    of those powers; ``fp4_pack`` takes both.)"""
     lead, matrices, n, k = _matrices(weight, "weight")
     dev, kind = weight.get_device(), _kind(weight, "weight", _ANY)
     to = _pair(codes, scales, "", lead, n, k, dev)

@@ -340,7 +340,8 @@ def _scores(scores):
 
 def _gate_rule(scores, groups, top_groups, group_top, renormalize, scale):
     """The gate's arguments as the C functions take them in a row."""
-    return (SCORES[scores] if scores in SCORES else _scores(scores), groups, groups if top_groups is None else top_groups, group_top, bool(renormalize), scale)
+    return (SCORES[scores] if scores in SCORES else _scores(scores), groups,
+            groups if top_groups is None else top_groups, group_top, bool(renormalize), scale)
 
 
 def moe_route(x, router_weight, ids, probs, *, renormalize=False, scores="softmax", bias=None, groups=1,

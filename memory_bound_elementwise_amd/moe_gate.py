@@ -3,7 +3,8 @@ softmax or sigmoid scores, a bias for balance, groups of experts, top-k and reno
 from given logits, and the gradient of the logits. ``moe_block.moe_route`` runs the same gate
 behind the router's product.
 
-Argument marshalling as in ``moe_block``; no CPU or PyTorch fallback.
+Argument marshalling as in ``moe_block``; no CPU or PyTorch fallback. Logits and gradients start at 16
+bytes, as all tensors of the C functions do; ``MoeGate`` copies a slice that does not.
 """
 from __future__ import annotations
 
