@@ -426,8 +426,8 @@ __global__ __launch_bounds__(kFewWaves * 64) void fp4_down_few_kernel(ExpertArgs
 // and its walk over one ends by sending for the next one's first steps: k is short here (2048: 16
 // steps). Its pairs' terms come from cache, 12 KB a pair and unit beside the unit's 278 KB of weights.
 // 64 tokens, 7168 x 2048, 64 experts: 115 us in a trace, 105 at best; when that was 107, a workgroup a
-// unit took 126, and the weights' stream and the stores of z alone 93. (Four waves of four tiles 115, four of two 158, sixteen of one 141, four steps
-// in flight 118.)
+// unit took 126, and the weights' stream and the stores of z alone 93. (Four waves of four tiles 115,
+// four of two 158, sixteen of one 141, four steps in flight 118.)
 constexpr int kDownWaves = 8, kDownTiles = 2;
 
 template <int G>
@@ -623,10 +623,10 @@ int pair_groups(const ExpertSizes &s, int group)
 // whose waves split k: the former for more tokens than a few, where that leaves two workgroups a CU, or
 // one for every other CU where experts may have so many tokens that the latter read their weights
 // again. (us, shared and split k: 7168 x 2048, 8 of 64 experts, 2 tokens 43.9 and 39.7, 4 tokens 67.8
-// and 66.5, 8 tokens, 1024 workgroups, of which 736 found an expert, 123.6 and 127.0, 64 tokens 160 and 211; 8 tokens, 2048 x 8192, 4 of
-// 8, 512 workgroups 27.7 and 33.8; 4096 x 4096, 2 of 8, 256 workgroups, 12 tokens 34.8 and 28.5, 64
-// tokens 37.4 and 48.6; 128 tokens, 2048 x 1408, 8 of 16, 176 workgroups 55.4 and 69.9; 100 tokens, 4096 x
-// 512, 2 of 8, 32 workgroups 36.1 and 17.6.)
+// and 66.5, 8 tokens, 1024 workgroups, of which 736 found an expert, 123.6 and 127.0, 64 tokens 160 and
+// 211; 8 tokens, 2048 x 8192, 4 of 8, 512 workgroups 27.7 and 33.8; 4096 x 4096, 2 of 8, 256
+// workgroups, 12 tokens 34.8 and 28.5, 64 tokens 37.4 and 48.6; 128 tokens, 2048 x 1408, 8 of 16, 176
+// workgroups 55.4 and 69.9; 100 tokens, 4096 x 512, 2 of 8, 32 workgroups 36.1 and 17.6.)
 bool up_shares(const ExpertArgs &a, int columns, unsigned experts)
 {
     const bool many = a.tokens * a.top_k > kFewPairs;

@@ -68,9 +68,9 @@ __global__ __launch_bounds__(kWaves * 64) void fp4_linear_few_kernel(Args a)
 // read). W needs no shared memory: each wave has 16 FN rows of it for itself, loads their tiles a
 // step ahead and widens a word of each when its turn comes. What is read from shared memory is so
 // 1 / FN of an operand a matrix instruction. (Three buffers and loads two steps ahead leave room
-// for fewer workgroups: 1009 x 1408 x 7168 26.6 -> 29.5 us, 6720 x 4096 x 7168 323 -> 371. Tiles of
-// 128 x 256, a wave a SIMD: 33.8 and 340. Two waves a workgroup: 27.4 and 470.) Weights come from cache
-// for all tiles but the first. 6720 x 4096 x 7168 takes 298 to 327 us in different sessions, 1.32 to 1.21
+// for fewer workgroups: 1009 x 1408 x 7168 26.6 -> 29.5 us, 6720 x 4096 x 7168 323 -> 371. Tiles of 128
+// x 256, a wave a SIMD: 33.8 and 340. Two waves a workgroup: 27.4 and 470.) Weights come from cache for
+// all tiles but the first. 6720 x 4096 x 7168 takes 298 to 327 us in different sessions, 1.32 to 1.21
 // PFLOP/s; the 896 tiles of 1009 x 1408 x 7168 24.8, 0.82, of 11 steps each and no whole number a CU.
 //   parts > 1: the sums over one of `parts` ranges of k, to partial [parts][m][n] in fp32.
 constexpr int kTileWaves = 4;

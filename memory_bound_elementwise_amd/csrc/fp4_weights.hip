@@ -44,11 +44,12 @@ __device__ __forceinline__ bool place(const Args &a, Place &p)
     return true;
 }
 
-// The byte of a group's power of two from the bits of its largest magnitude: the smallest power
-// with magnitude < 7 2^power, so that 6, the largest element, is the nearest one to all of the
-// group. (The format's own recipe takes the largest power up to the magnitude over 4, and cuts what is then
-// past 6 off at 6; groups whose largest is from 7 to 8 of those powers get twice the power here.) A group of zeros gets 127; one with an infinity or a NaN 255, which makes it all NaN.
-// 252 at most, so that no value passes bf16's range (the largest weights become 6 2^125 then).
+// The byte of a group's power of two from the bits of its largest magnitude: the smallest power with
+// magnitude < 7 2^power, so that 6, the largest element, is the nearest one to all of the group. (The
+// format's own recipe takes the largest power up to the magnitude over 4, and cuts what is then past 6
+// off at 6; groups whose largest is from 7 to 8 of those powers get twice the power here.) A group of
+// zeros gets 127; one with an infinity or a NaN 255, which makes it all NaN. 252 at most, so that no
+// value passes bf16's range (the largest weights become 6 2^125 then).
 __device__ __forceinline__ uint32_t scale_byte(uint32_t top)
 {
     const int power = (int)((top + 0x200000u) >> 23) - 2;  // carries where the mantissa reaches 1.75

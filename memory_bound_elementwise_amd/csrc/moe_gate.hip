@@ -6,12 +6,12 @@
 // values; what has to be seen by other lanes goes through the wave's own shared memory, and no
 // kernel here has a barrier.
 //
-// Few tokens of up to 256 experts take 2.8 to 5.7 us: a launch, a chain of exchanges for groups (1.3) and
-// one for each slot (0.15); of 512 experts up to 10.4. Many are bound by vector instructions, not by memory: with 256 experts in 8 groups of which 4
-// are kept, top 8, a wave of two tokens issues 1400 of them, and 6720 tokens (13.8 us for 6.9 MB) leave
-// some of the 1024 SIMDs four waves and others three. (Sixteen lanes a token 13.9 us, a wave each
-// 14.6; the same choice in fp32 where its gaps certify it 1196 instructions and 13.8; the winner's
-// index found in the scalar unit 14.0.)
+// Few tokens of up to 256 experts take 2.8 to 5.7 us: a launch, a chain of exchanges for groups (1.3)
+// and one for each slot (0.15); of 512 experts up to 10.4. Many are bound by vector instructions, not
+// by memory: with 256 experts in 8 groups of which 4 are kept, top 8, a wave of two tokens issues 1400
+// of them, and 6720 tokens (13.8 us for 6.9 MB) leave some of the 1024 SIMDs four waves and others
+// three. (Sixteen lanes a token 13.9 us, a wave each 14.6; the same choice in fp32 where its gaps
+// certify it 1196 instructions and 13.8; the winner's index found in the scalar unit 14.0.)
 #include <hip/hip_runtime.h>
 
 #include <stdint.h>
