@@ -31,11 +31,11 @@ def moe_gate_fwd(logits, ids, probs, *, scores="softmax", bias=None, groups=1, t
     ``ids`` (int32 [tokens, top_k]) and their weights into ``probs`` (fp32).
 
     ``scores``: "softmax" or "sigmoid" of the logits. Experts are ranked by score plus ``bias``
-    (fp32 [experts]; None: by their logits, the same order as the scores'); with ``groups`` > 1 only those of the ``top_groups`` groups (None:
-    all) whose ``group_top`` (1 or 2) largest ranks sum to most. The weights are the scores
-    without the bias, divided by their sum over the chosen ones (``renormalize``), times ``scale``.
-    A logit of -inf masks its expert: weight 0, chosen only where too few others are left. Ties go
-    to the lower expert. Rows at or past ``valid_tokens`` (device int32) are left as they were.
+    (fp32 [experts]; None: by their logits, the same order as the scores'); with ``groups`` > 1 only
+    those of the ``top_groups`` groups (None: all) whose ``group_top`` (1 or 2) largest ranks sum to
+    most. The weights are the scores without the bias, divided by their sum over the chosen ones
+    (``renormalize``), times ``scale``. A logit of -inf masks its expert: weight 0, chosen only where
+    too few others are left. Ties go to the lower expert. Rows at or past ``valid_tokens`` (device int32) are left as they were.
     Nothing is recorded for autograd: the gradient comes from ``moe_gate_bwd``, or from
     ``MoeGate``, which calls both."""
     pl, code, tokens, experts, top_k, dev = _logits(logits, ids)
